@@ -25,7 +25,8 @@ __all__ = [
     "zigzag_positions", "ring_attn_fwd_varlen", "varlen_padded_length", "check_status",
     "probe_wait_timeout", "ring_attn_fwd_host", "host_workspace_bytes", "ring_attn_bwd_gqa",
     "ring_attn_bwd_zigzag", "ring_attn_bwd_varlen", "ring_attn_fwd_ex", "ring_attn_bwd_ex",
-    "ulysses_attention_fused", "varlen_schedule", "EXPORTED_SYMBOLS",
+    "ulysses_attention_fused", "varlen_schedule", "EXPORTED_SYMBOLS", "RopeTable", "rope_table",
+    "rope_fwd", "rope_bwd", "paged_kv_append", "paged_attn_fwd", "paged_attn_workspace",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -49,6 +50,8 @@ EXPORTED_SYMBOLS = (
     "ring_attn_bwd_gqa", "ring_attn_bwd_zigzag", "ring_attn_bwd_varlen", "ring_attn_fwd_ex",
     "ring_attn_bwd_ex", "ulysses_attention_fused", "ring_attn_varlen_schedule",
     "ring_attn_varlen_schedule_bytes", "ra_padded_length", "ra_probe_bounds_check",
+    "ra_rope_phases", "ra_rope_phases_of", "rope_fwd", "rope_bwd", "paged_kv_append",
+    "paged_attn_fwd", "paged_attn_workspace_bytes",
 )
 
 
@@ -62,6 +65,45 @@ class AttnDesc(ctypes.Structure):
                 ("causal", ctypes.c_int), ("layout", ctypes.c_int),
                 ("cu_seqlens", ctypes.c_void_p), ("n_seqs", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("schedule", ctypes.c_void_p)]
+
+
+ROPE_STYLES = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class RopeConfig(ctypes.Structure):
+    """Mirror of ra_rope_config (include/ring_attn.h)."""
+    _fields_ = [("rot_dim", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_length", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
+
+
+class Rope(ctypes.Structure):
+    """Mirror of ra_rope (include/ring_attn.h)."""
+    _fields_ = [("phases", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("style", ctypes.c_int),
+                ("amplitude", ctypes.c_float)]
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of ra_rope_desc (include/ring_attn.h)."""
+    _fields_ = [("B", ctypes.c_int), ("L", ctypes.c_int), ("H", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("D", ctypes.c_int), ("P", ctypes.c_int),
+                ("layout", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int), ("positions", ctypes.c_void_p),
+                ("position_offset", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("q_out_stride", ctypes.c_longlong), ("k_out_stride", ctypes.c_longlong)]
+
+
+class PagedDesc(ctypes.Structure):
+    """Mirror of ra_paged_desc (include/ring_attn.h)."""
+    _fields_ = [("T", ctypes.c_int), ("n_seqs", ctypes.c_int), ("H", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("D", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("table_stride", ctypes.c_longlong),
+                ("page_table", ctypes.c_void_p), ("cu_new", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("dtype", ctypes.c_int), ("causal", ctypes.c_int)]
 
 
 class RingAttnError(RuntimeError):
@@ -134,6 +176,12 @@ def _open(path, build_if_missing, debug_bounds):
         "ring_attn_fwd_host": [vp, vp, vp, vp, f_p, vp, ctypes.c_ulonglong, i, i, i, i, i, i,
                                i, vp],
         "ring_attn_varlen_schedule": [vp, i, i, i, i, vp, ctypes.c_ulonglong, vp],
+        "ra_rope_phases": [vp, vp, vp],
+        "ra_rope_phases_of": [vp, i, vp],
+        "rope_fwd": [vp, vp, vp, vp, vp, vp, vp],
+        "rope_bwd": [vp, vp, vp, vp, vp, vp, vp],
+        "paged_kv_append": [vp, vp, vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, vp],
+        "paged_attn_fwd": [vp, vp, ll, vp, vp, vp, vp, vp, ctypes.c_ulonglong, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -145,6 +193,8 @@ def _open(path, build_if_missing, debug_bounds):
     lib.ring_attn_bwd_workspace_bytes.restype = ctypes.c_ulonglong
     lib.ring_attn_varlen_schedule_bytes.argtypes = [i, i]
     lib.ring_attn_varlen_schedule_bytes.restype = ctypes.c_ulonglong
+    lib.paged_attn_workspace_bytes.argtypes = [i, i]
+    lib.paged_attn_workspace_bytes.restype = ctypes.c_ulonglong
     lib.ra_status_string.argtypes = [ctypes.c_int]
     lib.ra_status_string.restype = ctypes.c_char_p
     lib.ra_padded_length.argtypes = [ctypes.c_longlong, i, i]
@@ -656,6 +706,278 @@ def ring_attn_bwd_ex(q, k, v, out, lse, dout, P: int = 1, causal: bool = False,
           _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
           workspace.numel() * workspace.element_size(), _stream(stream))
     return dq, dk, dv
+
+
+class RopeTable:
+    """Handle of a rotation (ra_rope): frequencies as 64-bit fixed-point fractions of a turn
+    on the device, the number of rotated dims, the pair style and the amplitude.  Made once
+    per model by rope_table."""
+
+    def __init__(self, phases, rot_dim: int, style: str, amplitude: float):
+        self.phases, self.rot_dim, self.style = phases, rot_dim, style
+        self.amplitude = amplitude
+
+    def _c(self):
+        return Rope(phases=self.phases.data_ptr(), rot_dim=self.rot_dim,
+                    style=ROPE_STYLES[self.style], amplitude=self.amplitude)
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, style: str = "half", scaling: str = "none",
+               factor: float = 1.0, original_length: float = 0.0, beta_fast: float = 32.0,
+               beta_slow: float = 1.0, inv_freq=None, amplitude: float | None = None,
+               device=None) -> RopeTable:
+    """The RopeTable of base^(-2i/rot_dim), scaled for longer contexts ("none", "linear",
+    "ntk", "yarn": see ra_rope_scaling), or of inv_freq, rot_dim/2 angles per position in
+    radians given directly.  amplitude overrides the scaling's own.  Computed on the host by
+    the library and copied to the device (waits for the copy)."""
+    if style not in ROPE_STYLES:
+        raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    n = rot_dim // 2
+    phases = (ctypes.c_ulonglong * n)()
+    amp = ctypes.c_float(1.0)
+    if inv_freq is not None:
+        f = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
+        if scaling != "none" or tuple(f.shape) != (n,):
+            raise ValueError("inv_freq must hold rot_dim/2 angles and excludes a scaling")
+        _call("ra_rope_phases_of", _ptr(f), n, phases)
+    else:
+        c = RopeConfig(rot_dim=rot_dim, scaling=ROPE_SCALINGS[scaling], base=base, factor=factor,
+                       original_length=original_length, beta_fast=beta_fast, beta_slow=beta_slow)
+        _call("ra_rope_phases", ctypes.byref(c), phases, ctypes.byref(amp))
+    host = torch.frombuffer(bytearray(phases), dtype=torch.int64).clone()
+    dev = torch.device(device) if device is not None else torch.device(
+        "cuda", torch.cuda.current_device())
+    return RopeTable(host.to(dev), rot_dim, style, amp.value if amplitude is None else amplitude)
+
+
+def _same_device(first, *others):
+    """The device that all the given tensors lie on (Nones are left out)."""
+    if not first.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on one device")
+    return first.device
+
+
+def _on(device, stream):
+    """The stream to launch on: the given one or the device's current one."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError("stream belongs to another device than the tensors")
+    return s
+
+
+def _index_tensor(t, name, dim, sizes=None):
+    if t.dtype != torch.int32 or t.dim() != dim or (sizes and tuple(t.shape) != sizes):
+        raise ValueError(f"{name} must be a {dim}-D int32 CUDA tensor"
+                         + (f" of shape {list(sizes)}" if sizes else ""))
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _token_stride(t, name, dim):
+    """Elements between tokens of [..., H, D] rows whose heads lie side by side (a view of a
+    fused projection output is one such)."""
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+    H, D = t.shape[-2:]
+    if t.stride(-1) != 1 and D > 1 or t.stride(-2) != D and H > 1:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if dim == 4 and t.shape[0] > 1 and t.shape[1] > 1 \
+            and t.stride(0) != t.shape[1] * t.stride(1):
+        raise ValueError(f"{name}: batches must follow one another at the token stride")
+    tokens = 1
+    for n in t.shape[:-2]:
+        tokens *= n
+    if tokens <= 1:
+        return H * D
+    return t.stride(0) if dim == 4 and t.shape[1] == 1 else t.stride(-3)
+
+
+def _float_code(t, name):
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be bf16 or fp32")
+    return RA_BF16 if t.dtype == torch.bfloat16 else RA_F32
+
+
+def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out, k_out, stream):
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    ref = q if q is not None else k
+    device = _same_device(ref, q, k, rope.phases, positions, cu_seqlens, q_out, k_out)
+    code = _float_code(ref, "q and k")
+    packed = layout == "packed"
+    dim = 3 if packed else 4
+    if ref.dim() != dim:
+        raise ValueError("q and k must be [L, H, D] (packed layout) or [B, L, H, D]")
+    B, L = (1, ref.shape[0]) if packed else ref.shape[:2]
+    if q is not None and k is not None and (q.shape[:-2] != k.shape[:-2]
+                                            or q.shape[-1] != k.shape[-1] or q.dtype != k.dtype):
+        raise ValueError("q and k must agree in every dimension but the heads, and in dtype")
+    if packed != (cu_seqlens is not None):
+        raise ValueError("cu_seqlens belongs to the packed layout, which needs it")
+    if packed:
+        _index_tensor(cu_seqlens, "cu_seqlens", 1)
+    if positions is not None:
+        _index_tensor(positions, "positions", 2, (B, L))
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
+    s = _on(device, stream)
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        for x, o in ((q, q_out), (k, k_out)):
+            if x is None and o is not None:
+                raise ValueError("an output without its input")
+            if o is not None and (o.shape != x.shape or o.dtype != x.dtype):
+                raise ValueError("outputs must be shaped and typed like their inputs")
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+        st = {n: _token_stride(t, n, dim) if t is not None and t.numel() else 0
+              for n, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))}
+        if ref.numel() == 0:
+            return q_out, k_out
+        d = RopeDesc(B=B, L=L, H=q.shape[-2] if q is not None else 0,
+                     H_kv=k.shape[-2] if k is not None else 0, D=ref.shape[-1], P=P,
+                     layout=LAYOUTS[layout],
+                     cu_seqlens=cu_seqlens.data_ptr() if packed else None,
+                     n_seqs=cu_seqlens.numel() - 1 if packed else 0,
+                     positions=positions.data_ptr() if positions is not None else None,
+                     position_offset=offset, dtype=code, q_stride=st["q"], k_stride=st["k"],
+                     q_out_stride=st["q_out"], k_out_stride=st["k_out"])
+        _call(name, ctypes.byref(d), ctypes.byref(rope._c()), _ptr(q), _ptr(k), _ptr(q_out),
+              _ptr(k_out), _stream(s))
+    return q_out, k_out
+
+
+def rope_fwd(q, k, rope: RopeTable, positions=None, offset: int = 0, layout: str = "contiguous",
+             P: int = 1, cu_seqlens=None, q_out=None, k_out=None, stream=None):
+    """q [B, L, H, D] and k [B, L, H_kv, D] (bf16 or fp32; either may be None) rotated by
+    their positions, in one launch: a row's position in its shard layout ("contiguous",
+    "zigzag" over P shards, or "packed" with [L, H, D] tensors and cu_seqlens), or
+    positions, an int32 [B, L]; offset is added.  Tokens may be strided views of a fused
+    projection output; q_out=q and k_out=k rotate in place.  Returns (q_out, k_out)."""
+    return _rope_call("rope_fwd", q, k, rope, positions, offset, layout, P, cu_seqlens, q_out,
+                      k_out, stream)
+
+
+def rope_bwd(dq_out, dk_out, rope: RopeTable, positions=None, offset: int = 0,
+             layout: str = "contiguous", P: int = 1, cu_seqlens=None, q_out=None, k_out=None,
+             stream=None):
+    """Gradients of rope_fwd's inputs for those of its outputs (the transposed rotation);
+    arguments as rope_fwd, q_out and k_out receiving dq and dk.  Returns (dq, dk)."""
+    return _rope_call("rope_bwd", dq_out, dk_out, rope, positions, offset, layout, P, cu_seqlens,
+                      q_out, k_out, stream)
+
+
+def _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal):
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype \
+            or k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages must be alike: [num_pages, page_size, H_kv, D] "
+                         "of one dtype with the same strides")
+    if k_pages.stride(3) != 1 and k_pages.shape[3] > 1:
+        raise ValueError("the head vectors of the pages must be contiguous")
+    code = _float_code(k_pages, "the pages")
+    n_seqs = kv_lens.numel()
+    _index_tensor(kv_lens, "kv_lens", 1)
+    _index_tensor(cu_new, "cu_new", 1, (n_seqs + 1,))
+    _index_tensor(page_table, "page_table", 2)
+    if page_table.shape[0] != n_seqs:
+        raise ValueError("page_table must have a row for every sequence")
+    num_pages, page_size, H_kv, D = k_pages.shape
+    return PagedDesc(T=T, n_seqs=n_seqs, H=H, H_kv=H_kv, D=D, num_pages=num_pages,
+                     page_size=page_size, max_pages=page_table.shape[1],
+                     page_stride=k_pages.stride(0), token_stride=k_pages.stride(1),
+                     head_stride=k_pages.stride(2),
+                     table_stride=page_table.stride(0) if n_seqs > 1 else page_table.shape[1],
+                     page_table=page_table.data_ptr(), cu_new=cu_new.data_ptr(),
+                     kv_lens=kv_lens.data_ptr(), dtype=code, causal=int(bool(causal)))
+
+
+def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
+                    rope: RopeTable | None = None, q=None, q_out=None, stream=None):
+    """Writes a step's new keys and values (k, v: [T, H_kv, D]; sequence g's are rows
+    [cu_new[g], cu_new[g + 1]), the last of its kv_lens[g]) into the pages [num_pages,
+    page_size, H_kv, D] that page_table names, k rotated by rope on the way.  q [T, H, D],
+    if given, is rotated into q_out (allocated like q, zeroed, if None; q_out=q in place)
+    and returned.  Pages and tokens may be strided views (see ra_paged_desc)."""
+    device = _same_device(k, v, k_pages, v_pages, page_table, cu_new, kv_lens, q, q_out,
+                          rope.phases if rope is not None else None)
+    T, H_kv, D = k.shape if k.dim() == 3 else (0, 0, 0)
+    if k.shape != v.shape or (H_kv, D) != tuple(k_pages.shape[2:]) or k.dtype != k_pages.dtype \
+            or v.dtype != k.dtype:
+        raise ValueError("k and v must be [T, H_kv, D], with the heads and dtype of the pages")
+    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype):
+        raise ValueError("q must be [T, H, D] with k's tokens, head dim and dtype")
+    if q_out is not None and (q is None or q_out.shape != q.shape or q_out.dtype != q.dtype):
+        raise ValueError("q_out must be shaped and typed like q")
+    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T,
+                    q.shape[1] if q is not None else 0, 0)
+    s = _on(device, stream)
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        if q is not None and q_out is None:
+            q_out = torch.zeros(q.shape, dtype=q.dtype, device=device)
+        if T == 0:
+            return q_out
+        st = [_token_stride(t, n, 3) if t is not None else 0
+              for n, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out))]
+        _call("paged_kv_append", ctypes.byref(d),
+              ctypes.byref(rope._c()) if rope is not None else None, _ptr(q), st[0], _ptr(k), st[1],
+              _ptr(v), st[2], _ptr(q_out), st[3], _ptr(k_pages), _ptr(v_pages), _stream(s))
+    return q_out
+
+
+def paged_attn_workspace(D: int, dtype=torch.bfloat16, device=None):
+    """A zeroed workspace for paged_attn_fwd, of a size that depends only on the head dim and
+    type: keep one per stream (calls that share one must not overlap on the GPU)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dtype must be bf16 or fp32")
+    n = int(load_library().paged_attn_workspace_bytes(
+        D, RA_BF16 if dtype == torch.bfloat16 else RA_F32))
+    if n == 0:
+        raise ValueError(f"no paged attention for head dim {D} in {dtype}")
+    dev = torch.device(device) if device is not None else torch.device(
+        "cuda", torch.cuda.current_device())
+    return torch.zeros(n, dtype=torch.uint8, device=dev)
+
+
+def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: bool = True, out=None,
+                   lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Attention of the step's queries q [T, H, D] over the paged cache (their own keys
+    appended before): row i of a sequence's n new ones sees keys [0, kv_lens - n + i], or all
+    with causal=False.  workspace: paged_attn_workspace(D, dtype), kept by the caller (None
+    allocates and zeroes one for this call).  Returns (out [T, H, D], lse fp32 [T, H]); rows
+    behind the last sequence are left as they are (zero in an out allocated here)."""
+    device = _same_device(q, k_pages, v_pages, page_table, cu_new, kv_lens, out, lse, workspace)
+    if q.dim() != 3 or q.dtype != k_pages.dtype or q.shape[2] != k_pages.shape[-1]:
+        raise ValueError("q must be [T, H, D] with the head dim and dtype of the pages")
+    T, H, D = q.shape
+    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal)
+    for name, t, shape, dtype in (("out", out, (T, H, D), q.dtype),
+                                  ("lse", lse, (T, H), torch.float32)):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    s = _on(device, stream)
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        if out is None:
+            out = torch.zeros((T, H, D), dtype=q.dtype, device=device)
+        if lse is None and want_lse:
+            lse = torch.zeros((T, H), dtype=torch.float32, device=device)
+        if workspace is None:
+            workspace = paged_attn_workspace(D, q.dtype, device)
+        if T == 0:
+            return out, lse
+        _call("paged_attn_fwd", ctypes.byref(d), _ptr(q), _token_stride(q, "q", 3), _ptr(k_pages),
+              _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(workspace),
+              workspace.numel() * workspace.element_size(), _stream(s))
+    return out, lse
 
 
 def check_status(stream=None) -> int:

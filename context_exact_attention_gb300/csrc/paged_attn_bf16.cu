@@ -1,0 +1,371 @@
+// paged_attn_bf16.cu -- paged_attn_fwd for calls with few query rows per key/value head
+// (single tokens, a few proposed ones), bf16: a stream over the cache.
+//
+// With R query rows per key/value head a key costs 4 D bytes and 4 D R operations, so up to
+// R of about 288 (the measured matrix rate over the measured bandwidth) the call is bound by
+// reading the cache.  This kernel serves the low end, where a 128-row tensor-memory tile
+// would be nearly empty: a tile is 16 packed rows (tokens x heads of the group), the rows
+// of an m16n8k16 warp product, held by a block of four warps.
+//
+// Each warp takes 16 of every 64 keys and runs by itself: it copies its 16 keys and values
+// into its own shared-memory ring with 16-byte asynchronous copies (zero-filled for keys
+// that the tile does not see, so that what lies in their slots never matters), multiplies
+// S = Q K^T from the ring, keeps its own running maximum and denominator, rounds the
+// weights to bf16 as they sit in the product's registers and adds P V to its own 16 x D
+// sum.  No barrier is met inside a segment; the four results are joined at its end through
+// shared memory.  The copies run ahead of the products across segments, so a sequence's
+// end does not empty the pipeline, and the page-table entry of a step is fetched one step
+// before its copies are issued.
+//
+// The maximum used in the exponentials is raised only when it grows by more than 2^8 (as
+// in the dense kernels: any common reference leaves the quotient unchanged), so the sums
+// are rarely rescaled.
+#include "paged_plan.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kRows = 16;
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kKeysW = 16;                     // keys per warp and step
+constexpr int kUnit = kKeysW * kWarps;         // keys per block and step
+constexpr float kRescaleThreshold = 8.0f;
+
+template <int D>
+struct Smem {
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kTile = kKeysW * D * 2;              // a warp's keys (or values)
+    static constexpr int kStage = 2 * kTile * kWarps;
+    static constexpr int kLdo = D + 8;                        // padded: rows in different banks
+    static constexpr int kBuf = kStages * kStage;
+    static constexpr int kStatW = kBuf + kRows * kLdo * 4;
+    static constexpr int kStat = kStatW + kWarps * kRows * 8;
+    static constexpr int kScratch = kStat + kRows * 8;
+    static constexpr int kFlag = kScratch + 34 * 8;
+    static constexpr int kBytes = kFlag + 16;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real)
+{
+    const int n = real ? 16 : 0;                              // 0: the 16 bytes become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedParams p)
+{
+    using S = Smem<D>;
+    using Walk = PagedWalk<FlatTiles<kRows>, kRows, kUnit>;
+    constexpr int kStages = S::kStages;
+    constexpr int kChunks = D / 8;                            // 16-byte chunks per key
+    constexpr int kRowsPerCopy = 32 / kChunks;                // keys one warp-wide copy covers
+    constexpr int kSteps = D / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float* buf = reinterpret_cast<float*>(smem + S::kBuf);
+    float2* stat_w = reinterpret_cast<float2*>(smem + S::kStatW);
+    float2* stat = reinterpret_cast<float2*>(smem + S::kStat);
+    long long* scratch = reinterpret_cast<long long*>(smem + S::kScratch);
+    int* flag = reinterpret_cast<int*>(smem + S::kFlag);
+    const PagedArgs& a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(a.k_pages);
+    const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(a.v_pages);
+    const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.q);
+    const uint32_t ring = smem_addr(smem) + warp * 2 * S::kTile;
+
+    Walk walk;                                  // of the products
+    walk.begin<kThreads>(p, scratch);
+    // of the copies, ahead of it
+    Walk ahead = walk;
+    Segment lt;
+    int lk = 0;
+    bool more = true;
+    lt.k1 = 0;
+    long long off = -1;                         // lane < 16: where the step's key lies
+    auto advance = [&]() {
+        lk += kUnit;
+        while (more && lk >= lt.k1) {
+            more = ahead.next(p, lt);
+            lk = lt.k0;
+        }
+        off = -1;
+        const int key = lk + kKeysW * warp + lane;
+        if (more && lane < kKeysW && key < lt.k1) off = key_offset(a, lt.g, lt.hk, key);
+    };
+    auto issue = [&](int stage) {
+        if (more) {
+            const uint32_t dst = ring + stage * S::kStage;
+#pragma unroll
+            for (int j = 0; j < kKeysW / kRowsPerCopy; ++j) {
+                const int row = j * kRowsPerCopy + lane / kChunks, c = lane % kChunks;
+                const long long o = __shfl_sync(0xffffffffu, off, row);
+                const bool real = o >= 0 && in_bounds(o + 8 * c, 8, a.page_elems, a.status);
+                const long long at = real ? o + 8 * c : 0;
+                const uint32_t to = dst + row * (2 * D) + ((c ^ (row & 7)) << 4);
+                cp_async16(to, K + at, real);
+                cp_async16(to + S::kTile, V + at, real);
+            }
+            advance();
+        }
+        cp_async_commit();
+    };
+    // The query fragments of a segment: thread's rows lane / 4 and lane / 4 + 8, columns
+    // 16 step + 2 (lane mod 4) and 8 further.
+    auto load_q = [&](const Segment& t, uint32_t (&q)[kSteps][4]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = (lane >> 2) + 8 * h;
+            long long at = -1;
+            if (r < t.rows) {
+                const long long pr = t.row0 + r, tok = pr / p.G;
+                at = (t.s.first + tok) * a.q_stride +
+                     static_cast<long long>(t.hk * p.G + (pr - tok * p.G)) * D + 2 * (lane & 3);
+            }
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x = 0;
+                    const long long i = at + 16 * k + 8 * c;
+                    if (at >= 0 && in_bounds(i, 2, a.q_elems, a.status))
+                        x = __ldg(reinterpret_cast<const unsigned int*>(Q + i));
+                    q[k][2 * c + h] = x;
+                }
+        }
+    };
+
+    lk = -kUnit;
+    advance();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    int st = 0;                                 // stage of the next step
+
+    Segment t;
+    bool have = walk.next(p, t);
+    uint32_t q[kSteps][4];
+    if (have) load_q(t, q);
+    while (have) {
+        float o[D / 8][4];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        // keys that this thread's two rows see, and that every row of the tile sees
+        auto seen_by = [&](int r) {
+            const int tok = static_cast<int>((t.row0 + r) / p.G);
+            return a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
+        };
+        const int see0 = seen_by(lane >> 2), see1 = seen_by((lane >> 2) + 8);
+        const int see_all = min(seen_by(0), t.k1);
+        for (int k = t.k0; k < t.k1; k += kUnit) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            issue(st == 0 ? kStages - 1 : st - 1);
+            const uint32_t kt = ring + st * S::kStage, vt = kt + S::kTile;
+            st = st + 1 == kStages ? 0 : st + 1;
+
+            float s[2][4] = {};
+            {
+                const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+                const uint32_t row = kt + key * (2 * D);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    uint32_t b[4];
+                    ldmatrix4(row + (((2 * i + half) ^ (key & 7)) << 4), b);
+                    mma16816(s[0], q[i], b[0], b[1]);
+                    mma16816(s[1], q[i], b[2], b[3]);
+                }
+            }
+            const int k0w = k + kKeysW * warp;
+            if (k0w + kKeysW > see_all) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int key = k0w + 8 * i + 2 * (lane & 3) + j;
+                        if (key >= see0 || key >= t.k1) s[i][j] = -INFINITY;
+                        if (key >= see1 || key >= t.k1) s[i][2 + j] = -INFINITY;
+                    }
+            }
+            float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+            float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2)) * p.scale_log2;
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2)) * p.scale_log2;
+            const bool up0 = mx0 > m0 + kRescaleThreshold, up1 = mx1 > m1 + kRescaleThreshold;
+            if (__any_sync(0xffffffffu, up0 || up1)) {
+                const float a0 = up0 ? ex2(m0 - mx0) : 1.f, a1 = up1 ? ex2(m1 - mx1) : 1.f;
+                m0 = up0 ? mx0 : m0;
+                m1 = up1 ? mx1 : m1;
+                l0 *= a0;
+                l1 *= a1;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= a0;
+                    o[i][1] *= a0;
+                    o[i][2] *= a1;
+                    o[i][3] *= a1;
+                }
+            }
+            const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                s[i][0] = ex2(fmaf(s[i][0], p.scale_log2, n0));
+                s[i][1] = ex2(fmaf(s[i][1], p.scale_log2, n0));
+                s[i][2] = ex2(fmaf(s[i][2], p.scale_log2, n1));
+                s[i][3] = ex2(fmaf(s[i][3], p.scale_log2, n1));
+                l0 += s[i][0] + s[i][1];
+                l1 += s[i][2] + s[i][3];
+            }
+            // weights rounded to bf16 (the matrix product's operand type; at most 2^-9
+            // relative each, under the output's own rounding), denominator in fp32
+            const uint32_t pf[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
+                                    pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
+            {
+                const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
+                const uint32_t row = vt + key * (2 * D);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    uint32_t b[4];
+                    ldmatrix4_trans(row + (((2 * i + half) ^ (key & 7)) << 4), b);
+                    mma16816(o[2 * i], pf, b[0], b[1]);
+                    mma16816(o[2 * i + 1], pf, b[2], b[3]);
+                }
+            }
+        }
+        // the next segment's queries are fetched while this one is finished
+        Segment nt;
+        const bool next = walk.next(p, nt);
+        if (next) load_q(nt, q);
+
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        const int r0 = lane >> 2, r1 = r0 + 8;
+        if ((lane & 3) == 0) {
+            stat_w[warp * kRows + r0] = make_float2(m0, l0);
+            stat_w[warp * kRows + r1] = make_float2(m1, l1);
+        }
+        __syncthreads();
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = h ? r1 : r0;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat_w[w * kRows + r].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 x = stat_w[w * kRows + r];
+                if (!(x.y == 0.f)) L += part_weight(x.x, x.y, M) * x.y;
+            }
+            f[h] = part_weight(h ? m1 : m0, h ? l1 : l0, M);
+            if (warp == 0 && (lane & 3) == 0) stat[r] = make_float2(M, L);
+        }
+        for (int w = 0; w < kWarps; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float2* dst = reinterpret_cast<float2*>(
+                            buf + (h ? r1 : r0) * S::kLdo + 8 * i + 2 * (lane & 3));
+                        float2 x = w == 0 ? make_float2(0.f, 0.f) : *dst;
+                        x.x = fmaf(f[h], o[i][2 * h], x.x);
+                        x.y = fmaf(f[h], o[i][2 * h + 1], x.y);
+                        *dst = x;
+                    }
+            }
+            __syncthreads();
+        }
+        finish_segment<__nv_bfloat16, kRows, kThreads>(p, t, buf, S::kLdo, stat, flag);
+        t = nt;
+        have = next;
+    }
+    cp_async_wait<0>();
+}
+
+template <int D>
+cudaError_t launch_d(PagedParams& p)
+{
+    const PagedArgs& a = p.a;
+    static std::atomic<int> configured[kMaxDevices];
+    int dev = 0, sms = 148, per_sm = 1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = smem_limit_once(configured, dev, paged_bf16_kernel<D>, Smem<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_bf16_kernel<D>, kThreads,
+                                                      Smem<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    long long grid = static_cast<long long>(sms) * (per_sm > 0 ? per_sm : 1);
+    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
+    p.grid = static_cast<int>(grid);
+    p.min_chunk = 2 * kUnit;
+    p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
+    const PagedWorkspace w = paged_workspace_of(p.grid, kRows, D);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    p.counters = reinterpret_cast<unsigned int*>(ws);
+    p.part_stat = reinterpret_cast<float*>(ws + w.stat);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
+    paged_bf16_kernel<D><<<static_cast<unsigned>(grid), kThreads, Smem<D>::kBytes, a.stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_bf16(const PagedArgs& a)
+{
+    PagedParams p;
+    p.a = a;
+    p.G = a.H / a.H_kv;
+    if (a.D == 64) return launch_d<64>(p);
+    if (a.D == 128) return launch_d<128>(p);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_paged(const PagedArgs& a)
+{
+    return a.elem == 2 ? launch_paged_bf16(a) : launch_paged_simt(a);
+}
+
+unsigned long long paged_workspace_bytes(int D, int elem)
+{
+    return paged_workspace_of(kPagedMaxCtas, elem == 2 ? kRows : 4, D).total;
+}
+
+}  // namespace ra

@@ -1,0 +1,228 @@
+// paged_attn_simt.cu -- paged_attn_fwd without tensor cores: fp32 caches.
+//
+// One block holds four query rows of one key/value head in registers (a lane keeps four
+// consecutive columns of each) and its four warps walk the CTA's part of the keys in turns
+// of eight.  A key's row is read by a warp as one coalesced run straight into registers:
+// every element is used for four rows and never goes through shared memory.  The 32 dot
+// products of a turn (8 keys x 4 rows) are partial sums over columns in every lane; a
+// butterfly that halves the values at each step leaves the total of (key, row) in lane
+// 4 key + row with 31 shuffles, where reducing them one by one would take 160.  That lane
+// then owns the score: mask, maximum over the keys (three shuffles), exponential, and the
+// eight weights of a row are read back by shuffle for the value sum.
+//
+// What bounds it: bytes, for up to four rows a head.  A turn moves 8 keys (8 KB at D 128)
+// for about 400 warp instructions, which an SM issues in 100 cycles; HBM delivers them in
+// about 350.  More rows per head (long prompts in fp32) are taken four at a time and
+// re-read the keys, which then come from L2.
+#include "paged_plan.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kRows = 4;
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTurn = 8;                       // keys per warp and turn
+constexpr int kUnit = kTurn * kWarps;
+
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+
+template <int kVec4>
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams p)
+{
+    using Walk = PagedWalk<FlatTiles<kRows>, kRows, kUnit>;
+    __shared__ long long scratch[34];
+    __shared__ float2 stat_w[kWarps][kRows];
+    __shared__ float2 stat[kRows];
+    __shared__ int flag;
+    __shared__ alignas(16) float buf[kRows][kVec4 * 128];
+    const PagedArgs& a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int D = a.D;
+    const float* Q = static_cast<const float*>(a.q);
+    const float* K = static_cast<const float*>(a.k_pages);
+    const float* V = static_cast<const float*>(a.v_pages);
+
+    Walk walk;
+    walk.begin<kThreads>(p, scratch);
+    Segment t;
+    while (walk.next(p, t)) {
+        float4 q[kRows][kVec4], o[kRows][kVec4];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+            for (int u = 0; u < kVec4; ++u) {
+                const int c = 4 * (lane + 32 * u);
+                q[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                o[r][u] = q[r][u];
+                if (r < t.rows && c < D) {
+                    const long long pr = t.row0 + r, tok = pr / p.G;
+                    const long long at = (t.s.first + tok) * a.q_stride +
+                                         static_cast<long long>(t.hk * p.G + (pr - tok * p.G)) * D + c;
+                    if (in_bounds(at, 4, a.q_elems, a.status)) q[r][u] = load4(Q + at);
+                }
+            }
+        }
+        // this lane's score is of row lane & 3: the keys it sees are [0, seen)
+        const int my_row = lane & 3, my_key = lane >> 2;
+        int seen = 0;
+        if (my_row < t.rows) {
+            const int tok = static_cast<int>((t.row0 + my_row) / p.G);
+            seen = a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
+        }
+        float m = -INFINITY, l = 0.f;      // of row my_row; l over this lane's keys only
+        for (int k = t.k0 + kTurn * warp; k < t.k1; k += kUnit) {
+            long long off = -1;
+            if (lane < kTurn && k + lane < t.k1) off = key_offset(a, t.g, t.hk, k + lane);
+            float4 kk[kTurn][kVec4], vv[kTurn][kVec4];
+#pragma unroll
+            for (int j = 0; j < kTurn; ++j) {
+                const long long oj = __shfl_sync(0xffffffffu, off, j);
+#pragma unroll
+                for (int u = 0; u < kVec4; ++u) {
+                    const int c = 4 * (lane + 32 * u);
+                    kk[j][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    vv[j][u] = kk[j][u];
+                    if (oj >= 0 && c < D && in_bounds(oj + c, 4, a.page_elems, a.status)) {
+                        kk[j][u] = load4(K + oj + c);
+                        vv[j][u] = load4(V + oj + c);
+                    }
+                }
+            }
+            float s[32];
+#pragma unroll
+            for (int j = 0; j < kTurn; ++j)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int u = 0; u < kVec4; ++u) {
+                        x = fmaf(q[r][u].x, kk[j][u].x, x);
+                        x = fmaf(q[r][u].y, kk[j][u].y, x);
+                        x = fmaf(q[r][u].z, kk[j][u].z, x);
+                        x = fmaf(q[r][u].w, kk[j][u].w, x);
+                    }
+                    s[4 * j + r] = x;
+                }
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) {
+                const bool up = lane & w;
+#pragma unroll
+                for (int i = 0; i < w; ++i) {
+                    const float send = up ? s[i] : s[i + w];
+                    const float keep = up ? s[i + w] : s[i];
+                    s[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+                }
+            }
+            const int key = k + my_key;
+            const bool sees = key < seen && key < t.k1;
+            const unsigned vis = __ballot_sync(0xffffffffu, sees);
+            const float x = sees ? s[0] * p.scale_log2 : -INFINITY;
+            float mx = x;
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float m_new = fmaxf(m, mx);
+            const float alpha = m_new > m ? ex2(m - m_new) : 1.f;
+            const float pe = ex2(x - (m_new == -INFINITY ? 0.f : m_new));
+            l = l * alpha + pe;
+            m = m_new;
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const float ar = __shfl_sync(0xffffffffu, alpha, r);
+#pragma unroll
+                    for (int u = 0; u < kVec4; ++u) {
+                        o[r][u].x *= ar;
+                        o[r][u].y *= ar;
+                        o[r][u].z *= ar;
+                        o[r][u].w *= ar;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kTurn; ++j)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const float w = __shfl_sync(0xffffffffu, pe, 4 * j + r);
+                    // a value that the row does not see stays out even if it is not finite
+                    if (!((vis >> (4 * j + r)) & 1)) continue;
+#pragma unroll
+                    for (int u = 0; u < kVec4; ++u) {
+                        o[r][u].x = fmaf(w, vv[j][u].x, o[r][u].x);
+                        o[r][u].y = fmaf(w, vv[j][u].y, o[r][u].y);
+                        o[r][u].z = fmaf(w, vv[j][u].z, o[r][u].z);
+                        o[r][u].w = fmaf(w, vv[j][u].w, o[r][u].w);
+                    }
+                }
+        }
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+        // the four warps' results, joined in warp order
+        if (lane < kRows) stat_w[warp][lane] = make_float2(m, l);
+        __syncthreads();
+        if (threadIdx.x < kRows) {
+            float M = -INFINITY, L = 0.f;
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat_w[w][threadIdx.x].x);
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 st = stat_w[w][threadIdx.x];
+                if (!(st.y == 0.f)) L += part_weight(st.x, st.y, M) * st.y;
+            }
+            stat[threadIdx.x] = make_float2(M, L);
+        }
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const float f = part_weight(stat_w[w][r].x, stat_w[w][r].y, stat[r].x);
+#pragma unroll
+                    for (int u = 0; u < kVec4; ++u) {
+                        float4* dst = reinterpret_cast<float4*>(&buf[r][4 * (lane + 32 * u)]);
+                        float4 x = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *dst;
+                        x.x = fmaf(f, o[r][u].x, x.x);
+                        x.y = fmaf(f, o[r][u].y, x.y);
+                        x.z = fmaf(f, o[r][u].z, x.z);
+                        x.w = fmaf(f, o[r][u].w, x.w);
+                        *dst = x;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        finish_segment<float, kRows, kThreads>(p, t, &buf[0][0], kVec4 * 128, stat, &flag);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_simt(const PagedArgs& a)
+{
+    PagedParams p;
+    p.a = a;
+    p.G = a.H / a.H_kv;
+    int dev = 0, sms = 148, per_sm = 1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    e = a.D <= 128
+            ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_simt_kernel<1>, kThreads, 0)
+            : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_simt_kernel<2>, kThreads, 0);
+    if (e != cudaSuccess) return e;
+    long long grid = static_cast<long long>(sms) * (per_sm > 0 ? per_sm : 1);
+    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
+    p.grid = static_cast<int>(grid);
+    p.min_chunk = 4 * kUnit;
+    p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.D));
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    const PagedWorkspace w = paged_workspace_of(p.grid, kRows, a.D);
+    p.counters = reinterpret_cast<unsigned int*>(ws);
+    p.part_stat = reinterpret_cast<float*>(ws + w.stat);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
+    if (a.D <= 128)
+        paged_simt_kernel<1><<<static_cast<unsigned>(grid), kThreads, 0, a.stream>>>(p);
+    else
+        paged_simt_kernel<2><<<static_cast<unsigned>(grid), kThreads, 0, a.stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace ra

@@ -141,6 +141,64 @@ cudaError_t launch_ulysses_permute(const void* in, void* out, int B, int L, int 
 cudaError_t launch_wait_probe(unsigned int* status, unsigned long long timeout_ns,
                               cudaStream_t stream);
 
+// Rotary positions (rope_fwd, rope_bwd) and the paged append: rows of heads, rotated.
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    const void* v;                 // paged append only
+    void* q_out;
+    void* k_out;                   // paged append: the k pages
+    void* v_out;                   // paged append: the v pages
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;   // elements per token
+    long long q_elems, k_elems, v_elems, q_out_elems, k_out_elems;        // extents, for checks
+    long long rows;                // tokens
+    int L, P, H, H_kv, D, elem;    // H, H_kv: heads of q, of k (and v); elem: bytes
+    int rot, half_style;
+    float amplitude, sign;
+    const unsigned long long* phases;
+    ra_layout layout;
+    const int* positions;          // or null: by layout
+    int position_offset;
+    const int* cu_seqlens;         // packed layout; paged append: the new tokens' starts
+    int n_seqs;
+    int paged;
+    const int* kv_lens;
+    const int* page_table;
+    long long table_stride, table_elems, page_stride, token_stride, head_stride;
+    int num_pages, page_size, max_pages;
+    int tokens;                    // tokens per block (set by the launch)
+    unsigned int* status;
+    cudaStream_t stream;
+};
+cudaError_t launch_rope(const RopeArgs& a);
+
+// Attention over a paged cache (paged_attn_fwd).
+struct PagedArgs {
+    const void* q;
+    const void* k_pages;
+    const void* v_pages;
+    void* out;
+    float* lse;                    // may be null
+    void* workspace;
+    long long q_stride;            // elements per token
+    long long q_elems, page_elems, out_elems, lse_elems, table_elems;     // extents, for checks
+    long long page_stride, token_stride, head_stride, table_stride;
+    int T, n_seqs, H, H_kv, D, elem, causal;
+    int num_pages, page_size, max_pages;
+    const int* cu_new;
+    const int* kv_lens;
+    const int* page_table;
+    unsigned int* status;
+    unsigned long long timeout_ns;
+    cudaStream_t stream;
+};
+// CTAs a call may launch (the workspace holds two partial results for each).
+constexpr int kPagedMaxCtas = 1024;
+unsigned long long paged_workspace_bytes(int D, int elem);
+cudaError_t launch_paged(const PagedArgs& a);        // chooses among:
+cudaError_t launch_paged_simt(const PagedArgs& a);   // fp32
+cudaError_t launch_paged_bf16(const PagedArgs& a);   // bf16
+
 // Device address of the current device's status word (api.cu).
 ra_status current_status_word(unsigned int** out);
 

@@ -495,6 +495,212 @@ ra_status ring_attn_bwd_ex(const ra_attn_desc* desc, const void* q, const void* 
                            ra_stream_t stream);
 
 /*
+ * Rotary positions.
+ *
+ * The first rot_dim dims of a head vector form rot_dim/2 pairs: (x[i], x[i + rot_dim/2])
+ * in the half style, (x[2i], x[2i + 1]) in the interleaved one.  Pair i of a token at
+ * position p turns by the angle t = p f_i and is scaled by the amplitude A:
+ *   y_a = A (x_a cos t - x_b sin t),   y_b = A (x_b cos t + x_a sin t);
+ * the dims behind rot_dim pass through unchanged.  (No counterpart on the pages, whose
+ * layouts it serves: "序列并行与 Ring Attention", section 3.4's zigzag shards and section
+ * 6.5's packed sequences change which position a row has.)
+ *
+ * ra_rope is the handle a program makes once per model:
+ *   phases     DEVICE array of rot_dim/2 frequencies as 64-bit fixed-point fractions of a
+ *              turn per position (f_i / (2 pi) 2^64), so that p * phases[i] modulo 2^64 is
+ *              the angle exactly for every position; filled on the host by ra_rope_phases
+ *              or ra_rope_phases_of and copied there by the caller;
+ *   rot_dim    even, 2 <= rot_dim <= D;
+ *   style      ra_rope_style;
+ *   amplitude  A (1 unless the scaling sets it).
+ */
+typedef enum { RA_ROPE_HALF = 0, RA_ROPE_INTERLEAVED = 1 } ra_rope_style;
+
+typedef struct {
+    const unsigned long long* phases;
+    int rot_dim;
+    ra_rope_style style;
+    float amplitude;
+} ra_rope;
+
+/*
+ * Frequencies f_i = base^(-2 i / rot_dim), and how they are changed to reach contexts
+ * `factor` times longer than a model was trained for:
+ *   RA_ROPE_NONE    unchanged;
+ *   RA_ROPE_LINEAR  positions interpolated: f_i / factor;
+ *   RA_ROPE_NTK     base raised: base factor^(rot_dim / (rot_dim - 2));
+ *   RA_ROPE_YARN    by parts: pairs that make more than beta_fast turns over
+ *                   original_length positions keep f_i, those that make fewer than
+ *                   beta_slow get f_i / factor, a linear ramp over the pair index in
+ *                   between; amplitude 0.1 ln(factor) + 1 for factor > 1.
+ */
+typedef enum {
+    RA_ROPE_NONE = 0, RA_ROPE_LINEAR = 1, RA_ROPE_NTK = 2, RA_ROPE_YARN = 3
+} ra_rope_scaling;
+
+typedef struct {
+    int rot_dim;
+    ra_rope_scaling scaling;
+    double base, factor, original_length, beta_fast, beta_slow;
+} ra_rope_config;
+
+/*
+ * ra_rope_phases -- the HOST array phases[rot_dim / 2] and the amplitude for *config.
+ * ra_rope_phases_of -- the same conversion for n angles per position given directly, in
+ * radians (any other scaling rule).  Pure host arithmetic (no device, no stream).
+ * RA_ERR_INVALID_ARG: NULL pointers, an odd or non-positive rot_dim, n < 1, a base or
+ * factor that is not positive and finite, an unknown scaling, an angle that is not finite.
+ */
+ra_status ra_rope_phases(const ra_rope_config* config, unsigned long long* phases,
+                         float* amplitude);
+ra_status ra_rope_phases_of(const double* inv_freq, int n, unsigned long long* phases);
+
+/*
+ * Problem description of rope_fwd / rope_bwd.
+ *   B, L, H, H_kv, D  q is [B, L, H, D], k is [B, L, H_kv, D]; one of H, H_kv may be 0 (its
+ *                     pointers NULL).  D * element size a multiple of 16 bytes, D <= 256;
+ *   layout, P         the position of row l: RA_LAYOUT_CONTIGUOUS l; RA_LAYOUT_ZIGZAG the
+ *                     global position of ring_attn_fwd_zigzag's row order (L % 2P == 0);
+ *                     RA_LAYOUT_PACKED (B == 1) its offset in its own sequence, rows that
+ *                     no sequence holds being left as they are;
+ *   cu_seqlens        RA_LAYOUT_PACKED only: DEVICE int32 [n_seqs + 1], non-decreasing;
+ *   positions         NULL, or with RA_LAYOUT_CONTIGUOUS a DEVICE int32 [B, L]: the
+ *                     position of every row (any int32, negative ones included);
+ *   position_offset   added to every position (the tokens before a continued sequence);
+ *   dtype             RA_BF16 or RA_F32;
+ *   *_stride          elements from one token's first head to the next token's (row
+ *                     b * L + l), 0 for H * D (H_kv * D): q and k may be views of a fused
+ *                     projection output.  Multiples of 16 bytes.
+ */
+typedef struct {
+    int B, L, H, H_kv, D, P;
+    ra_layout layout;
+    const int* cu_seqlens;
+    int n_seqs;
+    const int* positions;
+    int position_offset;
+    ra_dtype dtype;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+} ra_rope_desc;
+
+/*
+ * rope_fwd -- q and k rotated into q_out and k_out in one launch.  In place is allowed
+ * (q_out == q with the same stride), any other overlap is refused; q and k (and their
+ * outputs) may be interleaved rows of one buffer.  Angles are exact to fp32 at any position;
+ * products in fp32, one rounding to the tensor's type (nearest even).
+ * rope_bwd -- its backward: the transpose, which is the rotation by the opposite angle with
+ * the same amplitude.  dq_out, dk_out are the gradients of q_out, k_out (strides q_stride,
+ * k_stride), dq, dk those of q, k (strides q_out_stride, k_out_stride).
+ * Errors: RA_ERR_INVALID_ARG (NULL or superfluous pointers, sizes, strides, overlap,
+ * positions together with another layout), RA_ERR_UNSUPPORTED (dtype, D),
+ * RA_ERR_MISALIGNED (pointers and strides not multiples of 16 bytes), RA_ERR_NOT_DIVISIBLE
+ * (L % P, or L % 2P for zigzag).  Malformed cu_seqlens give undefined results, never
+ * out-of-bounds accesses.
+ */
+ra_status rope_fwd(const ra_rope_desc* desc, const ra_rope* rope, const void* q, const void* k,
+                   void* q_out, void* k_out, ra_stream_t stream);
+ra_status rope_bwd(const ra_rope_desc* desc, const ra_rope* rope, const void* dq_out,
+                   const void* dk_out, void* dq, void* dk, ra_stream_t stream);
+
+/*
+ * The paged key/value cache (no counterpart on the pages: the serving side of the same
+ * attention).
+ *
+ * The keys of a layer lie in num_pages pages of page_size slots, [num_pages, page_size,
+ * H_kv, D] with the strides below, and the values in a second array of the same geometry.
+ * Sequence g's key at position j is slot j % page_size of page
+ * page_table[g * table_stride + j / page_size].  A step brings T new token rows: rows
+ * [cu_new[g], cu_new[g + 1]) are the last ones of sequence g, which then has kv_lens[g]
+ * keys, so row i of its n new ones stands at position kv_lens[g] - n + i.
+ *
+ *   T, n_seqs         new token rows (0 allowed) and sequences; rows that no sequence holds
+ *                     (padding behind the last one) are neither read into a result nor
+ *                     written;
+ *   H, H_kv, D        query heads, key/value heads, head dim;
+ *   page_stride, token_stride, head_stride
+ *                     elements between pages, slots, heads: any order (a page may hold its
+ *                     heads or its slots outermost, keys and values may alternate in one
+ *                     buffer) as long as head vectors are contiguous, do not overlap and
+ *                     start on 16-byte boundaries;
+ *   page_table        DEVICE int32 [n_seqs, max_pages], rows table_stride entries apart;
+ *   cu_new            DEVICE int32 [n_seqs + 1], non-decreasing (equal entries: a sequence
+ *                     without new tokens);
+ *   kv_lens           DEVICE int32 [n_seqs], keys including the new tokens;
+ *   dtype             RA_BF16 or RA_F32;
+ *   causal            paged_attn_fwd only: a row sees the keys up to its own position, or
+ *                     with 0 all kv_lens[g].
+ * The lengths are read on the device by every launch: a captured graph follows what the
+ * arrays hold when it is replayed.  Sequences may share pages that they only read.
+ * Whatever these arrays hold, no access leaves the tensors: a page index outside
+ * [0, num_pages) stores nothing in the append and reads as zero keys and values in the
+ * attention, and positions at or beyond max_pages * page_size are not stored; the attention
+ * takes kv_lens above that as that.
+ */
+typedef struct {
+    int T, n_seqs, H, H_kv, D;
+    int num_pages, page_size, max_pages;
+    long long page_stride, token_stride, head_stride, table_stride;
+    const int* page_table;
+    const int* cu_new;
+    const int* kv_lens;
+    ra_dtype dtype;
+    int causal;
+} ra_paged_desc;
+
+/*
+ * paged_kv_append -- writes a step's new keys and values into the pages, rotating on the
+ * way, in one launch: k is rotated by its position and stored, v is stored as it is, and q
+ * (optional) is rotated into q_out, so that the step's attention can follow directly.
+ *
+ * rope: the rotation (rope_fwd's numerics), or NULL to store k (and copy q) unrotated.
+ * q, k, v: [T, H, D] and [T, H_kv, D], head vectors contiguous, tokens *_stride elements
+ * apart (0: contiguous), so that all three may be views of a fused projection output.
+ * q, q_out: both NULL, or q_out as q (in place allowed).  The pages must overlap nothing
+ * else; k_pages and v_pages may alternate in one buffer.  If two rows map to one slot,
+ * either's vectors may be the ones kept.  D * element size a multiple of 16 bytes, D <= 256.
+ * Errors as rope_fwd.
+ */
+ra_status paged_kv_append(const ra_paged_desc* desc, const ra_rope* rope, const void* q,
+                          long long q_stride, const void* k, long long k_stride, const void* v,
+                          long long v_stride, void* q_out, long long q_out_stride, void* k_pages,
+                          void* v_pages, ra_stream_t stream);
+
+/*
+ * paged_attn_workspace_bytes -- device bytes paged_attn_fwd needs for a head dim and type,
+ * whatever the lengths (0 for a head dim the type does not have).
+ */
+unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
+
+/*
+ * paged_attn_fwd -- the new tokens' queries attend to the cache (their own keys included,
+ * which paged_kv_append has stored before): for row i of sequence g and query head h, with
+ * key/value head h / (H / H_kv),
+ *   out = sum_j softmax_j(q . k_j / sqrt(D)) v_j,   lse = ln sum_j exp(q . k_j / sqrt(D))
+ * over the keys j the row sees.  One token per sequence or thousands, in any mixture: the
+ * keys are shared out evenly over the GPU whatever the lengths are.  (out, lse) is a partial
+ * that attn_merge_partials can join with another over other keys.  A row that sees no key
+ * gets 0 and -inf.  Slots behind a sequence's last key are never used, whatever they hold.
+ * In the tensor-core kernels (bf16) a value row that is not finite may also reach rows of
+ * the same call that stand up to 127 positions before it.
+ *
+ * q: [T, H, D], tokens q_stride elements apart (0: contiguous); out: [T, H, D] contiguous;
+ * lse: fp32 [T, H] or NULL.  D 64 or 128 (RA_BF16), a multiple of 4 up to 256 (RA_F32).
+ * workspace: at least paged_attn_workspace_bytes(D, dtype) bytes, 256-byte aligned, ZEROED
+ * by the caller before its first use; every call leaves it ready for the next.  Calls that
+ * share a workspace must not overlap on the GPU (two captured graphs that share one must be
+ * replayed in order).  After a call that timed out (ra_check_status) zero it again.
+ * Scores and softmax in fp32; the bf16 kernels round the weights to bf16 for the value
+ * product, whose sums are fp32; out is rounded once.  Repeated calls on the same inputs give
+ * the same bits; the split over the GPU, and with it the last bits, depends on all lengths of
+ * the call.  Limits: T * H < 2^31.  Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED (dtype,
+ * D), RA_ERR_NOT_DIVISIBLE (H % H_kv), RA_ERR_MISALIGNED, RA_ERR_CUDA.
+ */
+ra_status paged_attn_fwd(const ra_paged_desc* desc, const void* q, long long q_stride,
+                         const void* k_pages, const void* v_pages, void* out, float* lse,
+                         void* workspace, unsigned long long workspace_bytes,
+                         ra_stream_t stream);
+
+/*
  * ra_check_status -- synchronise `stream`, then read and clear the status word
  * of the current device.  Returns RA_ERR_TIMEOUT if a kernel gave up on a
  * bounded wait since the last check, RA_ERR_BOUNDS (debug build) if an index
