@@ -716,10 +716,7 @@ class RopeTable:
     def __init__(self, phases, rot_dim: int, style: str, amplitude: float):
         self.phases, self.rot_dim, self.style = phases, rot_dim, style
         self.amplitude = amplitude
-
-    def _c(self):
-        return Rope(phases=self.phases.data_ptr(), rot_dim=self.rot_dim,
-                    style=ROPE_STYLES[self.style], amplitude=self.amplitude)
+        self._c = ctypes.byref(Rope(phases.data_ptr(), rot_dim, ROPE_STYLES[style], amplitude))
 
 
 def rope_table(rot_dim: int, base: float = 10000.0, style: str = "half", scaling: str = "none",
@@ -754,72 +751,92 @@ def rope_table(rot_dim: int, base: float = 10000.0, style: str = "half", scaling
     return RopeTable(host.to(dev), rot_dim, style, amp.value if amplitude is None else amplitude)
 
 
+# The calls below are short on the GPU (a decoding step's are a few microseconds), so what
+# they do on the host counts: no context managers unless the call leaves the current device
+# or stream, integers for pointers, descriptors filled by position.
+
 def _same_device(first, *others):
     """The device that all the given tensors lie on (Nones are left out)."""
-    if not first.is_cuda:
+    device = first.device
+    if device.type != "cuda":
         raise ValueError("tensors must be CUDA tensors")
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.device != device:
             raise ValueError("all tensors must be on one device")
-    return first.device
+    return device
 
 
-def _on(device, stream):
-    """The stream to launch on: the given one or the device's current one."""
+def _launch_on(device, stream, body):
+    """body(stream handle) with `device` current and, if a stream is given, `stream` current
+    as well (so that what body allocates belongs to it)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(torch.cuda.current_stream(device).cuda_stream)
     s = stream if stream is not None else torch.cuda.current_stream(device)
     if s.device != device:
         raise ValueError("stream belongs to another device than the tensors")
-    return s
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        return body(s.cuda_stream)
+
+
+def _call_fast(name, *args):
+    rc = getattr(_lib if _lib is not None else load_library(), name)(*args)
+    if rc != 0:
+        raise RingAttnError(name, rc)
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _index_tensor(t, name, dim, sizes=None):
     if t.dtype != torch.int32 or t.dim() != dim or (sizes and tuple(t.shape) != sizes):
         raise ValueError(f"{name} must be a {dim}-D int32 CUDA tensor"
                          + (f" of shape {list(sizes)}" if sizes else ""))
-    if t.numel() and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.numel() > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 def _token_stride(t, name, dim):
     """Elements between tokens of [..., H, D] rows whose heads lie side by side (a view of a
     fused projection output is one such)."""
-    if t.dim() != dim:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
-    H, D = t.shape[-2:]
-    if t.stride(-1) != 1 and D > 1 or t.stride(-2) != D and H > 1:
+    H, D = shape[-2:]
+    if stride[-1] != 1 and D > 1 or stride[-2] != D and H > 1:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if dim == 4 and t.shape[0] > 1 and t.shape[1] > 1 \
-            and t.stride(0) != t.shape[1] * t.stride(1):
+    if dim == 3:
+        return stride[0] if shape[0] > 1 else H * D
+    B, L = shape[:2]
+    if B > 1 and L > 1 and stride[0] != L * stride[1]:
         raise ValueError(f"{name}: batches must follow one another at the token stride")
-    tokens = 1
-    for n in t.shape[:-2]:
-        tokens *= n
-    if tokens <= 1:
-        return H * D
-    return t.stride(0) if dim == 4 and t.shape[1] == 1 else t.stride(-3)
+    return stride[1] if L > 1 else stride[0] if B > 1 else H * D
 
 
-def _float_code(t, name):
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name} must be bf16 or fp32")
-    return RA_BF16 if t.dtype == torch.bfloat16 else RA_F32
+def _float_code(dtype, name):
+    if dtype == torch.bfloat16:
+        return RA_BF16
+    if dtype == torch.float32:
+        return RA_F32
+    raise ValueError(f"{name} must be bf16 or fp32")
 
 
 def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out, k_out, stream):
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
-    if q is None and k is None:
-        raise ValueError("q or k must be given")
     ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
     device = _same_device(ref, q, k, rope.phases, positions, cu_seqlens, q_out, k_out)
-    code = _float_code(ref, "q and k")
+    code = _float_code(ref.dtype, "q and k")
     packed = layout == "packed"
     dim = 3 if packed else 4
     if ref.dim() != dim:
         raise ValueError("q and k must be [L, H, D] (packed layout) or [B, L, H, D]")
-    B, L = (1, ref.shape[0]) if packed else ref.shape[:2]
-    if q is not None and k is not None and (q.shape[:-2] != k.shape[:-2]
-                                            or q.shape[-1] != k.shape[-1] or q.dtype != k.dtype):
+    lead = ref.shape[:-2]
+    B, L = (1, lead[0]) if packed else lead
+    if q is not None and k is not None and (k.shape[:-2] != lead or q.shape[-1] != k.shape[-1]
+                                            or q.dtype != k.dtype):
         raise ValueError("q and k must agree in every dimension but the heads, and in dtype")
     if packed != (cu_seqlens is not None):
         raise ValueError("cu_seqlens belongs to the packed layout, which needs it")
@@ -829,32 +846,26 @@ def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out
         _index_tensor(positions, "positions", 2, (B, L))
         if not positions.is_contiguous():
             raise ValueError("positions must be contiguous")
-    s = _on(device, stream)
-    with torch.cuda.device(device), torch.cuda.stream(s):
-        for x, o in ((q, q_out), (k, k_out)):
-            if x is None and o is not None:
-                raise ValueError("an output without its input")
-            if o is not None and (o.shape != x.shape or o.dtype != x.dtype):
-                raise ValueError("outputs must be shaped and typed like their inputs")
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
-        st = {n: _token_stride(t, n, dim) if t is not None and t.numel() else 0
-              for n, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))}
-        if ref.numel() == 0:
-            return q_out, k_out
-        d = RopeDesc(B=B, L=L, H=q.shape[-2] if q is not None else 0,
-                     H_kv=k.shape[-2] if k is not None else 0, D=ref.shape[-1], P=P,
-                     layout=LAYOUTS[layout],
-                     cu_seqlens=cu_seqlens.data_ptr() if packed else None,
-                     n_seqs=cu_seqlens.numel() - 1 if packed else 0,
-                     positions=positions.data_ptr() if positions is not None else None,
-                     position_offset=offset, dtype=code, q_stride=st["q"], k_stride=st["k"],
-                     q_out_stride=st["q_out"], k_out_stride=st["k_out"])
-        _call(name, ctypes.byref(d), ctypes.byref(rope._c()), _ptr(q), _ptr(k), _ptr(q_out),
-              _ptr(k_out), _stream(s))
-    return q_out, k_out
+    for x, o in ((q, q_out), (k, k_out)):
+        if o is not None and (x is None or o.shape != x.shape or o.dtype != x.dtype):
+            raise ValueError("outputs must be shaped and typed like their inputs")
+
+    def body(s):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=device) if q is not None and q_out is None else q_out
+        ko = torch.empty(k.shape, dtype=k.dtype, device=device) if k is not None and k_out is None else k_out
+        if B == 0 or L == 0:
+            return qo, ko
+        H, qs, qos = (q.shape[-2], _token_stride(q, "q", dim),
+                      _token_stride(qo, "q_out", dim)) if q is not None else (0, 0, 0)
+        H_kv, ks, kos = (k.shape[-2], _token_stride(k, "k", dim),
+                         _token_stride(ko, "k_out", dim)) if k is not None else (0, 0, 0)
+        d = RopeDesc(B, L, H, H_kv, ref.shape[-1], P, LAYOUTS[layout], _addr(cu_seqlens),
+                     cu_seqlens.numel() - 1 if packed else 0, _addr(positions), offset, code,
+                     qs, ks, qos, kos)
+        _call_fast(name, ctypes.byref(d), rope._c, _addr(q), _addr(k), _addr(qo), _addr(ko), s)
+        return qo, ko
+
+    return _launch_on(device, stream, body)
 
 
 def rope_fwd(q, k, rope: RopeTable, positions=None, offset: int = 0, layout: str = "contiguous",
@@ -878,27 +889,24 @@ def rope_bwd(dq_out, dk_out, rope: RopeTable, positions=None, offset: int = 0,
 
 
 def _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal):
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype \
-            or k_pages.stride() != v_pages.stride():
+    shape, stride = k_pages.shape, k_pages.stride()
+    if len(shape) != 4 or shape != v_pages.shape or k_pages.dtype != v_pages.dtype \
+            or stride != v_pages.stride():
         raise ValueError("k_pages and v_pages must be alike: [num_pages, page_size, H_kv, D] "
                          "of one dtype with the same strides")
-    if k_pages.stride(3) != 1 and k_pages.shape[3] > 1:
+    if stride[3] != 1 and shape[3] > 1:
         raise ValueError("the head vectors of the pages must be contiguous")
-    code = _float_code(k_pages, "the pages")
+    code = _float_code(k_pages.dtype, "the pages")
     n_seqs = kv_lens.numel()
     _index_tensor(kv_lens, "kv_lens", 1)
     _index_tensor(cu_new, "cu_new", 1, (n_seqs + 1,))
     _index_tensor(page_table, "page_table", 2)
-    if page_table.shape[0] != n_seqs:
+    rows, cols = page_table.shape
+    if rows != n_seqs:
         raise ValueError("page_table must have a row for every sequence")
-    num_pages, page_size, H_kv, D = k_pages.shape
-    return PagedDesc(T=T, n_seqs=n_seqs, H=H, H_kv=H_kv, D=D, num_pages=num_pages,
-                     page_size=page_size, max_pages=page_table.shape[1],
-                     page_stride=k_pages.stride(0), token_stride=k_pages.stride(1),
-                     head_stride=k_pages.stride(2),
-                     table_stride=page_table.stride(0) if n_seqs > 1 else page_table.shape[1],
-                     page_table=page_table.data_ptr(), cu_new=cu_new.data_ptr(),
-                     kv_lens=kv_lens.data_ptr(), dtype=code, causal=int(bool(causal)))
+    return PagedDesc(T, n_seqs, H, shape[2], shape[3], shape[0], shape[1], cols, stride[0],
+                     stride[1], stride[2], page_table.stride(0) if n_seqs > 1 else cols,
+                     page_table.data_ptr(), cu_new.data_ptr(), kv_lens.data_ptr(), code, causal)
 
 
 def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
@@ -920,27 +928,28 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
         raise ValueError("q_out must be shaped and typed like q")
     d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T,
                     q.shape[1] if q is not None else 0, 0)
-    s = _on(device, stream)
-    with torch.cuda.device(device), torch.cuda.stream(s):
-        if q is not None and q_out is None:
-            q_out = torch.zeros(q.shape, dtype=q.dtype, device=device)
-        if T == 0:
-            return q_out
-        st = [_token_stride(t, n, 3) if t is not None else 0
-              for n, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out))]
-        _call("paged_kv_append", ctypes.byref(d),
-              ctypes.byref(rope._c()) if rope is not None else None, _ptr(q), st[0], _ptr(k), st[1],
-              _ptr(v), st[2], _ptr(q_out), st[3], _ptr(k_pages), _ptr(v_pages), _stream(s))
-    return q_out
+
+    def body(s):
+        qo = q_out
+        qs = qos = 0
+        if q is not None:
+            if qo is None:
+                qo = torch.zeros(q.shape, dtype=q.dtype, device=device)
+            qs, qos = _token_stride(q, "q", 3), _token_stride(qo, "q_out", 3)
+        if T > 0:
+            _call_fast("paged_kv_append", ctypes.byref(d), rope._c if rope is not None else None,
+                       _addr(q), qs, k.data_ptr(), _token_stride(k, "k", 3), v.data_ptr(),
+                       _token_stride(v, "v", 3), _addr(qo), qos, k_pages.data_ptr(),
+                       v_pages.data_ptr(), s)
+        return qo
+
+    return _launch_on(device, stream, body)
 
 
 def paged_attn_workspace(D: int, dtype=torch.bfloat16, device=None):
     """A zeroed workspace for paged_attn_fwd, of a size that depends only on the head dim and
     type: keep one per stream (calls that share one must not overlap on the GPU)."""
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("dtype must be bf16 or fp32")
-    n = int(load_library().paged_attn_workspace_bytes(
-        D, RA_BF16 if dtype == torch.bfloat16 else RA_F32))
+    n = int(load_library().paged_attn_workspace_bytes(D, _float_code(dtype, "dtype")))
     if n == 0:
         raise ValueError(f"no paged attention for head dim {D} in {dtype}")
     dev = torch.device(device) if device is not None else torch.device(
@@ -959,25 +968,26 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
     if q.dim() != 3 or q.dtype != k_pages.dtype or q.shape[2] != k_pages.shape[-1]:
         raise ValueError("q must be [T, H, D] with the head dim and dtype of the pages")
     T, H, D = q.shape
-    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal)
-    for name, t, shape, dtype in (("out", out, (T, H, D), q.dtype),
-                                  ("lse", lse, (T, H), torch.float32)):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
-    s = _on(device, stream)
-    with torch.cuda.device(device), torch.cuda.stream(s):
-        if out is None:
-            out = torch.zeros((T, H, D), dtype=q.dtype, device=device)
-        if lse is None and want_lse:
-            lse = torch.zeros((T, H), dtype=torch.float32, device=device)
-        if workspace is None:
-            workspace = paged_attn_workspace(D, q.dtype, device)
-        if T == 0:
-            return out, lse
-        _call("paged_attn_fwd", ctypes.byref(d), _ptr(q), _token_stride(q, "q", 3), _ptr(k_pages),
-              _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(workspace),
-              workspace.numel() * workspace.element_size(), _stream(s))
-    return out, lse
+    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, 1 if causal else 0)
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous()):
+        raise ValueError("out must be contiguous and shaped and typed like q")
+    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [T, H] tensor")
+
+    def body(s):
+        o = torch.zeros((T, H, D), dtype=q.dtype, device=device) if out is None else out
+        ls = lse
+        if ls is None and want_lse:
+            ls = torch.zeros((T, H), dtype=torch.float32, device=device)
+        if T > 0:
+            ws = workspace if workspace is not None else paged_attn_workspace(D, q.dtype, device)
+            _call_fast("paged_attn_fwd", ctypes.byref(d), q.data_ptr(), _token_stride(q, "q", 3),
+                       k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(), _addr(ls),
+                       ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        return o, ls
+
+    return _launch_on(device, stream, body)
 
 
 def check_status(stream=None) -> int:

@@ -322,19 +322,12 @@ template <int D>
 cudaError_t launch_d(PagedParams& p)
 {
     const PagedArgs& a = p.a;
-    static std::atomic<int> configured[kMaxDevices];
-    int dev = 0, sms = 148, per_sm = 1;
-    cudaError_t e = cudaGetDevice(&dev);
+    static std::atomic<int> known[kMaxDevices];
+    int grid = 0;
+    const cudaError_t e =
+        resident_ctas(known, paged_bf16_kernel<D>, kThreads, Smem<D>::kBytes, &grid);
     if (e != cudaSuccess) return e;
-    e = smem_limit_once(configured, dev, paged_bf16_kernel<D>, Smem<D>::kBytes);
-    if (e != cudaSuccess) return e;
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_bf16_kernel<D>, kThreads,
-                                                      Smem<D>::kBytes);
-    if (e != cudaSuccess) return e;
-    long long grid = static_cast<long long>(sms) * (per_sm > 0 ? per_sm : 1);
-    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
-    p.grid = static_cast<int>(grid);
+    p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.min_chunk = 2 * kUnit;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, D);
@@ -342,7 +335,7 @@ cudaError_t launch_d(PagedParams& p)
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
-    paged_bf16_kernel<D><<<static_cast<unsigned>(grid), kThreads, Smem<D>::kBytes, a.stream>>>(p);
+    paged_bf16_kernel<D><<<p.grid, kThreads, Smem<D>::kBytes, a.stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -200,17 +200,12 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     PagedParams p;
     p.a = a;
     p.G = a.H / a.H_kv;
-    int dev = 0, sms = 148, per_sm = 1;
-    cudaError_t e = cudaGetDevice(&dev);
+    static std::atomic<int> known1[kMaxDevices], known2[kMaxDevices];
+    int grid = 0;
+    const cudaError_t e = a.D <= 128 ? resident_ctas(known1, paged_simt_kernel<1>, kThreads, 0, &grid)
+                                     : resident_ctas(known2, paged_simt_kernel<2>, kThreads, 0, &grid);
     if (e != cudaSuccess) return e;
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    e = a.D <= 128
-            ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_simt_kernel<1>, kThreads, 0)
-            : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_simt_kernel<2>, kThreads, 0);
-    if (e != cudaSuccess) return e;
-    long long grid = static_cast<long long>(sms) * (per_sm > 0 ? per_sm : 1);
-    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
-    p.grid = static_cast<int>(grid);
+    p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.min_chunk = 4 * kUnit;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.D));
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -219,9 +214,9 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
     if (a.D <= 128)
-        paged_simt_kernel<1><<<static_cast<unsigned>(grid), kThreads, 0, a.stream>>>(p);
+        paged_simt_kernel<1><<<p.grid, kThreads, 0, a.stream>>>(p);
     else
-        paged_simt_kernel<2><<<static_cast<unsigned>(grid), kThreads, 0, a.stream>>>(p);
+        paged_simt_kernel<2><<<p.grid, kThreads, 0, a.stream>>>(p);
     return cudaGetLastError();
 }
 

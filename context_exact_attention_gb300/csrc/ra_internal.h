@@ -28,6 +28,30 @@ cudaError_t smem_limit_once(std::atomic<int>* done, int dev, Kernel kernel, int 
     return e;
 }
 
+// CTAs of a kernel that the current device holds at once (SMs times resident CTAs), asked
+// once per device: `known` is one value per device (static storage: 0, not asked yet).  Also
+// raises the kernel's dynamic shared-memory limit to `bytes`.
+template <typename Kernel>
+cudaError_t resident_ctas(std::atomic<int>* known, Kernel kernel, int threads, int bytes, int* ctas)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    *ctas = known[dev].load(std::memory_order_acquire);
+    if (*ctas > 0) return cudaSuccess;
+    int sms = 0, per_sm = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, bytes);
+    if (e != cudaSuccess) return e;
+    *ctas = sms * (per_sm > 0 ? per_sm : 1);
+    known[dev].store(*ctas, std::memory_order_release);
+    return cudaSuccess;
+}
+
 // Everything one attention launch needs; validated by the ABI layer.
 struct AttnArgs {
     const void* q;
