@@ -266,6 +266,26 @@ ra_status permute_impl(const void* in, void* out, int B, int L, int H, int D, in
 }  // namespace
 
 namespace ra {
+
+bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const unsigned long long* dims,
+                     const unsigned long long* strides, const unsigned int* box)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5];
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        if (i > 0) st[i - 1] = strides[i - 1];
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+              const_cast<void*>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 __global__ void wait_probe_kernel(unsigned int* status, unsigned long long timeout_ns)

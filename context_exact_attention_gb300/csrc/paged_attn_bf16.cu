@@ -85,7 +85,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedParams p)
 {
     using S = Smem<D>;
-    using Walk = PagedWalk<FlatTiles<kRows>, kRows, kUnit>;
+    using Walk = PagedWalk<FlatTiles<kRows>, kUnit>;
     constexpr int kStages = S::kStages;
     constexpr int kChunks = D / 8;                            // 16-byte chunks per key
     constexpr int kRowsPerCopy = 32 / kChunks;                // keys one warp-wide copy covers
@@ -353,12 +353,16 @@ cudaError_t launch_paged_bf16(const PagedArgs& a)
 
 cudaError_t launch_paged(const PagedArgs& a)
 {
-    return a.elem == 2 ? launch_paged_bf16(a) : launch_paged_simt(a);
+    if (a.elem != 2) return launch_paged_simt(a);
+    return paged_tc_applies(a) ? launch_paged_tc(a) : launch_paged_bf16(a);
 }
 
 unsigned long long paged_workspace_bytes(int D, int elem)
 {
-    return paged_workspace_of(kPagedMaxCtas, elem == 2 ? kRows : 4, D).total;
+    if (elem != 2) return paged_workspace_of(kPagedMaxCtas, 4, D).total;
+    const unsigned long long few = paged_workspace_of(kPagedMaxCtas, kRows, D).total;
+    const unsigned long long many = paged_workspace_of(kPagedTcCtas, 256, D).total;
+    return few > many ? few : many;
 }
 
 }  // namespace ra

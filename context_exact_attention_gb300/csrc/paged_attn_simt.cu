@@ -30,7 +30,7 @@ __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpr
 template <int kVec4>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams p)
 {
-    using Walk = PagedWalk<FlatTiles<kRows>, kRows, kUnit>;
+    using Walk = PagedWalk<FlatTiles<kRows>, kUnit>;
     __shared__ long long scratch[34];
     __shared__ float2 stat_w[kWarps][kRows];
     __shared__ float2 stat[kRows];

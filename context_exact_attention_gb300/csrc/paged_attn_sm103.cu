@@ -1,0 +1,747 @@
+// paged_attn_sm103.cu -- paged_attn_fwd for calls with many query rows per key/value head
+// (chunks of prompts, mixed batches), bf16 on the tensor cores (tcgen05 + TMEM + TMA).
+//
+// One persistent CTA per SM takes its part of the call's tiles (paged_plan.cuh).  A tile is
+// two 128-row query sub-tiles of one key/value head: 128 / G tokens with the G query heads
+// that read the head, token-major, so that every key block loaded into shared memory serves
+// all of them.  The roles are those of the dense forward (attn_bf16_sm103.cu):
+//   warp 0      producer: walks the CTA's segments, publishes each to the other warps
+//               through a two-slot ring in shared memory, and loads the query sub-tiles
+//               and the 128-key blocks of K and V by TMA, one box per page (one lane each,
+//               the page-table entries fetched a block ahead);
+//   warp 1      issues S_t = Q_t K^T and O_t += P_t V;
+//   warps 4-7, 8-11  softmax of sub-tile 0, 1: one thread per row.
+// The sub-tiles ping-pong, and the next segment's loads and first products overlap the
+// output of the last.  A tile with no more than one sub-tile of rows runs that one alone.
+//
+// A box of a page that the table does not name properly, or of a page behind the last key,
+// is loaded at an index outside the tensor, which TMA fills with zeros without reading
+// memory.  Slots behind the last key in its page hold whatever they hold: their scores are
+// masked, and their rows of V are zeroed in shared memory before the product (0 times NaN
+// is NaN), which only the last block of a sequence needs.
+//
+// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D).
+#include <cuda.h>
+
+#include "paged_plan.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kSub = 128;         // rows of a sub-tile = TMEM lanes
+constexpr int kKeys = 128;        // keys per block
+constexpr int kThreads = 384;
+constexpr int kReaders = 1 + 8;   // warps that read a published segment
+constexpr float kRescaleThreshold = 8.0f;
+
+template <int D>
+struct Layout {
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kTile = 128 * D * 2;
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + 2 * kTile;
+    static constexpr int kV = kK + 2 * kTile;
+    static constexpr int kStage = kV + 2 * kTile;     // 8 warps x 32 rows x D/2 bf16
+    static constexpr int kBar = kStage + kTile;
+    static constexpr int kSmem = kBar + 1024 + 1024;  // barriers, scratch; alignment slack
+    __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
+    __device__ static constexpr uint32_t col_o(int t) { return 256u + static_cast<uint32_t>(D) * t; }
+};
+
+enum : int {
+    kBarQ = 0,           // +sub-tile: queries loaded
+    kBarQEmpty = 2,      // +sub-tile: the segment's last Q K^T of the sub-tile finished
+    kBarKFull = 4,       // +stage
+    kBarKEmpty = 6,      // +stage
+    kBarVFull = 8,       // +stage
+    kBarVEmpty = 10,     // +stage
+    kBarSFull = 12,      // +sub-tile
+    kBarPFull = 14,      // +2 sub-tile + half
+    kBarOFull = 18,      // +sub-tile
+    kBarSegFull = 20,    // +slot
+    kBarSegEmpty = 22,   // +slot
+    kBarPart = 24,       // the eight softmax warps have written their partials
+    kBarFlag = 25,       // whether this CTA joins them is known
+    kBarDone = 26,
+    kBarCount = 27
+};
+// shared-memory words after the barriers
+constexpr int kTmemSlot = kBarCount * 8, kAbort = kTmemSlot + 4, kLast = kTmemSlot + 8;
+constexpr int kSegInts = 14;
+constexpr int kSegSlots = kTmemSlot + 16;                   // 2 slots of kSegInts ints
+constexpr int kScratch = (kSegSlots + 2 * kSegInts * 4 + 7) / 8 * 8;
+static_assert(kScratch + 34 * 8 <= 1024, "barrier area");
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, int c2, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
+}
+
+// What the other warps need of a segment.
+struct Seg {
+    int hk, rows, n_sub, first, n, kv, k0, n_blocks, c_first, c_last;
+    long long row0;
+};
+__device__ __forceinline__ void publish(volatile int* e, int more, const Seg& s)
+{
+    e[0] = more;
+    e[1] = s.hk;
+    e[2] = s.rows;
+    e[3] = s.n_sub;
+    e[4] = s.first;
+    e[5] = s.n;
+    e[6] = s.kv;
+    e[7] = s.k0;
+    e[8] = s.n_blocks;
+    e[9] = s.c_first;
+    e[10] = s.c_last;
+    e[11] = static_cast<int>(s.row0);          // T * H < 2^31
+}
+__device__ __forceinline__ bool consume(volatile int* e, Seg& s)
+{
+    s.hk = e[1];
+    s.rows = e[2];
+    s.n_sub = e[3];
+    s.first = e[4];
+    s.n = e[5];
+    s.kv = e[6];
+    s.k0 = e[7];
+    s.n_blocks = e[8];
+    s.c_first = e[9];
+    s.c_last = e[10];
+    s.row0 = e[11];
+    return e[0] != 0;
+}
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                    const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, const PagedParams p)
+{
+    using Lay = Layout<D>;
+    using Walk = PagedWalk<StepTiles, kKeys>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_addr(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
+    const uint32_t sbase = smem_addr(smem);
+    uint8_t* area = smem + Lay::kBar;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(area + kTmemSlot);
+    int* abort_flag = reinterpret_cast<int*>(area + kAbort);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(area + kLast);
+    volatile int* seg_slot = reinterpret_cast<volatile int*>(area + kSegSlots);
+    long long* scratch = reinterpret_cast<long long*>(area + kScratch);
+    auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
+    const PagedArgs& a = p.a;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int sub_tokens = p.tile_tokens / 2;
+    const int sub_rows = sub_tokens * p.G;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarQ + i), 1);
+            mbar_init(bar(kBarQEmpty + i), 1);
+            mbar_init(bar(kBarKFull + i), 1);
+            mbar_init(bar(kBarKEmpty + i), 1);
+            mbar_init(bar(kBarVFull + i), 1);
+            mbar_init(bar(kBarVEmpty + i), 1);
+            mbar_init(bar(kBarSFull + i), 1);
+            mbar_init(bar(kBarPFull + 2 * i), kSub);
+            mbar_init(bar(kBarPFull + 2 * i + 1), kSub);
+            mbar_init(bar(kBarOFull + i), 1);
+            mbar_init(bar(kBarSegFull + i), 1);
+            mbar_init(bar(kBarSegEmpty + i), kReaders);
+        }
+        mbar_init(bar(kBarPart), 8);
+        mbar_init(bar(kBarFlag), 1);
+        mbar_init(bar(kBarDone), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    Walk walk;
+    walk.begin<kThreads>(p, scratch);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    WaitCtx wc{abort_flag, a.status, a.timeout_ns};
+
+    // The i-th segment of this CTA, as the consumer warps get it (false: no more).
+    auto get_seg = [&](int i, Seg& s) -> bool {
+        const int slot = i & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarSegFull + slot), (i >> 1) & 1, wc)))
+            return false;
+        const bool more = consume(seg_slot + kSegInts * slot, s);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarSegEmpty + slot));
+        return more;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        const bool leader = elect_one();
+        if (leader) {
+            tma_prefetch_desc(&tmap_q);
+            tma_prefetch_desc(&tmap_k);
+            tma_prefetch_desc(&tmap_v);
+        }
+        const uint64_t keep = l2_policy_evict_last();
+        const uint64_t once = l2_policy_evict_first();
+        const int box_rows = min(a.page_size, kKeys);
+        const int n_boxes = kKeys / box_rows;                 // pages a block touches, at most 16
+        // lane: box lane / kBoxes of the block's pages, columns 64 (lane mod kBoxes)
+        const int my_box = lane / Lay::kBoxes, my_col = lane % Lay::kBoxes;
+        const bool loads = my_box < n_boxes;
+        uint32_t N = 0;                                       // blocks loaded so far
+        uint32_t q_loads[2] = {0, 0};                         // query loads per sub-tile so far
+        int last_k[2] = {-1, -1}, last_v[2] = {-1, -1};
+        bool ok = true;
+        Segment t;
+        for (int i = 0; ok; ++i) {
+            const bool more = walk.next(p, t);
+            Seg s{};
+            if (more) {
+                s.hk = t.hk;
+                s.rows = t.rows;
+                s.n_sub = t.rows > sub_rows ? 2 : 1;
+                s.first = t.s.first;
+                s.n = t.s.n;
+                s.kv = t.s.kv;
+                s.k0 = t.k0;
+                s.n_blocks = t.k1 > t.k0 ? (t.k1 - t.k0 + kKeys - 1) / kKeys : 0;
+                s.c_first = t.c_first;
+                s.c_last = t.c_last;
+                s.row0 = t.row0;
+            }
+            const int slot = i & 1;
+            if (i >= 2 &&
+                !(ok = __all_sync(0xffffffffu,
+                                  mbar_wait(bar(kBarSegEmpty + slot), ((i - 2) >> 1) & 1, wc))))
+                break;
+            if (leader) {
+                publish(seg_slot + kSegInts * slot, more, s);
+                mbar_arrive(bar(kBarSegFull + slot));
+            }
+            __syncwarp();
+            if (!more) break;
+            if (s.n_blocks == 0) continue;
+            const int tok0 = t.s.first + static_cast<int>(t.row0 / p.G);
+            for (int tq = 0; tq < s.n_sub && ok; ++tq) {
+                if (q_loads[tq] > 0 &&
+                    !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQEmpty + tq),
+                                                             (q_loads[tq] - 1) & 1, wc))))
+                    break;
+                if (leader) {
+                    mbar_arrive_expect_tx(bar(kBarQ + tq), sub_rows * D * 2);
+                    for (int bx = 0; bx < Lay::kBoxes; ++bx)
+                        tma_load_3d(sbase + Lay::kQ + tq * Lay::kTile + bx * 16384, &tmap_q,
+                                    bar(kBarQ + tq), bx * 64, s.hk * p.G, tok0 + tq * sub_tokens, once);
+                }
+                ++q_loads[tq];
+                __syncwarp();
+            }
+            // page and slot of this lane's box of the block at key kb: an index outside the
+            // cache (zeros) behind the last key and for an entry that names no page
+            auto page_of = [&](int kb) -> int {
+                const int key = kb + my_box * box_rows;
+                int page = -1;
+                if (loads && key < s.kv)
+                    page = checked_ldg(a.page_table, t.g * a.table_stride + key / a.page_size,
+                                       a.table_elems, a.status);
+                return static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages) ? page
+                                                                                      : a.num_pages;
+            };
+            int page = page_of(s.k0);
+            for (int n = 0; n < s.n_blocks && ok; ++n) {
+                const int kb = s.k0 + n * kKeys;
+                const int in_page = a.page_size > kKeys ? kb % a.page_size : 0;
+                const int page_next = n + 1 < s.n_blocks ? page_of(kb + kKeys) : 0;
+                const uint32_t Nn = N + n;
+                const int st = Nn & 1;
+                const uint32_t ph = (Nn >> 1) & 1;
+                const uint32_t to = my_col * 16384 + my_box * box_rows * 128;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarKEmpty + st), ph ^ 1, wc)))) break;
+                if (leader) mbar_arrive_expect_tx(bar(kBarKFull + st), Lay::kTile);
+                __syncwarp();
+                if (loads)
+                    tma_load_4d(sbase + Lay::kK + st * Lay::kTile + to, &tmap_k, bar(kBarKFull + st),
+                                my_col * 64, s.hk, in_page, page, keep);
+                last_k[st] = static_cast<int>(Nn);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarVEmpty + st), ph ^ 1, wc)))) break;
+                if (leader) mbar_arrive_expect_tx(bar(kBarVFull + st), Lay::kTile);
+                __syncwarp();
+                if (loads)
+                    tma_load_4d(sbase + Lay::kV + st * Lay::kTile + to, &tmap_v, bar(kBarVFull + st),
+                                my_col * 64, s.hk, in_page, page, keep);
+                last_v[st] = static_cast<int>(Nn);
+                page = page_next;
+            }
+            N += s.n_blocks;
+        }
+        // let this CTA's own copies land before anyone leaves
+        for (int tq = 0; tq < 2; ++tq)
+            if (q_loads[tq] > 0) mbar_wait_drain(bar(kBarQ + tq), (q_loads[tq] - 1) & 1, wc);
+        for (int st = 0; st < 2; ++st) {
+            if (last_k[st] >= 0) mbar_wait_drain(bar(kBarKFull + st), (last_k[st] >> 1) & 1, wc);
+            if (last_v[st] >= 0) mbar_wait_drain(bar(kBarVFull + st), (last_v[st] >> 1) & 1, wc);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMA issuer
+        const bool leader = elect_one();
+        constexpr uint32_t kIdescQK = idesc_bf16_f32(kSub, kKeys, false);
+        constexpr uint32_t kIdescPV = idesc_bf16_f32(kSub, D, true);
+        constexpr uint64_t kTileU = Lay::kTile >> 4;
+        const uint64_t dq = sdesc_sw128(sbase + Lay::kQ, 16, 1024);
+        const uint64_t dk = sdesc_sw128(sbase + Lay::kK, 16, 1024);
+        const uint64_t dv = sdesc_sw128(sbase + Lay::kV, 16384, 1024);
+        auto issue_qk = [&](int tq, int st) {
+            const uint32_t d_t = tmem + Lay::col_s(tq);
+            const uint64_t a0 = dq + tq * kTileU, b0 = dk + st * kTileU;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                mma_ss(d_t, a0 + off, b0 + off, kIdescQK, k > 0 ? 1u : 0u);
+            }
+        };
+        auto issue_pv = [&](int tq, int st, int half, bool acc) {
+            const uint32_t d_t = tmem + Lay::col_o(tq);
+            const uint32_t pa = tmem + Lay::col_s(tq) + 32 * half;
+            const uint64_t b0 = dv + st * kTileU + ((half * 64 * 128) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_ts(d_t, pa + k * 8, b0 + ((k * 2048) >> 4), kIdescPV, (acc || k > 0) ? 1u : 0u);
+        };
+        auto wait_all = [&](int idx, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar(idx), parity, wc));
+        };
+        // rows of V behind the last key of the sequence become zeros
+        auto zero_tail = [&](int st, int from) {
+            uint8_t* v = smem + Lay::kV + st * Lay::kTile;
+            for (int i = lane; i < (kKeys - from) * 8 * Lay::kBoxes; i += 32) {
+                const int r = i / (8 * Lay::kBoxes), c = i % (8 * Lay::kBoxes);
+                *reinterpret_cast<uint4*>(v + (c >> 3) * 16384 + (from + r) * 128 + (c & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
+        uint32_t N = 0;
+        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};     // query loads; blocks of each sub-tile
+        bool ok = true;
+        Seg s;
+        for (int i = 0; ok; ++i) {
+            if (!get_seg(i, s)) break;
+            if (s.n_blocks == 0) continue;
+            const bool two = s.n_sub == 2;
+            const int st0 = N & 1;
+            ok = wait_all(kBarQ, qn[0] & 1) && wait_all(kBarKFull + st0, (N >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+                issue_qk(0, st0);
+                tc_commit(bar(kBarSFull + 0));
+                if (s.n_blocks == 1) tc_commit(bar(kBarQEmpty + 0));
+                if (!two) tc_commit(bar(kBarKEmpty + st0));
+            }
+            __syncwarp();
+            ++qn[0];
+            if (two) {
+                if (!(ok = wait_all(kBarQ + 1, qn[1] & 1))) break;
+                tc_fence_after();
+                if (leader) {
+                    issue_qk(1, st0);
+                    tc_commit(bar(kBarSFull + 1));
+                    if (s.n_blocks == 1) tc_commit(bar(kBarQEmpty + 1));
+                    tc_commit(bar(kBarKEmpty + st0));
+                }
+                __syncwarp();
+                ++qn[1];
+            }
+            for (int n = 0; n < s.n_blocks; ++n) {
+                const uint32_t Nn = N + n;
+                const int st = Nn & 1;
+                const uint32_t ph = (Nn >> 1) & 1;
+                const bool more = n + 1 < s.n_blocks;
+                const bool last_qk = n + 2 == s.n_blocks;
+                const int st1 = (Nn + 1) & 1;
+                const uint32_t ph1 = ((Nn + 1) >> 1) & 1;
+                const int held = s.kv - (s.k0 + n * kKeys);       // keys of the block that exist
+                if (held < kKeys) {
+                    if (!(ok = wait_all(kBarVFull + st, ph))) break;
+                    zero_tail(st, max(held, 0));
+                }
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait2(bar(kBarVFull + st), ph,
+                                                              bar(kBarPFull + 0), pn[0] & 1, wc))))
+                    break;
+                tc_fence_after();
+                if (leader) issue_pv(0, st, 0, n > 0);
+                __syncwarp();
+                ok = more ? mbar_wait2(bar(kBarPFull + 1), pn[0] & 1, bar(kBarKFull + st1), ph1, wc)
+                          : mbar_wait(bar(kBarPFull + 1), pn[0] & 1, wc);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                if (leader) {
+                    issue_pv(0, st, 1, true);
+                    if (!two) tc_commit(bar(kBarVEmpty + st));
+                    if (!more) tc_commit(bar(kBarOFull + 0));
+                    if (more) {
+                        issue_qk(0, st1);
+                        tc_commit(bar(kBarSFull + 0));
+                        if (last_qk) tc_commit(bar(kBarQEmpty + 0));
+                        if (!two) tc_commit(bar(kBarKEmpty + st1));
+                    }
+                }
+                __syncwarp();
+                ++pn[0];
+                if (!two) continue;
+                if (!(ok = wait_all(kBarPFull + 2, pn[1] & 1))) break;
+                tc_fence_after();
+                if (leader) issue_pv(1, st, 0, n > 0);
+                __syncwarp();
+                if (!(ok = wait_all(kBarPFull + 3, pn[1] & 1))) break;
+                tc_fence_after();
+                if (leader) {
+                    issue_pv(1, st, 1, true);
+                    tc_commit(bar(kBarVEmpty + st));
+                    if (!more) tc_commit(bar(kBarOFull + 1));
+                    if (more) {
+                        issue_qk(1, st1);
+                        tc_commit(bar(kBarSFull + 1));
+                        if (last_qk) tc_commit(bar(kBarQEmpty + 1));
+                        tc_commit(bar(kBarKEmpty + st1));
+                    }
+                }
+                __syncwarp();
+                ++pn[1];
+            }
+            N += s.n_blocks;
+        }
+        // every MMA this CTA issued has finished before TMEM is released
+        if (leader) tc_commit(bar(kBarDone));
+        __syncwarp();
+        mbar_wait_drain(bar(kBarDone), 0, wc);
+        __syncwarp();
+    } else if (warp >= 4) {
+        // -------------------------------------------------------------- softmax
+        const int tq = (warp - 4) >> 2;
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;                   // within the sub-tile
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_off + Lay::col_s(tq);
+        const uint32_t tO = tmem + lane_off + Lay::col_o(tq);
+        const float sl2 = p.scale_log2;
+        const int part_row = tq * kSub + row;                  // row in a partial result
+        uint32_t sn = 0;                                       // S tiles seen by this sub-tile
+        uint32_t on = 0;                                       // finished outputs of it
+        uint32_t splits = 0;                                   // split segments of the CTA
+        bool ok = true;
+        Seg s;
+        for (int i = 0; ok; ++i) {
+            if (!get_seg(i, s)) break;
+            const bool active = tq < s.n_sub;
+            const int in_tile = tq * sub_rows + row;           // packed row within the tile
+            const bool valid = row < sub_rows && in_tile < s.rows;
+            const int tok = static_cast<int>((s.row0 + in_tile) / p.G);    // within the sequence
+            const int head = static_cast<int>(s.row0 + in_tile - static_cast<long long>(tok) * p.G);
+            // keys that this row sees: [0, seen)
+            const int seen = !valid ? 0 : a.causal ? s.kv - s.n + tok + 1 : s.kv;
+            const int n_blocks = active ? s.n_blocks : 0;
+
+            float m = -INFINITY, l = 0.f;
+            for (int n = 0; n < n_blocks; ++n) {
+                ok = mbar_wait(bar(kBarSFull + tq), sn & 1, wc);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++sn;
+                tc_fence_after();
+
+                uint32_t sraw[128];
+                tmem_ld128(tS, sraw);
+                float sv[128];
+#pragma unroll
+                for (int c = 0; c < 128; ++c) sv[c] = u2f(sraw[c]);
+                const int lim = seen - (s.k0 + n * kKeys);     // columns [0, lim) are seen
+                if (lim < kKeys) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) sv[c] = c >= lim ? -INFINITY : sv[c];
+                }
+                float mx0 = fmaxf(sv[0], sv[1]), mx1 = fmaxf(sv[2], sv[3]);
+                float mx2 = fmaxf(sv[4], sv[5]), mx3 = fmaxf(sv[6], sv[7]);
+#pragma unroll
+                for (int c = 8; c < 128; c += 8) {
+                    mx0 = fmax3(mx0, sv[c], sv[c + 1]);
+                    mx1 = fmax3(mx1, sv[c + 2], sv[c + 3]);
+                    mx2 = fmax3(mx2, sv[c + 4], sv[c + 5]);
+                    mx3 = fmax3(mx3, sv[c + 6], sv[c + 7]);
+                }
+                const float m_blk = fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2;
+                const float m_new = fmaxf(m, m_blk);
+                const bool raise = m_new > m + kRescaleThreshold;
+                const float m_ref = raise ? m_new : m;
+                const float alpha = raise ? ex2(m - m_ref) : 1.f;
+                const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+                // weights 2^(s - m_ref), rounded to bf16 (the product's operand type) over S
+                // in two halves; the denominator is summed in fp32 before the rounding
+                const uint64_t scale2 = f2pack(sl2, sl2), negm2 = f2pack(neg_m, neg_m);
+                uint64_t sum_a = 0, sum_b = 0;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i2 = 0; i2 < 32; ++i2) {
+                        const int c = 64 * half + 2 * i2;
+                        float x0, x1;
+                        f2unpack(ffma2(f2pack(sv[c], sv[c + 1]), scale2, negm2), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        if (i2 & 1) sum_b = fadd2(sum_b, f2pack(p0, p1));
+                        else sum_a = fadd2(sum_a, f2pack(p0, p1));
+                        pk[i2] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st32(tS + 32 * half, pk);
+                    // O was last written by P V of the previous block, finished before this
+                    // block's S; it is rescaled before this block's P V accumulates into it
+                    if (half == 0 && n > 0 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + 32 * c, o);
+#pragma unroll
+                            for (int i2 = 0; i2 < 32; ++i2) o[i2] = f2u(u2f(o[i2]) * alpha);
+                            tmem_st32(tO + 32 * c, o);
+                        }
+                    }
+                    tc_fence_before();
+                    mbar_arrive(bar(kBarPFull + 2 * tq + half));
+                }
+                float sa0, sa1;
+                f2unpack(fadd2(sum_a, sum_b), sa0, sa1);
+                l = l * alpha + (sa0 + sa1);
+                m = m_ref;
+            }
+            if (!ok) break;
+            const bool empty = n_blocks == 0;
+            if (!empty) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarOFull + tq), on & 1, wc));
+                if (!ok) break;
+                ++on;
+                tc_fence_after();
+            }
+
+            // Output element offset of this thread's row, -1 for a row outside the tile.
+            const long long my_row =
+                valid ? static_cast<long long>(s.first + tok) * a.H + s.hk * p.G + head : -1;
+            bool write = true;          // whether this CTA writes the tile's output
+            bool joined = false;        // ... of several CTAs' partials
+            float M = m, L = l;
+            const int nc = s.c_last - s.c_first + 1;
+            const long long n_rows = 2ll * p.grid * 2 * kSub;  // rows of all partial slots
+            auto part_of = [&](int cta) -> long long {         // slot of a CTA's partial
+                return 2ll * cta + (cta == s.c_first ? 1 : 0);
+            };
+            if (nc > 1) {
+                // this CTA's partial: statistics by row, sums column by column (rows of a
+                // warp side by side)
+                const long long slot = part_of(blockIdx.x);
+                if (valid) {
+                    const long long r = slot * 2 * kSub + part_row;
+                    if (in_bounds(r, 1, n_rows, a.status))
+                        __stcg(reinterpret_cast<float2*>(p.part_stat) + r, make_float2(m, l));
+                }
+                if (!empty) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * c, o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const long long at = (slot * D + 32 * c + j) * 2 * kSub + part_row;
+                            if (valid && in_bounds(at, 1, n_rows * D, a.status))
+                                __stcg(p.part_o + at, u2f(o[j]));
+                        }
+                    }
+                }
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarPart));
+                if (warp == 4) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarPart), splits & 1, wc));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        int last = 0;
+                        __threadfence();
+                        if (in_bounds(s.c_first, 1, kPagedMaxCtas, a.status)) {
+                            last = atomicAdd(p.counters + s.c_first, 1u) ==
+                                   static_cast<unsigned>(nc - 1);
+                            if (last) p.counters[s.c_first] = 0;
+                        }
+                        *last_flag = last;
+                        mbar_arrive(bar(kBarFlag));
+                    }
+                    __syncwarp();
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarFlag), splits & 1, wc));
+                if (!ok) break;
+                ++splits;
+                write = joined = *last_flag != 0;
+                if (joined) {
+                    __threadfence();
+                    M = -INFINITY;
+                    L = 0.f;
+                    for (int c = 0; c < nc && valid; ++c) {
+                        const long long r = part_of(s.c_first + c) * 2 * kSub + part_row;
+                        if (in_bounds(r, 1, n_rows, a.status))
+                            M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(p.part_stat) + r).x);
+                    }
+                }
+            }
+            if (write && active) {
+                const long long n_elems = n_rows * D;
+                constexpr int kHalf = D / 2;
+                constexpr int kChunks = kHalf / 8;             // 16-byte chunks per staged row
+                constexpr int kRowsPerStore = 32 / kChunks;
+                uint8_t* stage = smem + Lay::kStage + (warp - 4) * 32 * (2 * kHalf);
+#pragma unroll 1
+                for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll 1
+                    for (int c = 0; c < kHalf / 32; ++c) {
+                        const int col = hh * kHalf + 32 * c;
+                        float o[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+                        if (joined) {
+                            L = 0.f;
+                            for (int k = 0; k < nc && valid; ++k) {
+                                const long long sl = part_of(s.c_first + k);
+                                const long long r = sl * 2 * kSub + part_row;
+                                if (!in_bounds(r, 1, n_rows, a.status)) continue;
+                                const float2 st =
+                                    __ldcg(reinterpret_cast<const float2*>(p.part_stat) + r);
+                                if (st.y == 0.f) continue;
+                                const float w = part_weight(st.x, st.y, M);
+                                L = fmaf(w, st.y, L);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    const long long at = (sl * D + col + j) * 2 * kSub + part_row;
+                                    if (in_bounds(at, 1, n_elems, a.status))
+                                        o[j] = fmaf(w, __ldcg(p.part_o + at), o[j]);
+                                }
+                            }
+                        } else if (!empty) {
+                            uint32_t raw[32];
+                            tmem_ld32(tO + col, raw);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = u2f(raw[j]);
+                        }
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            pk[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int sl = (4 * c + j) ^ (lane & (kChunks - 1));
+                            *reinterpret_cast<uint4*>(stage + lane * (2 * kHalf) + sl * 16) =
+                                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                        }
+                    }
+                    __syncwarp();
+                    const int part = lane / kChunks, cc = lane % kChunks;
+#pragma unroll
+                    for (int k = 0; k < 32 / kRowsPerStore; ++k) {
+                        const int rr = k * kRowsPerStore + part;
+                        const long long orow = __shfl_sync(0xffffffffu, my_row, rr);
+                        const uint4 val = *reinterpret_cast<const uint4*>(
+                            stage + rr * (2 * kHalf) + ((cc ^ (rr & (kChunks - 1))) * 16));
+                        const long long at = orow * D + hh * kHalf + cc * 8;
+                        if (orow >= 0 && in_bounds(at, 8, a.out_elems, a.status))
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at) = val;
+                    }
+                    __syncwarp();
+                }
+                if (valid && a.lse != nullptr && in_bounds(my_row, 1, a.lse_elems, a.status))
+                    a.lse[my_row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
+            }
+        }
+    }
+
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv)
+{
+    static std::atomic<int> known[kMaxDevices];
+    int grid = 0;
+    const cudaError_t e = resident_ctas(known, paged_tc_kernel<D>, kThreads, Layout<D>::kSmem, &grid);
+    if (e != cudaSuccess) return e;
+    p.grid = grid < kPagedTcCtas ? grid : kPagedTcCtas;
+    p.min_chunk = 2 * kKeys;
+    p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
+    const PagedWorkspace w = paged_workspace_of(p.grid, 2 * kSub, D);
+    uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
+    p.counters = reinterpret_cast<unsigned int*>(ws);
+    p.part_stat = reinterpret_cast<float*>(ws + w.stat);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
+    paged_tc_kernel<D><<<p.grid, kThreads, Layout<D>::kSmem, p.a.stream>>>(tq, tk, tv, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool paged_tc_applies(const PagedArgs& a)
+{
+    // A page must cover whole 8-row swizzle atoms of a 128-key block, or whole blocks, and a
+    // sub-tile at least one token.
+    const bool pages = a.page_size % 8 == 0 && (kKeys % a.page_size == 0 || a.page_size % kKeys == 0);
+    if (a.elem != 2 || !pages || a.H / a.H_kv > kSub) return false;
+    return static_cast<long long>(a.T) * (a.H / a.H_kv) > 16ll * a.n_seqs;
+}
+
+cudaError_t launch_paged_tc(const PagedArgs& a)
+{
+    PagedParams p;
+    p.a = a;
+    p.G = a.H / a.H_kv;
+    const int sub_tokens = kSub / p.G;
+    p.tile_tokens = 2 * sub_tokens;
+    using ull = unsigned long long;
+    const ull D = static_cast<ull>(a.D);
+    CUtensorMap tq, tk, tv;
+    const ull qd[3] = {D, static_cast<ull>(a.H), static_cast<ull>(a.T)};
+    const ull qs[2] = {2 * D, 2ull * a.q_stride};
+    const unsigned qb[3] = {64, static_cast<unsigned>(p.G), static_cast<unsigned>(sub_tokens)};
+    const ull kd[4] = {D, static_cast<ull>(a.H_kv), static_cast<ull>(a.page_size),
+                       static_cast<ull>(a.num_pages)};
+    // (a dimension of one entry never uses its stride, which need not be a valid one)
+    const ull ks[3] = {a.H_kv > 1 ? 2ull * a.head_stride : 2 * D,
+                       a.page_size > 1 ? 2ull * a.token_stride : 2 * D,
+                       a.num_pages > 1 ? 2ull * a.page_stride : 2 * D};
+    const unsigned kb[4] = {64, 1, static_cast<unsigned>(a.page_size < kKeys ? a.page_size : kKeys), 1};
+    if (!encode_bf16_map(&tq, a.q, 3, qd, qs, qb) || !encode_bf16_map(&tk, a.k_pages, 4, kd, ks, kb) ||
+        !encode_bf16_map(&tv, a.v_pages, 4, kd, ks, kb))
+        return cudaErrorInvalidValue;
+    if (a.D == 64) return launch_d<64>(p, tq, tk, tv);
+    if (a.D == 128) return launch_d<128>(p, tq, tk, tv);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace ra

@@ -33,6 +33,7 @@ struct PagedParams {
     int G;                  // query heads per key/value head
     int grid;
     int min_chunk;          // smallest part worth a CTA, in keys
+    int tile_tokens;        // new tokens of a tile (StepTiles)
     float scale_log2;       // log2(e) / sqrt(D): scores in base-2 units
     unsigned int* counters; // [kPagedMaxCtas], zero between calls
     float* part_stat;       // [2 grid][rows][2]: maximum, denominator
@@ -40,7 +41,7 @@ struct PagedParams {
 };
 
 // The workspace, in bytes: work counters, then the statistics and sums of two partial tiles
-// for every CTA.
+// for every CTA.  (rows packed rows of a tile; the sums lie as each kernel likes.)
 struct PagedWorkspace {
     unsigned long long stat, o, total;
 };
@@ -77,6 +78,7 @@ template <int kRows>
 struct FlatTiles {
     int n_tiles;
     long long cost;         // of one tile
+    __device__ __forceinline__ static int rows(const PagedParams&) { return kRows; }
     __device__ __forceinline__ void init(const PagedParams& p, const SeqSpan& s)
     {
         n_tiles = static_cast<int>((static_cast<long long>(s.n) * p.G + kRows - 1) / kRows);
@@ -84,6 +86,44 @@ struct FlatTiles {
     }
     __device__ __forceinline__ long long prefix(int j) const { return j * cost; }
     __device__ __forceinline__ int at(long long x) const { return static_cast<int>(x / cost); }
+};
+
+// The same where a sequence may have many tiles: under the causal rule tile j of `per` tokens
+// sees (up to) the keys before the new tokens and the first (j + 1) per of those, so a
+// sequence's costs form an arithmetic series, summed in closed form and searched by halving.
+struct StepTiles {
+    int n_tiles, per, n, kv, causal;
+    long long before;       // keys before the new tokens
+    __device__ __forceinline__ static int rows(const PagedParams& p) { return p.tile_tokens * p.G; }
+    __device__ __forceinline__ void init(const PagedParams& p, const SeqSpan& s)
+    {
+        per = p.tile_tokens;
+        n = s.n;
+        kv = s.kv;
+        causal = p.a.causal;
+        before = max(s.kv - s.n, 0);
+        n_tiles = (s.n + per - 1) / per;
+    }
+    __device__ __forceinline__ long long prefix(int j) const
+    {
+        if (!causal) return j * (static_cast<long long>(kTileCost) + kv);
+        // full tiles before j, and the last one, which ends with the last token
+        long long c = j * (kTileCost + before);
+        const long long full = j < n_tiles ? j : n_tiles - 1;
+        c += per * (full * (full + 1) / 2);
+        return j < n_tiles ? c : c + n;
+    }
+    __device__ __forceinline__ int at(long long x) const
+    {
+        if (!causal) return static_cast<int>(x / (static_cast<long long>(kTileCost) + kv));
+        int lo = 0, hi = n_tiles;               // prefix(lo) <= x < prefix(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix(mid) <= x) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    }
 };
 
 // One CTA's share of one tile.
@@ -99,7 +139,7 @@ struct Segment {
 
 // Walk over the segments of this CTA.  kUnit: keys per step of the kernel, to which cuts
 // inside a tile are rounded.
-template <typename Tiles, int kRows, int kUnit>
+template <typename Tiles, int kUnit>
 struct PagedWalk {
     long long x, end, chunk;
     long long seq0, seq_cost, head_cost;
@@ -138,9 +178,9 @@ struct PagedWalk {
         const long long a = seq0 + head0 + tiles.prefix(j), b = seq0 + head0 + tiles.prefix(j + 1);
         t.g = g;
         t.s = s;
-        t.row0 = static_cast<long long>(j) * kRows;
-        t.rows = static_cast<int>(min(static_cast<long long>(kRows),
-                                      static_cast<long long>(s.n) * p.G - t.row0));
+        const long long rows = Tiles::rows(p);
+        t.row0 = j * rows;
+        t.rows = static_cast<int>(min(rows, static_cast<long long>(s.n) * p.G - t.row0));
         // the last token of the tile sees the most keys
         const int last = static_cast<int>((t.row0 + t.rows - 1) / p.G);
         t.keys = p.a.causal ? min(max(s.kv - s.n + last + 1, 0), s.kv) : s.kv;

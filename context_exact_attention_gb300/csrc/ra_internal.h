@@ -218,10 +218,20 @@ struct PagedArgs {
 };
 // CTAs a call may launch (the workspace holds two partial results for each).
 constexpr int kPagedMaxCtas = 1024;
+constexpr int kPagedTcCtas = 160;     // of the tensor-core kernel (one per SM)
 unsigned long long paged_workspace_bytes(int D, int elem);
 cudaError_t launch_paged(const PagedArgs& a);        // chooses among:
 cudaError_t launch_paged_simt(const PagedArgs& a);   // fp32
-cudaError_t launch_paged_bf16(const PagedArgs& a);   // bf16
+cudaError_t launch_paged_bf16(const PagedArgs& a);   // bf16, few rows per key/value head
+// bf16, many rows: CTAs, and tensor maps of q ({D, H, T}, boxes of 64 x G x tokens) and of
+// the pages ({D, H_kv, page_size, num_pages}, boxes of 64 x 1 x min(page_size, 128) x 1).
+bool paged_tc_applies(const PagedArgs& a);
+cudaError_t launch_paged_tc(const PagedArgs& a);
+
+// bf16 tensor of `rank` dims (innermost first, strides in bytes of dims 1 and up) with boxes
+// of 64 innermost elements, 128-byte swizzle, zeros outside.  False if the driver refuses it.
+bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const unsigned long long* dims,
+                     const unsigned long long* strides, const unsigned int* box);
 
 // Device address of the current device's status word (api.cu).
 ra_status current_status_word(unsigned int** out);
