@@ -435,7 +435,7 @@ ra_status paged_attn_fwd(const ra_paged_desc* d, const void* q, long long q_stri
     if (d->H % d->H_kv != 0) return RA_ERR_NOT_DIVISIBLE;
     const long long nq = static_cast<long long>(d->H) * d->D;
     if (nq > 0x7fffffffll || static_cast<ull>(d->T) * nq >= kMaxElems ||
-        static_cast<ull>(d->T) * d->H > 0x7fffffffull)
+        static_cast<ull>(d->T) * d->H > 0x7fffff00ull)
         return RA_ERR_INVALID_ARG;
     if ((st = row_stride(&q_stride, nq, elem)) != RA_OK) return st;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||

@@ -82,7 +82,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedParams p)
+__global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_constant__ PagedParams p)
 {
     using S = Smem<D>;
     using Walk = PagedWalk<FlatTiles<kRows>, kUnit>;
@@ -103,41 +103,44 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedPara
     const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.q);
     const uint32_t ring = smem_addr(smem) + warp * 2 * S::kTile;
 
-    Walk walk;                                  // of the products
+    Walk walk;
     walk.begin<kThreads>(p, scratch);
-    // of the copies, ahead of it
-    Walk ahead = walk;
-    Segment lt;
-    int lk = 0;
-    bool more = true;
-    lt.k1 = 0;
+    Segment t{}, nt{};                          // the segment being multiplied, the next one
+    bool have = false, have_next = walk.next(p, nt);
+    // The copies: step `lk` of segment nt (in_next) or t, up to kStages steps ahead of the
+    // products.  They cross into the next segment but not beyond it.
+    bool in_next = true;
+    int lk = have_next ? nt.k0 : 0;
+    uint32_t issued = 0, used = 0;              // steps
     long long off = -1;                         // lane < 16: where the step's key lies
-    auto advance = [&]() {
-        lk += kUnit;
-        while (more && lk >= lt.k1) {
-            more = ahead.next(p, lt);
-            lk = lt.k0;
-        }
-        off = -1;
+    auto look_up = [&]() {
         const int key = lk + kKeysW * warp + lane;
-        if (more && lane < kKeysW && key < lt.k1) off = key_offset(a, lt.g, lt.hk, key);
+        const int k1 = in_next ? (have_next ? nt.k1 : 0) : t.k1;
+        off = -1;
+        if (lane < kKeysW && key < k1)
+            off = key_offset(p, in_next ? nt.g : t.g, in_next ? nt.hk : t.hk, key);
     };
-    auto issue = [&](int stage) {
-        if (more) {
-            const uint32_t dst = ring + stage * S::kStage;
+    auto loadable = [&]() { return lk < (in_next ? (have_next ? nt.k1 : 0) : t.k1); };
+    auto issue = [&]() {
+        const uint32_t dst = ring + (issued % kStages) * S::kStage;
 #pragma unroll
-            for (int j = 0; j < kKeysW / kRowsPerCopy; ++j) {
-                const int row = j * kRowsPerCopy + lane / kChunks, c = lane % kChunks;
-                const long long o = __shfl_sync(0xffffffffu, off, row);
-                const bool real = o >= 0 && in_bounds(o + 8 * c, 8, a.page_elems, a.status);
-                const long long at = real ? o + 8 * c : 0;
-                const uint32_t to = dst + row * (2 * D) + ((c ^ (row & 7)) << 4);
-                cp_async16(to, K + at, real);
-                cp_async16(to + S::kTile, V + at, real);
-            }
-            advance();
+        for (int j = 0; j < kKeysW / kRowsPerCopy; ++j) {
+            const int row = j * kRowsPerCopy + lane / kChunks, c = lane % kChunks;
+            const long long o = __shfl_sync(0xffffffffu, off, row);
+            const bool real = o >= 0 && in_bounds(o + 8 * c, 8, a.page_elems, a.status);
+            const long long at = real ? o + 8 * c : 0;
+            const uint32_t to = dst + row * (2 * D) + ((c ^ (row & 7)) << 4);
+            cp_async16(to, K + at, real);
+            cp_async16(to + S::kTile, V + at, real);
         }
         cp_async_commit();
+        ++issued;
+        lk += kUnit;
+        if (!in_next && lk >= t.k1) {
+            in_next = true;
+            lk = have_next ? nt.k0 : 0;
+        }
+        look_up();
     };
     // The query fragments of a segment: thread's rows lane / 4 and lane / 4 + 8, columns
     // 16 step + 2 (lane mod 4) and 8 further.
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedPara
             const int r = (lane >> 2) + 8 * h;
             long long at = -1;
             if (r < t.rows) {
-                const long long pr = t.row0 + r, tok = pr / p.G;
+                const int pr = t.row0 + r, tok = pr / p.G;
                 at = (t.s.first + tok) * a.q_stride +
                      static_cast<long long>(t.hk * p.G + (pr - tok * p.G)) * D + 2 * (lane & 3);
             }
@@ -164,17 +167,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedPara
         }
     };
 
-    lk = -kUnit;
-    advance();
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-    int st = 0;                                 // stage of the next step
-
-    Segment t;
-    bool have = walk.next(p, t);
-    uint32_t q[kSteps][4];
-    if (have) load_q(t, q);
-    while (have) {
+    look_up();
+    // Each turn moves on to the next segment, fetches its queries, finishes the segment
+    // before while they come, and walks its keys.
+#pragma unroll 1
+    for (;;) {
+        uint32_t q[kSteps][4];
+        if (have_next) load_q(nt, q);
+        if (have) finish_segment<__nv_bfloat16, kRows, kThreads>(p, t, buf, S::kLdo, stat, flag);
+        have = have_next;
+        if (!have) break;
+        t = nt;
+        have_next = walk.next(p, nt);
+        in_next = lk >= t.k1;
+        if (in_next) lk = have_next ? nt.k0 : 0;
+        look_up();
         float o[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
@@ -183,17 +190,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedPara
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         // keys that this thread's two rows see, and that every row of the tile sees
         auto seen_by = [&](int r) {
-            const int tok = static_cast<int>((t.row0 + r) / p.G);
+            const int tok = (t.row0 + r) / p.G;
             return a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
         };
         const int see0 = seen_by(lane >> 2), see1 = seen_by((lane >> 2) + 8);
         const int see_all = min(seen_by(0), t.k1);
         for (int k = t.k0; k < t.k1; k += kUnit) {
-            cp_async_wait<kStages - 2>();
+            // (every lane has read the step before, whose place in the ring is taken next)
             __syncwarp();
-            issue(st == 0 ? kStages - 1 : st - 1);
-            const uint32_t kt = ring + st * S::kStage, vt = kt + S::kTile;
-            st = st + 1 == kStages ? 0 : st + 1;
+#pragma unroll 1
+            while (issued - used < kStages && loadable()) issue();
+            if (issued - used == kStages) cp_async_wait<kStages - 1>();
+            else cp_async_wait<0>();
+            __syncwarp();
+            const uint32_t kt = ring + (used % kStages) * S::kStage, vt = kt + S::kTile;
+            ++used;
 
             float s[2][4] = {};
             {
@@ -265,11 +276,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedPara
                 }
             }
         }
-        // the next segment's queries are fetched while this one is finished
-        Segment nt;
-        const bool next = walk.next(p, nt);
-        if (next) load_q(nt, q);
-
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -295,12 +301,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedPara
             f[h] = part_weight(h ? m1 : m0, h ? l1 : l0, M);
             if (warp == 0 && (lane & 3) == 0) stat[r] = make_float2(M, L);
         }
+#pragma unroll 1
         for (int w = 0; w < kWarps; ++w) {
             if (warp == w) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
+                for (int h = 0; h < 2; ++h) {
+                    if ((h ? r1 : r0) >= t.rows) continue;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int i = 0; i < D / 8; ++i) {
                         float2* dst = reinterpret_cast<float2*>(
                             buf + (h ? r1 : r0) * S::kLdo + 8 * i + 2 * (lane & 3));
                         float2 x = w == 0 ? make_float2(0.f, 0.f) : *dst;
@@ -308,12 +316,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const PagedPara
                         x.y = fmaf(f[h], o[i][2 * h + 1], x.y);
                         *dst = x;
                     }
+                }
             }
             __syncthreads();
         }
-        finish_segment<__nv_bfloat16, kRows, kThreads>(p, t, buf, S::kLdo, stat, flag);
-        t = nt;
-        have = next;
     }
     cp_async_wait<0>();
 }
@@ -346,6 +352,7 @@ cudaError_t launch_paged_bf16(const PagedArgs& a)
     PagedParams p;
     p.a = a;
     p.G = a.H / a.H_kv;
+    p.page_shift = page_shift_of(a.page_size);
     if (a.D == 64) return launch_d<64>(p);
     if (a.D == 128) return launch_d<128>(p);
     return cudaErrorInvalidValue;

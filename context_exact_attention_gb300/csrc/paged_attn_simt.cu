@@ -28,7 +28,7 @@ constexpr int kUnit = kTurn * kWarps;
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
 template <int kVec4>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams p)
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedParams p)
 {
     using Walk = PagedWalk<FlatTiles<kRows>, kUnit>;
     __shared__ long long scratch[34];
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
                 q[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
                 o[r][u] = q[r][u];
                 if (r < t.rows && c < D) {
-                    const long long pr = t.row0 + r, tok = pr / p.G;
+                    const int pr = t.row0 + r, tok = pr / p.G;
                     const long long at = (t.s.first + tok) * a.q_stride +
                                          static_cast<long long>(t.hk * p.G + (pr - tok * p.G)) * D + c;
                     if (in_bounds(at, 4, a.q_elems, a.status)) q[r][u] = load4(Q + at);
@@ -67,13 +67,13 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
         const int my_row = lane & 3, my_key = lane >> 2;
         int seen = 0;
         if (my_row < t.rows) {
-            const int tok = static_cast<int>((t.row0 + my_row) / p.G);
+            const int tok = (t.row0 + my_row) / p.G;
             seen = a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
         }
         float m = -INFINITY, l = 0.f;      // of row my_row; l over this lane's keys only
         for (int k = t.k0 + kTurn * warp; k < t.k1; k += kUnit) {
             long long off = -1;
-            if (lane < kTurn && k + lane < t.k1) off = key_offset(a, t.g, t.hk, k + lane);
+            if (lane < kTurn && k + lane < t.k1) off = key_offset(p, t.g, t.hk, k + lane);
             float4 kk[kTurn][kVec4], vv[kTurn][kVec4];
 #pragma unroll
             for (int j = 0; j < kTurn; ++j) {
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
             }
             __syncthreads();
         }
-        finish_segment<float, kRows, kThreads>(p, t, &buf[0][0], kVec4 * 128, stat, &flag);
+        finish_segment<float, kRows, kThreads, kVec4>(p, t, &buf[0][0], kVec4 * 128, stat, &flag);
     }
 }
 
@@ -200,6 +200,7 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     PagedParams p;
     p.a = a;
     p.G = a.H / a.H_kv;
+    p.page_shift = page_shift_of(a.page_size);
     static std::atomic<int> known1[kMaxDevices], known2[kMaxDevices];
     int grid = 0;
     const cudaError_t e = a.D <= 128 ? resident_ctas(known1, paged_simt_kernel<1>, kThreads, 0, &grid)

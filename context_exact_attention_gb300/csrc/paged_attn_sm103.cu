@@ -67,7 +67,7 @@ enum : int {
 };
 // shared-memory words after the barriers
 constexpr int kTmemSlot = kBarCount * 8, kAbort = kTmemSlot + 4, kLast = kTmemSlot + 8;
-constexpr int kSegInts = 14;
+constexpr int kSegInts = 12;
 constexpr int kSegSlots = kTmemSlot + 16;                   // 2 slots of kSegInts ints
 constexpr int kScratch = (kSegSlots + 2 * kSegInts * 4 + 7) / 8 * 8;
 static_assert(kScratch + 34 * 8 <= 1024, "barrier area");
@@ -84,8 +84,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 
 // What the other warps need of a segment.
 struct Seg {
-    int hk, rows, n_sub, first, n, kv, k0, n_blocks, c_first, c_last;
-    long long row0;
+    int hk, rows, n_sub, first, n, kv, k0, n_blocks, c_first, c_last, row0;
 };
 __device__ __forceinline__ void publish(volatile int* e, int more, const Seg& s)
 {
@@ -100,7 +99,7 @@ __device__ __forceinline__ void publish(volatile int* e, int more, const Seg& s)
     e[8] = s.n_blocks;
     e[9] = s.c_first;
     e[10] = s.c_last;
-    e[11] = static_cast<int>(s.row0);          // T * H < 2^31
+    e[11] = s.row0;
 }
 __device__ __forceinline__ bool consume(volatile int* e, Seg& s)
 {
@@ -125,7 +124,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     const __grid_constant__ CUtensorMap tmap_k,
-                    const __grid_constant__ CUtensorMap tmap_v, const PagedParams p)
+                    const __grid_constant__ CUtensorMap tmap_v,
+                    const __grid_constant__ PagedParams p)
 {
     using Lay = Layout<D>;
     using Walk = PagedWalk<StepTiles, kKeys>;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (!more) break;
             if (s.n_blocks == 0) continue;
-            const int tok0 = t.s.first + static_cast<int>(t.row0 / p.G);
+            const int tok0 = t.s.first + t.row0 / p.G;
             for (int tq = 0; tq < s.n_sub && ok; ++tq) {
                 if (q_loads[tq] > 0 &&
                     !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQEmpty + tq),
@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool active = tq < s.n_sub;
             const int in_tile = tq * sub_rows + row;           // packed row within the tile
             const bool valid = row < sub_rows && in_tile < s.rows;
-            const int tok = static_cast<int>((s.row0 + in_tile) / p.G);    // within the sequence
-            const int head = static_cast<int>(s.row0 + in_tile - static_cast<long long>(tok) * p.G);
+            const int tok = (s.row0 + in_tile) / p.G;              // within the sequence
+            const int head = s.row0 + in_tile - tok * p.G;
             // keys that this row sees: [0, seen)
             const int seen = !valid ? 0 : a.causal ? s.kv - s.n + tok + 1 : s.kv;
             const int n_blocks = active ? s.n_blocks : 0;
@@ -721,6 +721,7 @@ cudaError_t launch_paged_tc(const PagedArgs& a)
     PagedParams p;
     p.a = a;
     p.G = a.H / a.H_kv;
+    p.page_shift = page_shift_of(a.page_size);
     const int sub_tokens = kSub / p.G;
     p.tile_tokens = 2 * sub_tokens;
     using ull = unsigned long long;

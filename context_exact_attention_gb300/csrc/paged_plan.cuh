@@ -34,6 +34,7 @@ struct PagedParams {
     int grid;
     int min_chunk;          // smallest part worth a CTA, in keys
     int tile_tokens;        // new tokens of a tile (StepTiles)
+    int page_shift;         // log2 of the page size, or -1
     float scale_log2;       // log2(e) / sqrt(D): scores in base-2 units
     unsigned int* counters; // [kPagedMaxCtas], zero between calls
     float* part_stat;       // [2 grid][rows][2]: maximum, denominator
@@ -54,6 +55,13 @@ inline PagedWorkspace paged_workspace_of(int ctas, int rows, int D)
     return w;
 }
 
+inline int page_shift_of(int page_size)
+{
+    int k = 0;
+    while ((1 << k) < page_size) ++k;
+    return (1 << k) == page_size ? k : -1;
+}
+
 // The new tokens and keys of sequence g, clamped to what the call's tensors hold.
 struct SeqSpan {
     int first, n;           // first token row, new tokens
@@ -72,6 +80,13 @@ __device__ __forceinline__ SeqSpan seq_span_of(const PagedArgs& a, int g)
     return s;
 }
 
+// a / b of non-negative values, in 32 bits where they fit (several times shorter).
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    if (static_cast<unsigned long long>(a | b) >> 32) return a / b;
+    return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+}
+
 // Tiles of one (sequence, head).  kRows packed rows a tile; every tile of a sequence
 // counts all the keys (sequences with few new tokens see nearly all in every tile).
 template <int kRows>
@@ -81,11 +96,11 @@ struct FlatTiles {
     __device__ __forceinline__ static int rows(const PagedParams&) { return kRows; }
     __device__ __forceinline__ void init(const PagedParams& p, const SeqSpan& s)
     {
-        n_tiles = static_cast<int>((static_cast<long long>(s.n) * p.G + kRows - 1) / kRows);
+        n_tiles = (s.n * p.G + kRows - 1) / kRows;        // n G <= T H < 2^31 - 16
         cost = kTileCost + s.kv;
     }
     __device__ __forceinline__ long long prefix(int j) const { return j * cost; }
-    __device__ __forceinline__ int at(long long x) const { return static_cast<int>(x / cost); }
+    __device__ __forceinline__ int at(long long x) const { return static_cast<int>(quotient(x, cost)); }
 };
 
 // The same where a sequence may have many tiles: under the causal rule tile j of `per` tokens
@@ -115,7 +130,7 @@ struct StepTiles {
     }
     __device__ __forceinline__ int at(long long x) const
     {
-        if (!causal) return static_cast<int>(x / (static_cast<long long>(kTileCost) + kv));
+        if (!causal) return static_cast<int>(quotient(x, static_cast<long long>(kTileCost) + kv));
         int lo = 0, hi = n_tiles;               // prefix(lo) <= x < prefix(hi)
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -129,7 +144,7 @@ struct StepTiles {
 // One CTA's share of one tile.
 struct Segment {
     int g, hk;              // sequence, key/value head
-    long long row0;         // first packed row of the tile within the sequence
+    int row0;               // first packed row of the tile within the sequence (T * H < 2^31)
     int rows;               // packed rows of the tile
     SeqSpan s;
     int keys;               // keys that some row of the tile sees: [0, keys)
@@ -172,23 +187,23 @@ struct PagedWalk {
             load_seq(p);
         }
         const long long rel = x - seq0;
-        t.hk = static_cast<int>(rel / head_cost);
+        t.hk = static_cast<int>(quotient(rel, head_cost));
         const long long head0 = t.hk * head_cost;
         const int j = tiles.at(rel - head0);
         const long long a = seq0 + head0 + tiles.prefix(j), b = seq0 + head0 + tiles.prefix(j + 1);
         t.g = g;
         t.s = s;
-        const long long rows = Tiles::rows(p);
+        const int rows = Tiles::rows(p);
         t.row0 = j * rows;
-        t.rows = static_cast<int>(min(rows, static_cast<long long>(s.n) * p.G - t.row0));
+        t.rows = min(rows, s.n * p.G - t.row0);
         // the last token of the tile sees the most keys
-        const int last = static_cast<int>((t.row0 + t.rows - 1) / p.G);
+        const int last = (t.row0 + t.rows - 1) / p.G;
         t.keys = p.a.causal ? min(max(s.kv - s.n + last + 1, 0), s.kv) : s.kv;
         const long long stop = min(end, b);
         t.k0 = cut(x - a, b - a, t.keys);
         t.k1 = cut(stop - a, b - a, t.keys);
-        t.c_first = static_cast<int>(a / chunk);
-        t.c_last = static_cast<int>((b - 1) / chunk);
+        t.c_first = static_cast<int>(quotient(a, chunk));
+        t.c_last = static_cast<int>(quotient(b - 1, chunk));
         x = stop;
         return true;
     }
@@ -291,9 +306,8 @@ __device__ __forceinline__ float part_weight(float m, float l, float M)
 // Output row of packed row r of a segment.
 __device__ __forceinline__ long long out_row(const PagedParams& p, const Segment& t, int r)
 {
-    const long long pr = t.row0 + r;
-    const long long tok = pr / p.G;
-    return (t.s.first + tok) * p.a.H + t.hk * p.G + (pr - tok * p.G);
+    const int pr = t.row0 + r, tok = pr / p.G;
+    return static_cast<long long>(t.s.first + tok) * p.a.H + t.hk * p.G + (pr - tok * p.G);
 }
 
 template <typename T>
@@ -312,7 +326,7 @@ __device__ __forceinline__ void write_row4(const PagedParams& p, const Segment& 
 // End of a segment, by the whole block: buf[rows][ldo] holds the CTA's unnormalised sums
 // and stat[rows] = (maximum in base-2 units, denominator).  Writes the tile's output, or
 // the CTA's partial and, in the last CTA of the tile, the joined output.
-template <typename T, int kRows, int kThreads>
+template <typename T, int kRows, int kThreads, int kVec4 = 1>
 __device__ void finish_segment(const PagedParams& p, const Segment& t, const float* buf, int ldo,
                                const float2* stat, int* flag)
 {
@@ -361,7 +375,7 @@ __device__ void finish_segment(const PagedParams& p, const Segment& t, const flo
     if (*flag) {
         __threadfence();
         const int nc = t.c_last - t.c_first + 1;
-        constexpr int kVec4 = 2;                       // float4 per lane: D <= 256
+        // kVec4 float4 per lane: D <= 128 kVec4
         for (int r = warp; r < t.rows; r += kThreads / 32) {
             auto stat_at = [&](int i) -> float2 {
                 const long long at = static_cast<long long>(slot_of(t.c_first + i)) * kRows + r;
@@ -369,36 +383,48 @@ __device__ void finish_segment(const PagedParams& p, const Segment& t, const flo
                     return make_float2(-INFINITY, 0.f);
                 return __ldcg(reinterpret_cast<const float2*>(p.part_stat) + at);
             };
-            float M = -INFINITY;
-            for (int i0 = 0; i0 < nc; i0 += 32) M = fmaxf(M, stat_at(i0 + lane).x);
+            const float2 mine = stat_at(lane);             // of the first 32 contributors
+            float M = mine.x;
+            for (int i0 = 32; i0 < nc; i0 += 32) M = fmaxf(M, stat_at(i0 + lane).x);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             float L = 0.f;
             float4 acc[kVec4];
 #pragma unroll
             for (int u = 0; u < kVec4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
             for (int i0 = 0; i0 < nc; i0 += 32) {
-                const float2 st = stat_at(i0 + lane);
+                const float2 st = i0 == 0 ? mine : stat_at(i0 + lane);
                 const float w = part_weight(st.x, st.y, M);
                 L += st.y == 0.f ? 0.f : w * st.y;
                 const unsigned have = __ballot_sync(0xffffffffu, !(st.y == 0.f));
                 const int cnt = min(32, nc - i0);
-#pragma unroll 8
-                for (int i = 0; i < cnt; ++i) {
-                    const float wi = __shfl_sync(0xffffffffu, w, i);
-                    if (!((have >> i) & 1)) continue;
-                    const long long at =
-                        (static_cast<long long>(slot_of(t.c_first + i0 + i)) * kRows + r) * p.a.D;
+                // eight contributors' sums in flight; an empty one wrote none
+#pragma unroll 1
+                for (int i = 0; i < cnt; i += 8) {
+                    float4 o[8][kVec4];
 #pragma unroll
-                    for (int u = 0; u < kVec4; ++u) {
-                        const int cc = lane + 32 * u;
-                        if (cc < v4 && in_bounds(at + 4 * cc, 4, n_slots * kRows * p.a.D, p.a.status)) {
-                            const float4 o =
-                                __ldcg(reinterpret_cast<const float4*>(p.part_o + at + 4 * cc));
-                            acc[u].x = fmaf(wi, o.x, acc[u].x);
-                            acc[u].y = fmaf(wi, o.y, acc[u].y);
-                            acc[u].z = fmaf(wi, o.z, acc[u].z);
-                            acc[u].w = fmaf(wi, o.w, acc[u].w);
+                    for (int e = 0; e < 8; ++e) {
+                        const long long at =
+                            (static_cast<long long>(slot_of(t.c_first + i0 + i + e)) * kRows + r) * p.a.D;
+#pragma unroll
+                        for (int u = 0; u < kVec4; ++u) {
+                            const int cc = lane + 32 * u;
+                            o[e][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (i + e < cnt && ((have >> (i + e)) & 1) && cc < v4 &&
+                                in_bounds(at + 4 * cc, 4, n_slots * kRows * p.a.D, p.a.status))
+                                o[e][u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at + 4 * cc));
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float wi = __shfl_sync(0xffffffffu, w, (i + e) & 31);
+#pragma unroll
+                        for (int u = 0; u < kVec4; ++u) {
+                            acc[u].x = fmaf(wi, o[e][u].x, acc[u].x);
+                            acc[u].y = fmaf(wi, o[e][u].y, acc[u].y);
+                            acc[u].z = fmaf(wi, o[e][u].z, acc[u].z);
+                            acc[u].w = fmaf(wi, o[e][u].w, acc[u].w);
                         }
                     }
                 }
@@ -415,9 +441,10 @@ __device__ void finish_segment(const PagedParams& p, const Segment& t, const flo
 
 // Element offset of key `key` of head hk of a sequence in the pages, or -1 (a page index
 // outside the cache: the key and its value read as zeros).
-__device__ __forceinline__ long long key_offset(const PagedArgs& a, int g, int hk, int key)
+__device__ __forceinline__ long long key_offset(const PagedParams& p, int g, int hk, int key)
 {
-    const int col = key / a.page_size;
+    const PagedArgs& a = p.a;
+    const int col = p.page_shift >= 0 ? key >> p.page_shift : key / a.page_size;
     const int page = checked_ldg(a.page_table, g * a.table_stride + col, a.table_elems, a.status);
     if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) return -1;
     return page * a.page_stride + (key - col * a.page_size) * a.token_stride + hk * a.head_stride;

@@ -692,7 +692,7 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  * Scores and softmax in fp32; the bf16 kernels round the weights to bf16 for the value
  * product, whose sums are fp32; out is rounded once.  Repeated calls on the same inputs give
  * the same bits; the split over the GPU, and with it the last bits, depends on all lengths of
- * the call.  Limits: T * H < 2^31.  Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED (dtype,
+ * the call.  Limits: T * H <= 2^31 - 256.  Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED (dtype,
  * D), RA_ERR_NOT_DIVISIBLE (H % H_kv), RA_ERR_MISALIGNED, RA_ERR_CUDA.
  */
 ra_status paged_attn_fwd(const ra_paged_desc* desc, const void* q, long long q_stride,
