@@ -12,7 +12,11 @@
 //   warp 1      issues S_t = Q_t K^T and O_t += P_t V;
 //   warps 4-7, 8-11  softmax of sub-tile 0, 1: one thread per row.
 // The sub-tiles ping-pong, and the next segment's loads and first products overlap the
-// output of the last.  A tile with no more than one sub-tile of rows runs that one alone.
+// output of the last.  A tile with no more than one sub-tile of rows would leave the tensor
+// core idle during its softmax; it ping-pongs with itself instead: the two warpgroups take
+// its even and odd key blocks, each with its own running softmax and its own O, and the
+// first one adds the second's result to its own at the end (both hold a row in the same
+// lane, so it reads the other's O from TMEM directly).
 //
 // A box of a page that the table does not name properly, or of a page behind the last key,
 // is loaded at an index outside the tensor, which TMA fills with zeros without reading
@@ -43,7 +47,7 @@ struct Layout {
     static constexpr int kV = kK + 2 * kTile;
     static constexpr int kStage = kV + 2 * kTile;     // 8 warps x 32 rows x D/2 bf16
     static constexpr int kBar = kStage + kTile;
-    static constexpr int kSmem = kBar + 1024 + 1024;  // barriers, scratch; alignment slack
+    static constexpr int kSmem = kBar + 2048 + 1024;  // barriers, scratch; alignment slack
     __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
     __device__ static constexpr uint32_t col_o(int t) { return 256u + static_cast<uint32_t>(D) * t; }
 };
@@ -62,15 +66,18 @@ enum : int {
     kBarSegEmpty = 22,   // +slot
     kBarPart = 24,       // the eight softmax warps have written their partials
     kBarFlag = 25,       // whether this CTA joins them is known
-    kBarDone = 26,
-    kBarCount = 27
+    kBarOdd = 26,        // single sub-tile: the odd blocks' statistics are in shared memory
+    kBarAdded = 27,      // ... and their O has been read
+    kBarDone = 28,
+    kBarCount = 29
 };
 // shared-memory words after the barriers
 constexpr int kTmemSlot = kBarCount * 8, kAbort = kTmemSlot + 4, kLast = kTmemSlot + 8;
 constexpr int kSegInts = 12;
 constexpr int kSegSlots = kTmemSlot + 16;                   // 2 slots of kSegInts ints
 constexpr int kScratch = (kSegSlots + 2 * kSegInts * 4 + 7) / 8 * 8;
-static_assert(kScratch + 34 * 8 <= 1024, "barrier area");
+constexpr int kOddStat = kScratch + 34 * 8;                 // 128 x (maximum, denominator)
+static_assert(kOddStat + kSub * 8 <= 2048, "barrier area");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int c0, int c1, int c2, uint64_t policy)
@@ -163,6 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(bar(kBarPart), 8);
         mbar_init(bar(kBarFlag), 1);
+        mbar_init(bar(kBarOdd), 4);
+        mbar_init(bar(kBarAdded), 4);
         mbar_init(bar(kBarDone), 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -308,8 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq = sdesc_sw128(sbase + Lay::kQ, 16, 1024);
         const uint64_t dk = sdesc_sw128(sbase + Lay::kK, 16, 1024);
         const uint64_t dv = sdesc_sw128(sbase + Lay::kV, 16384, 1024);
-        auto issue_qk = [&](int tq, int st) {
-            const uint32_t d_t = tmem + Lay::col_s(tq);
+        // S_x = Q_tq K^T, O_x += P_x V
+        auto issue_qk = [&](int tq, int x, int st) {
+            const uint32_t d_t = tmem + Lay::col_s(x);
             const uint64_t a0 = dq + tq * kTileU, b0 = dk + st * kTileU;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -328,8 +338,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait_all = [&](int idx, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar(idx), parity, wc));
         };
-        // rows of V behind the last key of the sequence become zeros
-        auto zero_tail = [&](int st, int from) {
+        // rows of V behind the last key of the sequence become zeros (block n of the segment)
+        auto clean_tail = [&](const Seg& s, int n, int st, uint32_t ph) -> bool {
+            const int held = s.kv - (s.k0 + n * kKeys);       // keys of the block that exist
+            if (held >= kKeys) return true;
+            if (!wait_all(kBarVFull + st, ph)) return false;
+            const int from = max(held, 0);
             uint8_t* v = smem + Lay::kV + st * Lay::kTile;
             for (int i = lane; i < (kKeys - from) * 8 * Lay::kBoxes; i += 32) {
                 const int r = i / (8 * Lay::kBoxes), c = i % (8 * Lay::kBoxes);
@@ -338,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
+            return true;
         };
         uint32_t N = 0;
         uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};     // query loads; blocks of each sub-tile
@@ -346,31 +361,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok; ++i) {
             if (!get_seg(i, s)) break;
             if (s.n_blocks == 0) continue;
-            const bool two = s.n_sub == 2;
             const int st0 = N & 1;
             ok = wait_all(kBarQ, qn[0] & 1) && wait_all(kBarKFull + st0, (N >> 1) & 1);
             if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-                issue_qk(0, st0);
-                tc_commit(bar(kBarSFull + 0));
-                if (s.n_blocks == 1) tc_commit(bar(kBarQEmpty + 0));
-                if (!two) tc_commit(bar(kBarKEmpty + st0));
-            }
-            __syncwarp();
             ++qn[0];
-            if (two) {
-                if (!(ok = wait_all(kBarQ + 1, qn[1] & 1))) break;
+            if (s.n_sub == 1) {
+                // even blocks through S0, O0, odd ones through S1, O1, the same queries
                 tc_fence_after();
                 if (leader) {
-                    issue_qk(1, st0);
-                    tc_commit(bar(kBarSFull + 1));
-                    if (s.n_blocks == 1) tc_commit(bar(kBarQEmpty + 1));
+                    issue_qk(0, 0, st0);
+                    tc_commit(bar(kBarSFull + 0));
                     tc_commit(bar(kBarKEmpty + st0));
+                    if (s.n_blocks == 1) tc_commit(bar(kBarQEmpty + 0));
                 }
                 __syncwarp();
-                ++qn[1];
+                if (s.n_blocks > 1) {
+                    const uint32_t N1 = N + 1;
+                    if (!(ok = wait_all(kBarKFull + (N1 & 1), (N1 >> 1) & 1))) break;
+                    tc_fence_after();
+                    if (leader) {
+                        issue_qk(0, 1, N1 & 1);
+                        tc_commit(bar(kBarSFull + 1));
+                        tc_commit(bar(kBarKEmpty + (N1 & 1)));
+                        if (s.n_blocks == 2) tc_commit(bar(kBarQEmpty + 0));
+                    }
+                    __syncwarp();
+                }
+                for (int n = 0; n < s.n_blocks; ++n) {
+                    const int x = n & 1;
+                    const uint32_t Nn = N + n, N2 = Nn + 2;
+                    const int st = Nn & 1;
+                    const uint32_t ph = (Nn >> 1) & 1;
+                    const bool more = n + 2 < s.n_blocks;         // of this block's parity
+                    if (!(ok = clean_tail(s, n, st, ph))) break;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait2(bar(kBarVFull + st), ph,
+                                                                  bar(kBarPFull + 2 * x), pn[x] & 1,
+                                                                  wc))))
+                        break;
+                    tc_fence_after();
+                    if (leader) issue_pv(x, st, 0, n > 1);
+                    __syncwarp();
+                    ok = more ? mbar_wait2(bar(kBarPFull + 2 * x + 1), pn[x] & 1,
+                                           bar(kBarKFull + (N2 & 1)), (N2 >> 1) & 1, wc)
+                              : mbar_wait(bar(kBarPFull + 2 * x + 1), pn[x] & 1, wc);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    tc_fence_after();
+                    if (leader) {
+                        issue_pv(x, st, 1, true);
+                        tc_commit(bar(kBarVEmpty + st));
+                        if (!more) tc_commit(bar(kBarOFull + x));
+                        if (more) {
+                            issue_qk(0, x, N2 & 1);
+                            tc_commit(bar(kBarSFull + x));
+                            tc_commit(bar(kBarKEmpty + (N2 & 1)));
+                            if (n + 3 == s.n_blocks) tc_commit(bar(kBarQEmpty + 0));
+                        }
+                    }
+                    __syncwarp();
+                    ++pn[x];
+                }
+                N += s.n_blocks;
+                continue;
             }
+            tc_fence_after();
+            if (leader) {
+                issue_qk(0, 0, st0);
+                tc_commit(bar(kBarSFull + 0));
+                if (s.n_blocks == 1) tc_commit(bar(kBarQEmpty + 0));
+            }
+            __syncwarp();
+            if (!(ok = wait_all(kBarQ + 1, qn[1] & 1))) break;
+            tc_fence_after();
+            if (leader) {
+                issue_qk(1, 1, st0);
+                tc_commit(bar(kBarSFull + 1));
+                if (s.n_blocks == 1) tc_commit(bar(kBarQEmpty + 1));
+                tc_commit(bar(kBarKEmpty + st0));
+            }
+            __syncwarp();
+            ++qn[1];
             for (int n = 0; n < s.n_blocks; ++n) {
                 const uint32_t Nn = N + n;
                 const int st = Nn & 1;
@@ -379,11 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool last_qk = n + 2 == s.n_blocks;
                 const int st1 = (Nn + 1) & 1;
                 const uint32_t ph1 = ((Nn + 1) >> 1) & 1;
-                const int held = s.kv - (s.k0 + n * kKeys);       // keys of the block that exist
-                if (held < kKeys) {
-                    if (!(ok = wait_all(kBarVFull + st, ph))) break;
-                    zero_tail(st, max(held, 0));
-                }
+                if (!(ok = clean_tail(s, n, st, ph))) break;
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait2(bar(kBarVFull + st), ph,
                                                               bar(kBarPFull + 0), pn[0] & 1, wc))))
                     break;
@@ -396,18 +461,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if (leader) {
                     issue_pv(0, st, 1, true);
-                    if (!two) tc_commit(bar(kBarVEmpty + st));
                     if (!more) tc_commit(bar(kBarOFull + 0));
                     if (more) {
-                        issue_qk(0, st1);
+                        issue_qk(0, 0, st1);
                         tc_commit(bar(kBarSFull + 0));
                         if (last_qk) tc_commit(bar(kBarQEmpty + 0));
-                        if (!two) tc_commit(bar(kBarKEmpty + st1));
                     }
                 }
                 __syncwarp();
                 ++pn[0];
-                if (!two) continue;
                 if (!(ok = wait_all(kBarPFull + 2, pn[1] & 1))) break;
                 tc_fence_after();
                 if (leader) issue_pv(1, st, 0, n > 0);
@@ -419,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(bar(kBarVEmpty + st));
                     if (!more) tc_commit(bar(kBarOFull + 1));
                     if (more) {
-                        issue_qk(1, st1);
+                        issue_qk(1, 1, st1);
                         tc_commit(bar(kBarSFull + 1));
                         if (last_qk) tc_commit(bar(kBarQEmpty + 1));
                         tc_commit(bar(kBarKEmpty + st1));
@@ -448,18 +510,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sn = 0;                                       // S tiles seen by this sub-tile
         uint32_t on = 0;                                       // finished outputs of it
         uint32_t splits = 0;                                   // split segments of the CTA
+        uint32_t adds = 0;                                     // segments whose halves were added
+        uint32_t odd_n = 0;                                    // outputs of O1 so far
+        float2* odd_stat = reinterpret_cast<float2*>(area + kOddStat);
         bool ok = true;
         Seg s;
         for (int i = 0; ok; ++i) {
             if (!get_seg(i, s)) break;
-            const bool active = tq < s.n_sub;
-            const int in_tile = tq * sub_rows + row;           // packed row within the tile
+            // single sub-tile: both warpgroups hold its rows and take alternate key blocks
+            const bool single = s.n_sub == 1;
+            const int in_tile = (single ? 0 : tq * sub_rows) + row;   // packed row within the tile
+            const int stride = single ? 2 * kKeys : kKeys;
+            const int first_key = s.k0 + (single ? tq * kKeys : 0);
             const bool valid = row < sub_rows && in_tile < s.rows;
             const int tok = (s.row0 + in_tile) / p.G;              // within the sequence
             const int head = s.row0 + in_tile - tok * p.G;
             // keys that this row sees: [0, seen)
             const int seen = !valid ? 0 : a.causal ? s.kv - s.n + tok + 1 : s.kv;
-            const int n_blocks = active ? s.n_blocks : 0;
+            const int n_blocks = single ? (s.n_blocks + 1 - tq) / 2 : s.n_blocks;
 
             float m = -INFINITY, l = 0.f;
             for (int n = 0; n < n_blocks; ++n) {
@@ -474,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float sv[128];
 #pragma unroll
                 for (int c = 0; c < 128; ++c) sv[c] = u2f(sraw[c]);
-                const int lim = seen - (s.k0 + n * kKeys);     // columns [0, lim) are seen
+                const int lim = seen - (first_key + n * stride);   // columns [0, lim) are seen
                 if (lim < kKeys) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c) sv[c] = c >= lim ? -INFINITY : sv[c];
@@ -541,7 +609,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
 
+            if (single && s.n_blocks > 1) {
+                // the odd blocks' result is added to the even blocks'
+                if (tq == 1) {
+                    odd_stat[row] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarOdd));
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarAdded), adds & 1, wc));
+                    if (!ok) break;
+                } else {
+                    // (once the other warpgroup is here, all its earlier outputs are done, so
+                    // the parity of its last one is not mistaken for an older one's)
+                    ok = mbar_wait(bar(kBarOdd), adds & 1, wc) &&
+                         mbar_wait(bar(kBarOFull + 1), odd_n & 1, wc);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const float2 odd = odd_stat[row];
+                    const float M = fmaxf(m, odd.x);
+                    const float f0 = part_weight(m, l, M), f1 = part_weight(odd.x, odd.y, M);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o0[32], o1[32];
+                        tmem_ld32(tO + 32 * c, o0);
+                        tmem_ld32(tO + D + 32 * c, o1);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o0[j] = f2u(fmaf(f0, u2f(o0[j]), f1 * u2f(o1[j])));
+                        tmem_st32(tO + 32 * c, o0);
+                    }
+                    l = (l == 0.f ? 0.f : f0 * l) + (odd.y == 0.f ? 0.f : f1 * odd.y);
+                    m = M;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarAdded));
+                }
+                ++adds;
+            }
+            if (single ? s.n_blocks > 1 : s.n_blocks > 0) ++odd_n;
+
             // Output element offset of this thread's row, -1 for a row outside the tile.
+            const bool mine = !single || tq == 0;              // holds the rows' result
             const long long my_row =
                 valid ? static_cast<long long>(s.first + tok) * a.H + s.hk * p.G + head : -1;
             bool write = true;          // whether this CTA writes the tile's output
@@ -556,12 +664,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // this CTA's partial: statistics by row, sums column by column (rows of a
                 // warp side by side)
                 const long long slot = part_of(blockIdx.x);
-                if (valid) {
+                if (valid && mine) {
                     const long long r = slot * 2 * kSub + part_row;
                     if (in_bounds(r, 1, n_rows, a.status))
                         __stcg(reinterpret_cast<float2*>(p.part_stat) + r, make_float2(m, l));
                 }
-                if (!empty) {
+                if (!empty && mine) {
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
@@ -601,14 +709,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __threadfence();
                     M = -INFINITY;
                     L = 0.f;
-                    for (int c = 0; c < nc && valid; ++c) {
+                    for (int c = 0; c < nc && valid && mine; ++c) {
                         const long long r = part_of(s.c_first + c) * 2 * kSub + part_row;
                         if (in_bounds(r, 1, n_rows, a.status))
                             M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(p.part_stat) + r).x);
                     }
                 }
             }
-            if (write && active) {
+            if (write && mine) {
                 const long long n_elems = n_rows * D;
                 constexpr int kHalf = D / 2;
                 constexpr int kChunks = kHalf / 8;             // 16-byte chunks per staged row
