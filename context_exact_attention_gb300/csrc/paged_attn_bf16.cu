@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
             const int r = (lane >> 2) + 8 * h;
             long long at = -1;
             if (r < t.rows) {
-                const int pr = t.row0 + r, tok = pr / p.G;
+                const int pr = t.row0 + r, tok = p.token_of(pr);
                 at = (t.s.first + tok) * a.q_stride +
                      static_cast<long long>(t.hk * p.G + (pr - tok * p.G)) * D + 2 * (lane & 3);
             }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         // keys that this thread's two rows see, and that every row of the tile sees
         auto seen_by = [&](int r) {
-            const int tok = (t.row0 + r) / p.G;
+            const int tok = p.token_of(t.row0 + r);
             return a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
         };
         const int see0 = seen_by(lane >> 2), see1 = seen_by((lane >> 2) + 8);
@@ -334,8 +334,9 @@ cudaError_t launch_d(PagedParams& p)
         resident_ctas(known, paged_bf16_kernel<D>, kThreads, Smem<D>::kBytes, &grid);
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
+    p.tile_cost = 64;
+    p.key_cost = 1;
     p.min_chunk = 2 * kUnit;
-    p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, D);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     p.counters = reinterpret_cast<unsigned int*>(ws);
@@ -350,9 +351,7 @@ cudaError_t launch_d(PagedParams& p)
 cudaError_t launch_paged_bf16(const PagedArgs& a)
 {
     PagedParams p;
-    p.a = a;
-    p.G = a.H / a.H_kv;
-    p.page_shift = page_shift_of(a.page_size);
+    fill_params(&p, a);
     if (a.D == 64) return launch_d<64>(p);
     if (a.D == 128) return launch_d<128>(p);
     return cudaErrorInvalidValue;

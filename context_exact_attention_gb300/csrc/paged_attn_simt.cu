@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
                 q[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
                 o[r][u] = q[r][u];
                 if (r < t.rows && c < D) {
-                    const int pr = t.row0 + r, tok = pr / p.G;
+                    const int pr = t.row0 + r, tok = p.token_of(pr);
                     const long long at = (t.s.first + tok) * a.q_stride +
                                          static_cast<long long>(t.hk * p.G + (pr - tok * p.G)) * D + c;
                     if (in_bounds(at, 4, a.q_elems, a.status)) q[r][u] = load4(Q + at);
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
         const int my_row = lane & 3, my_key = lane >> 2;
         int seen = 0;
         if (my_row < t.rows) {
-            const int tok = (t.row0 + my_row) / p.G;
+            const int tok = p.token_of(t.row0 + my_row);
             seen = a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
         }
         float m = -INFINITY, l = 0.f;      // of row my_row; l over this lane's keys only
@@ -198,17 +198,16 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
 cudaError_t launch_paged_simt(const PagedArgs& a)
 {
     PagedParams p;
-    p.a = a;
-    p.G = a.H / a.H_kv;
-    p.page_shift = page_shift_of(a.page_size);
+    fill_params(&p, a);
     static std::atomic<int> known1[kMaxDevices], known2[kMaxDevices];
     int grid = 0;
     const cudaError_t e = a.D <= 128 ? resident_ctas(known1, paged_simt_kernel<1>, kThreads, 0, &grid)
                                      : resident_ctas(known2, paged_simt_kernel<2>, kThreads, 0, &grid);
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
+    p.tile_cost = 64;
+    p.key_cost = 1;
     p.min_chunk = 4 * kUnit;
-    p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.D));
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, a.D);
     p.counters = reinterpret_cast<unsigned int*>(ws);

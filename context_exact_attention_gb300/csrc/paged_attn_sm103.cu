@@ -35,18 +35,20 @@ namespace {
 constexpr int kSub = 128;         // rows of a sub-tile = TMEM lanes
 constexpr int kKeys = 128;        // keys per block
 constexpr int kThreads = 384;
-constexpr int kReaders = 1 + 8;   // warps that read a published segment
+constexpr int kReaders = 2 + 8;   // warps that read a published segment
 constexpr float kRescaleThreshold = 8.0f;
 
 template <int D>
 struct Layout {
     static constexpr int kBoxes = D / 64;
     static constexpr int kTile = 128 * D * 2;
+    static constexpr int kStages = D == 64 ? 4 : 2;   // of the K and the V ring: 64 KB each
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + 2 * kTile;
-    static constexpr int kV = kK + 2 * kTile;
-    static constexpr int kStage = kV + 2 * kTile;     // 8 warps x 32 rows x D/2 bf16
-    static constexpr int kBar = kStage + kTile;
+    static constexpr int kV = kK + kStages * kTile;
+    static constexpr int kStage = kV + kStages * kTile;   // 8 warps x 32 rows x D/2 bf16
+    // (a slice holds 32 rows of 32 floats or of D/2 bf16)
+    static constexpr int kBar = kStage + 8 * 32 * 128;
     static constexpr int kSmem = kBar + 2048 + 1024;  // barriers, scratch; alignment slack
     __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
     __device__ static constexpr uint32_t col_o(int t) { return 256u + static_cast<uint32_t>(D) * t; }
@@ -55,25 +57,25 @@ struct Layout {
 enum : int {
     kBarQ = 0,           // +sub-tile: queries loaded
     kBarQEmpty = 2,      // +sub-tile: the segment's last Q K^T of the sub-tile finished
-    kBarKFull = 4,       // +stage
-    kBarKEmpty = 6,      // +stage
-    kBarVFull = 8,       // +stage
-    kBarVEmpty = 10,     // +stage
-    kBarSFull = 12,      // +sub-tile
-    kBarPFull = 14,      // +2 sub-tile + half
-    kBarOFull = 18,      // +sub-tile
-    kBarSegFull = 20,    // +slot
-    kBarSegEmpty = 22,   // +slot
-    kBarPart = 24,       // the eight softmax warps have written their partials
-    kBarFlag = 25,       // whether this CTA joins them is known
-    kBarOdd = 26,        // single sub-tile: the odd blocks' statistics are in shared memory
-    kBarAdded = 27,      // ... and their O has been read
-    kBarDone = 28,
-    kBarCount = 29
+    kBarKFull = 4,       // +stage (up to 4)
+    kBarKEmpty = 8,      // +stage
+    kBarVFull = 12,      // +stage
+    kBarVEmpty = 16,     // +stage
+    kBarSFull = 20,      // +sub-tile
+    kBarPFull = 22,      // +2 sub-tile + half
+    kBarOFull = 26,      // +sub-tile
+    kBarSegFull = 28,    // +slot
+    kBarSegEmpty = 30,   // +slot
+    kBarPart = 32,       // the eight softmax warps have written their partials
+    kBarFlag = 33,       // whether this CTA joins them is known
+    kBarOdd = 34,        // single sub-tile: the odd blocks' statistics are in shared memory
+    kBarAdded = 35,      // ... and their O has been read
+    kBarDone = 36,
+    kBarCount = 37
 };
 // shared-memory words after the barriers
 constexpr int kTmemSlot = kBarCount * 8, kAbort = kTmemSlot + 4, kLast = kTmemSlot + 8;
-constexpr int kSegInts = 12;
+constexpr int kSegInts = 14;
 constexpr int kSegSlots = kTmemSlot + 16;                   // 2 slots of kSegInts ints
 constexpr int kScratch = (kSegSlots + 2 * kSegInts * 4 + 7) / 8 * 8;
 constexpr int kOddStat = kScratch + 34 * 8;                 // 128 x (maximum, denominator)
@@ -91,7 +93,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 
 // What the other warps need of a segment.
 struct Seg {
-    int hk, rows, n_sub, first, n, kv, k0, n_blocks, c_first, c_last, row0;
+    int g, hk, rows, n_sub, first, n, kv, k0, n_blocks, c_first, c_last, row0;
+    int once;               // the sequence's keys are read by this tile alone
 };
 __device__ __forceinline__ void publish(volatile int* e, int more, const Seg& s)
 {
@@ -107,6 +110,8 @@ __device__ __forceinline__ void publish(volatile int* e, int more, const Seg& s)
     e[9] = s.c_first;
     e[10] = s.c_last;
     e[11] = s.row0;
+    e[12] = s.g;
+    e[13] = s.once;
 }
 __device__ __forceinline__ bool consume(volatile int* e, Seg& s)
 {
@@ -121,6 +126,8 @@ __device__ __forceinline__ bool consume(volatile int* e, Seg& s)
     s.c_first = e[9];
     s.c_last = e[10];
     s.row0 = e[11];
+    s.g = e[12];
+    s.once = e[13];
     return e[0] != 0;
 }
 
@@ -154,13 +161,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sub_rows = sub_tokens * p.G;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kBarQ + i), 1);
-            mbar_init(bar(kBarQEmpty + i), 1);
+        for (int i = 0; i < Lay::kStages; ++i) {
             mbar_init(bar(kBarKFull + i), 1);
             mbar_init(bar(kBarKEmpty + i), 1);
             mbar_init(bar(kBarVFull + i), 1);
             mbar_init(bar(kBarVEmpty + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarQ + i), 1);
+            mbar_init(bar(kBarQEmpty + i), 1);
             mbar_init(bar(kBarSFull + i), 1);
             mbar_init(bar(kBarPFull + 2 * i), kSub);
             mbar_init(bar(kBarPFull + 2 * i + 1), kSub);
@@ -199,30 +208,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         return more;
     };
 
+    constexpr int kStages = Lay::kStages;
+    auto stage_of = [](uint32_t n) -> int { return n % kStages; };
+    auto phase_of = [](uint32_t n) -> uint32_t { return (n / kStages) & 1; };
+
+    // Loads the blocks of a segment into the K or the V ring and counts them in N, the blocks
+    // loaded so far (whole warp; false: a wait ran out).  Lane: box lane / kBoxes of the block's
+    // pages, columns 64 (lane mod kBoxes).
+    auto load_blocks = [&](const Seg& s, const CUtensorMap* map, int ring, int full, int empty,
+                           uint32_t& N, bool leader) -> bool {
+        const uint64_t policy = s.once ? l2_policy_evict_first() : l2_policy_evict_last();
+        const int box_rows = min(a.page_size, kKeys);
+        const int my_box = lane / Lay::kBoxes, my_col = lane % Lay::kBoxes;
+        const bool loads = my_box < kKeys / box_rows;         // at most 16 pages a block
+        const uint32_t to = my_col * 16384 + my_box * box_rows * 128;
+        // the page of this lane's box of the block at key kb: an index outside the cache
+        // (zeros) behind the last key and for an entry that names no page
+        auto page_of = [&](int kb) -> int {
+            const int key = kb + my_box * box_rows;
+            int page = -1;
+            if (loads && key < s.kv) {
+                const int col = p.page_shift >= 0 ? key >> p.page_shift : key / a.page_size;
+                page = checked_ldg(a.page_table, s.g * a.table_stride + col, a.table_elems, a.status);
+            }
+            return static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages) ? page
+                                                                                  : a.num_pages;
+        };
+        int page = page_of(s.k0);
+        for (int n = 0; n < s.n_blocks; ++n, ++N) {
+            const int kb = s.k0 + n * kKeys;
+            const int in_page = a.page_size > kKeys ? kb % a.page_size : 0;
+            const int page_next = n + 1 < s.n_blocks ? page_of(kb + kKeys) : 0;
+            const int st = stage_of(N);
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(empty + st), phase_of(N) ^ 1, wc)))
+                return false;
+            if (leader) mbar_arrive_expect_tx(bar(full + st), Lay::kTile);
+            __syncwarp();
+            if (loads)
+                tma_load_4d(sbase + ring + st * Lay::kTile + to, map, bar(full + st), my_col * 64,
+                            s.hk, in_page, page, policy);
+            page = page_next;
+        }
+        return true;
+    };
+    // Lets this warp's own copies into a ring land (N blocks loaded).
+    auto drain = [&](int full, uint32_t N) {
+        for (uint32_t n = N > kStages ? N - kStages : 0; n < N; ++n)
+            mbar_wait_drain(bar(full + stage_of(n)), phase_of(n), wc);
+        __syncwarp();
+    };
+
     if (warp == 0) {
-        // ------------------------------------------------------------ producer
+        // ---------------------------------------------- segments, queries and keys
         const bool leader = elect_one();
         if (leader) {
             tma_prefetch_desc(&tmap_q);
             tma_prefetch_desc(&tmap_k);
-            tma_prefetch_desc(&tmap_v);
         }
-        const uint64_t keep = l2_policy_evict_last();
         const uint64_t once = l2_policy_evict_first();
-        const int box_rows = min(a.page_size, kKeys);
-        const int n_boxes = kKeys / box_rows;                 // pages a block touches, at most 16
-        // lane: box lane / kBoxes of the block's pages, columns 64 (lane mod kBoxes)
-        const int my_box = lane / Lay::kBoxes, my_col = lane % Lay::kBoxes;
-        const bool loads = my_box < n_boxes;
-        uint32_t N = 0;                                       // blocks loaded so far
+        uint32_t N = 0;
         uint32_t q_loads[2] = {0, 0};                         // query loads per sub-tile so far
-        int last_k[2] = {-1, -1}, last_v[2] = {-1, -1};
         bool ok = true;
         Segment t;
         for (int i = 0; ok; ++i) {
             const bool more = walk.next(p, t);
             Seg s{};
             if (more) {
+                s.g = t.g;
                 s.hk = t.hk;
                 s.rows = t.rows;
                 s.n_sub = t.rows > sub_rows ? 2 : 1;
@@ -234,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s.c_first = t.c_first;
                 s.c_last = t.c_last;
                 s.row0 = t.row0;
+                s.once = t.s.n <= p.tile_tokens;
             }
             const int slot = i & 1;
             if (i >= 2 &&
@@ -247,8 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (!more) break;
             if (s.n_blocks == 0) continue;
-            const int tok0 = t.s.first + t.row0 / p.G;
-            for (int tq = 0; tq < s.n_sub && ok; ++tq) {
+            const int tok0 = s.first + p.token_of(s.row0);
+#pragma unroll
+            for (int tq = 0; tq < 2; ++tq) {
+                if (tq >= s.n_sub) break;
                 if (q_loads[tq] > 0 &&
                     !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQEmpty + tq),
                                                              (q_loads[tq] - 1) & 1, wc))))
@@ -262,52 +317,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++q_loads[tq];
                 __syncwarp();
             }
-            // page and slot of this lane's box of the block at key kb: an index outside the
-            // cache (zeros) behind the last key and for an entry that names no page
-            auto page_of = [&](int kb) -> int {
-                const int key = kb + my_box * box_rows;
-                int page = -1;
-                if (loads && key < s.kv)
-                    page = checked_ldg(a.page_table, t.g * a.table_stride + key / a.page_size,
-                                       a.table_elems, a.status);
-                return static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages) ? page
-                                                                                      : a.num_pages;
-            };
-            int page = page_of(s.k0);
-            for (int n = 0; n < s.n_blocks && ok; ++n) {
-                const int kb = s.k0 + n * kKeys;
-                const int in_page = a.page_size > kKeys ? kb % a.page_size : 0;
-                const int page_next = n + 1 < s.n_blocks ? page_of(kb + kKeys) : 0;
-                const uint32_t Nn = N + n;
-                const int st = Nn & 1;
-                const uint32_t ph = (Nn >> 1) & 1;
-                const uint32_t to = my_col * 16384 + my_box * box_rows * 128;
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarKEmpty + st), ph ^ 1, wc)))) break;
-                if (leader) mbar_arrive_expect_tx(bar(kBarKFull + st), Lay::kTile);
-                __syncwarp();
-                if (loads)
-                    tma_load_4d(sbase + Lay::kK + st * Lay::kTile + to, &tmap_k, bar(kBarKFull + st),
-                                my_col * 64, s.hk, in_page, page, keep);
-                last_k[st] = static_cast<int>(Nn);
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarVEmpty + st), ph ^ 1, wc)))) break;
-                if (leader) mbar_arrive_expect_tx(bar(kBarVFull + st), Lay::kTile);
-                __syncwarp();
-                if (loads)
-                    tma_load_4d(sbase + Lay::kV + st * Lay::kTile + to, &tmap_v, bar(kBarVFull + st),
-                                my_col * 64, s.hk, in_page, page, keep);
-                last_v[st] = static_cast<int>(Nn);
-                page = page_next;
-            }
-            N += s.n_blocks;
+            if (!ok) break;
+            ok = load_blocks(s, &tmap_k, Lay::kK, kBarKFull, kBarKEmpty, N, leader);
         }
-        // let this CTA's own copies land before anyone leaves
         for (int tq = 0; tq < 2; ++tq)
             if (q_loads[tq] > 0) mbar_wait_drain(bar(kBarQ + tq), (q_loads[tq] - 1) & 1, wc);
-        for (int st = 0; st < 2; ++st) {
-            if (last_k[st] >= 0) mbar_wait_drain(bar(kBarKFull + st), (last_k[st] >> 1) & 1, wc);
-            if (last_v[st] >= 0) mbar_wait_drain(bar(kBarVFull + st), (last_v[st] >> 1) & 1, wc);
+        drain(kBarKFull, N);
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- values
+        // (a warp of their own: a stage of V is held until its weights are ready, and the
+        // next keys must not wait for that)
+        const bool leader = elect_one();
+        if (leader) tma_prefetch_desc(&tmap_v);
+        uint32_t N = 0;
+        bool ok = true;
+        Seg s;
+        for (int i = 0; ok; ++i) {
+            if (!get_seg(i, s)) break;
+            ok = load_blocks(s, &tmap_v, Lay::kV, kBarVFull, kBarVEmpty, N, leader);
         }
-        __syncwarp();
+        drain(kBarVFull, N);
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
         const bool leader = elect_one();
@@ -361,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok; ++i) {
             if (!get_seg(i, s)) break;
             if (s.n_blocks == 0) continue;
-            const int st0 = N & 1;
-            ok = wait_all(kBarQ, qn[0] & 1) && wait_all(kBarKFull + st0, (N >> 1) & 1);
+            const int st0 = stage_of(N);
+            ok = wait_all(kBarQ, qn[0] & 1) && wait_all(kBarKFull + st0, phase_of(N));
             if (!ok) break;
             ++qn[0];
             if (s.n_sub == 1) {
@@ -376,22 +405,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (s.n_blocks > 1) {
-                    const uint32_t N1 = N + 1;
-                    if (!(ok = wait_all(kBarKFull + (N1 & 1), (N1 >> 1) & 1))) break;
+                    const int st1 = stage_of(N + 1);
+                    if (!(ok = wait_all(kBarKFull + st1, phase_of(N + 1)))) break;
                     tc_fence_after();
                     if (leader) {
-                        issue_qk(0, 1, N1 & 1);
+                        issue_qk(0, 1, st1);
                         tc_commit(bar(kBarSFull + 1));
-                        tc_commit(bar(kBarKEmpty + (N1 & 1)));
+                        tc_commit(bar(kBarKEmpty + st1));
                         if (s.n_blocks == 2) tc_commit(bar(kBarQEmpty + 0));
                     }
                     __syncwarp();
                 }
                 for (int n = 0; n < s.n_blocks; ++n) {
                     const int x = n & 1;
-                    const uint32_t Nn = N + n, N2 = Nn + 2;
-                    const int st = Nn & 1;
-                    const uint32_t ph = (Nn >> 1) & 1;
+                    const int st = stage_of(N + n), st2 = stage_of(N + n + 2);
+                    const uint32_t ph = phase_of(N + n);
                     const bool more = n + 2 < s.n_blocks;         // of this block's parity
                     if (!(ok = clean_tail(s, n, st, ph))) break;
                     if (!(ok = __all_sync(0xffffffffu, mbar_wait2(bar(kBarVFull + st), ph,
@@ -402,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (leader) issue_pv(x, st, 0, n > 1);
                     __syncwarp();
                     ok = more ? mbar_wait2(bar(kBarPFull + 2 * x + 1), pn[x] & 1,
-                                           bar(kBarKFull + (N2 & 1)), (N2 >> 1) & 1, wc)
+                                           bar(kBarKFull + st2), phase_of(N + n + 2), wc)
                               : mbar_wait(bar(kBarPFull + 2 * x + 1), pn[x] & 1, wc);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
@@ -411,9 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_commit(bar(kBarVEmpty + st));
                         if (!more) tc_commit(bar(kBarOFull + x));
                         if (more) {
-                            issue_qk(0, x, N2 & 1);
+                            issue_qk(0, x, st2);
                             tc_commit(bar(kBarSFull + x));
-                            tc_commit(bar(kBarKEmpty + (N2 & 1)));
+                            tc_commit(bar(kBarKEmpty + st2));
                             if (n + 3 == s.n_blocks) tc_commit(bar(kBarQEmpty + 0));
                         }
                     }
@@ -441,13 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++qn[1];
             for (int n = 0; n < s.n_blocks; ++n) {
-                const uint32_t Nn = N + n;
-                const int st = Nn & 1;
-                const uint32_t ph = (Nn >> 1) & 1;
+                const int st = stage_of(N + n), st1 = stage_of(N + n + 1);
+                const uint32_t ph = phase_of(N + n), ph1 = phase_of(N + n + 1);
                 const bool more = n + 1 < s.n_blocks;
                 const bool last_qk = n + 2 == s.n_blocks;
-                const int st1 = (Nn + 1) & 1;
-                const uint32_t ph1 = ((Nn + 1) >> 1) & 1;
                 if (!(ok = clean_tail(s, n, st, ph))) break;
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait2(bar(kBarVFull + st), ph,
                                                               bar(kBarPFull + 0), pn[0] & 1, wc))))
@@ -506,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_off + Lay::col_s(tq);
         const uint32_t tO = tmem + lane_off + Lay::col_o(tq);
         const float sl2 = p.scale_log2;
-        const int part_row = tq * kSub + row;                  // row in a partial result
         uint32_t sn = 0;                                       // S tiles seen by this sub-tile
         uint32_t on = 0;                                       // finished outputs of it
         uint32_t splits = 0;                                   // split segments of the CTA
@@ -523,8 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int stride = single ? 2 * kKeys : kKeys;
             const int first_key = s.k0 + (single ? tq * kKeys : 0);
             const bool valid = row < sub_rows && in_tile < s.rows;
-            const int tok = (s.row0 + in_tile) / p.G;              // within the sequence
-            const int head = s.row0 + in_tile - tok * p.G;
+            const int tok = p.token_of(s.row0 + in_tile);            // within the sequence
             // keys that this row sees: [0, seen)
             const int seen = !valid ? 0 : a.causal ? s.kv - s.n + tok + 1 : s.kv;
             const int n_blocks = single ? (s.n_blocks + 1 - tq) / 2 : s.n_blocks;
@@ -648,55 +671,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (single ? s.n_blocks > 1 : s.n_blocks > 0) ++odd_n;
 
-            // Output element offset of this thread's row, -1 for a row outside the tile.
             const bool mine = !single || tq == 0;              // holds the rows' result
-            const long long my_row =
-                valid ? static_cast<long long>(s.first + tok) * a.H + s.hk * p.G + head : -1;
-            bool write = true;          // whether this CTA writes the tile's output
-            bool joined = false;        // ... of several CTAs' partials
-            float M = m, L = l;
-            const int nc = s.c_last - s.c_first + 1;
-            const long long n_rows = 2ll * p.grid * 2 * kSub;  // rows of all partial slots
-            auto part_of = [&](int cta) -> long long {         // slot of a CTA's partial
-                return 2ll * cta + (cta == s.c_first ? 1 : 0);
-            };
-            if (nc > 1) {
-                // this CTA's partial: statistics by row, sums column by column (rows of a
-                // warp side by side)
-                const long long slot = part_of(blockIdx.x);
-                if (valid && mine) {
-                    const long long r = slot * 2 * kSub + part_row;
-                    if (in_bounds(r, 1, n_rows, a.status))
-                        __stcg(reinterpret_cast<float2*>(p.part_stat) + r, make_float2(m, l));
-                }
-                if (!empty && mine) {
-#pragma unroll
+            const TileRows tile{s.first, s.row0, s.rows, s.hk, s.c_first, s.c_last};
+            uint8_t* stage = smem + Lay::kStage + (warp - 4) * 32 * 128;
+            if (s.c_first != s.c_last) {
+                // this CTA's partial, row by row as the joining warps read it; the sums go
+                // through the warp's staging slice, 32 columns at a time, so that a store
+                // covers whole 128-byte runs of four rows
+                const long long all_rows = 2ll * p.grid * 2 * kSub;
+                const long long at0 = part_slot(tile, blockIdx.x) * 2 * kSub + tq * kSub;
+                if (valid && mine && in_bounds(at0 + row, 1, all_rows, a.status))
+                    __stcg(reinterpret_cast<float2*>(p.part_stat) + at0 + row, make_float2(m, l));
+                if (!empty && mine && __any_sync(0xffffffffu, valid)) {
+                    const unsigned rows_in = __ballot_sync(0xffffffffu, valid);
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld32(tO + 32 * c, o);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const long long at = (slot * D + 32 * c + j) * 2 * kSub + part_row;
-                            if (valid && in_bounds(at, 1, n_rows * D, a.status))
-                                __stcg(p.part_o + at, u2f(o[j]));
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int rr = 4 * k + (lane >> 3), cc = lane & 7;
+                            const float4 val = *reinterpret_cast<const float4*>(
+                                stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
+                            const long long at = (at0 + quarter * 32 + rr) * D + 32 * c + 4 * cc;
+                            if (((rows_in >> rr) & 1) && in_bounds(at, 4, all_rows * D, a.status))
+                                __stcg(reinterpret_cast<float4*>(p.part_o + at), val);
                         }
+                        __syncwarp();
                     }
                 }
-                __threadfence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarPart));
                 if (warp == 4) {
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarPart), splits & 1, wc));
                     if (!ok) break;
                     if (lane == 0) {
-                        int last = 0;
-                        __threadfence();
-                        if (in_bounds(s.c_first, 1, kPagedMaxCtas, a.status)) {
-                            last = atomicAdd(p.counters + s.c_first, 1u) ==
-                                   static_cast<unsigned>(nc - 1);
-                            if (last) p.counters[s.c_first] = 0;
-                        }
-                        *last_flag = last;
+                        *last_flag = arrive_last(p, tile);
                         mbar_arrive(bar(kBarFlag));
                     }
                     __syncwarp();
@@ -704,61 +719,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarFlag), splits & 1, wc));
                 if (!ok) break;
                 ++splits;
-                write = joined = *last_flag != 0;
-                if (joined) {
-                    __threadfence();
-                    M = -INFINITY;
-                    L = 0.f;
-                    for (int c = 0; c < nc && valid && mine; ++c) {
-                        const long long r = part_of(s.c_first + c) * 2 * kSub + part_row;
-                        if (in_bounds(r, 1, n_rows, a.status))
-                            M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(p.part_stat) + r).x);
-                    }
-                }
-            }
-            if (write && mine) {
-                const long long n_elems = n_rows * D;
+                if (*last_flag)
+                    join_rows<__nv_bfloat16, D / 4, 1, 8, 2>(
+                        p, tile, warp - 4, 8, 2 * kSub,
+                        [&](int r) { return r < sub_rows ? r : kSub + r - sub_rows; });
+            } else if (mine) {
+                // Rows leave through the staging slice too, half of the columns at a time: a
+                // thread writes its row's 16-byte chunk c at slot c ^ (row mod kChunks).
                 constexpr int kHalf = D / 2;
                 constexpr int kChunks = kHalf / 8;             // 16-byte chunks per staged row
                 constexpr int kRowsPerStore = 32 / kChunks;
-                uint8_t* stage = smem + Lay::kStage + (warp - 4) * 32 * (2 * kHalf);
+                const float inv = l == 0.f ? 0.f : 1.f / l;    // a row that saw no key: 0
+                const long long my_row = valid ? out_row(p, tile, in_tile) : -1;
 #pragma unroll 1
                 for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll 1
+#pragma unroll
                     for (int c = 0; c < kHalf / 32; ++c) {
-                        const int col = hh * kHalf + 32 * c;
-                        float o[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0.f;
-                        if (joined) {
-                            L = 0.f;
-                            for (int k = 0; k < nc && valid; ++k) {
-                                const long long sl = part_of(s.c_first + k);
-                                const long long r = sl * 2 * kSub + part_row;
-                                if (!in_bounds(r, 1, n_rows, a.status)) continue;
-                                const float2 st =
-                                    __ldcg(reinterpret_cast<const float2*>(p.part_stat) + r);
-                                if (st.y == 0.f) continue;
-                                const float w = part_weight(st.x, st.y, M);
-                                L = fmaf(w, st.y, L);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    const long long at = (sl * D + col + j) * 2 * kSub + part_row;
-                                    if (in_bounds(at, 1, n_elems, a.status))
-                                        o[j] = fmaf(w, __ldcg(p.part_o + at), o[j]);
-                                }
-                            }
-                        } else if (!empty) {
-                            uint32_t raw[32];
-                            tmem_ld32(tO + col, raw);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = u2f(raw[j]);
-                        }
-                        const float inv = L == 0.f ? 0.f : 1.f / L;
+                        uint32_t o[32] = {};
+                        if (!empty) tmem_ld32(tO + hh * kHalf + 32 * c, o);
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            pk[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+                            pk[j] = pack_bf16x2(u2f(o[2 * j]) * inv, u2f(o[2 * j + 1]) * inv);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int sl = (4 * c + j) ^ (lane & (kChunks - 1));
@@ -781,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 if (valid && a.lse != nullptr && in_bounds(my_row, 1, a.lse_elems, a.status))
-                    a.lse[my_row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
+                    a.lse[my_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPagedLn2;
             }
         }
     }
@@ -802,8 +784,10 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     const cudaError_t e = resident_ctas(known, paged_tc_kernel<D>, kThreads, Layout<D>::kSmem, &grid);
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedTcCtas ? grid : kPagedTcCtas;
-    p.min_chunk = 2 * kKeys;
-    p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
+    p.key_cost = 8;
+    p.key_cost_single = D == 64 ? 5 : 7;
+    p.tile_cost = 256 * p.key_cost;
+    p.min_chunk = 2 * kKeys * p.key_cost;
     const PagedWorkspace w = paged_workspace_of(p.grid, 2 * kSub, D);
     uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
     p.counters = reinterpret_cast<unsigned int*>(ws);
@@ -827,9 +811,7 @@ bool paged_tc_applies(const PagedArgs& a)
 cudaError_t launch_paged_tc(const PagedArgs& a)
 {
     PagedParams p;
-    p.a = a;
-    p.G = a.H / a.H_kv;
-    p.page_shift = page_shift_of(a.page_size);
+    fill_params(&p, a);
     const int sub_tokens = kSub / p.G;
     p.tile_tokens = 2 * sub_tokens;
     using ull = unsigned long long;

@@ -4,10 +4,10 @@
 // A tile is the query rows of one key/value head that one CTA holds at a time: the new
 // tokens of a sequence times the H / H_kv query heads that read the head, packed
 // token-major ("packed row" r is token r / G, head r % G of the group).  The tiles of a
-// call are laid end to end, sequence by sequence, head by head, on one axis whose unit is
-// a visited key, each tile kTileCost + its keys long, and CTA c takes the part
-// [c chunk, (c + 1) chunk) of that axis: whatever the lengths are, every CTA reads the
-// same number of keys, and one token over a long cache fills the whole GPU.  Everything is
+// call are laid end to end, sequence by sequence, head by head, on one axis of cost, each
+// tile as long as its fixed cost and its keys times a weight, and CTA c takes the part
+// [c chunk, (c + 1) chunk) of that axis: whatever the lengths are, every CTA does the same
+// work, and one token over a long cache fills the whole GPU.  Everything is
 // computed from the lengths on the device in each CTA (a scan over the sequences), so a
 // captured call follows the lengths that it finds when it is replayed.
 //
@@ -25,16 +25,24 @@
 namespace ra {
 
 constexpr float kPagedLn2 = 0.6931471805599453f;
-constexpr int kTileCost = 64;       // a tile's fixed cost (its queries and output), in keys
-
 // Kernel-side copy of PagedArgs, with the split.
 struct PagedParams {
     PagedArgs a;
     int G;                  // query heads per key/value head
     int grid;
-    int min_chunk;          // smallest part worth a CTA, in keys
+    int min_chunk;          // smallest part worth a CTA, in cost
+    int tile_cost;          // a tile's fixed cost (its queries and output)
+    int key_cost;           // of a key
+    int key_cost_single;    // StepTiles: of a key of a tile with one sub-tile of rows
     int tile_tokens;        // new tokens of a tile (StepTiles)
     int page_shift;         // log2 of the page size, or -1
+    unsigned g_magic;       // division by G: see token_of
+    int g_shift;
+    // r / G of a packed row (r < 2^31), by multiplication
+    __device__ __forceinline__ int token_of(int r) const
+    {
+        return static_cast<int>((__umulhi(static_cast<unsigned>(r), g_magic) + r) >> g_shift);
+    }
     float scale_log2;       // log2(e) / sqrt(D): scores in base-2 units
     unsigned int* counters; // [kPagedMaxCtas], zero between calls
     float* part_stat;       // [2 grid][rows][2]: maximum, denominator
@@ -55,11 +63,22 @@ inline PagedWorkspace paged_workspace_of(int ctas, int rows, int D)
     return w;
 }
 
-inline int page_shift_of(int page_size)
+// The parts of the parameters that every kernel fills alike.
+inline void fill_params(PagedParams* p, const PagedArgs& a)
 {
+    p->a = a;
+    p->G = a.H / a.H_kv;
     int k = 0;
-    while ((1 << k) < page_size) ++k;
-    return (1 << k) == page_size ? k : -1;
+    while ((1ll << k) < a.page_size) ++k;
+    p->page_shift = (1ll << k) == a.page_size ? k : -1;
+    // ceil(2^(32 + s) / G) - 2^32 with 2^s >= G: r / G = (r + hi(r magic)) >> s exactly for
+    // r < 2^31 (the sum does not overflow, and the error r e / (G 2^(32 + s)), e < G <= 2^s,
+    // stays below 1 / G)
+    int s = 0;
+    while ((1ll << s) < p->G) ++s;
+    p->g_shift = s;
+    p->g_magic = static_cast<unsigned>((((1ull << s) - p->G) << 32) / p->G + 1);
+    p->scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.D));
 }
 
 // The new tokens and keys of sequence g, clamped to what the call's tensors hold.
@@ -97,47 +116,56 @@ struct FlatTiles {
     __device__ __forceinline__ void init(const PagedParams& p, const SeqSpan& s)
     {
         n_tiles = (s.n * p.G + kRows - 1) / kRows;        // n G <= T H < 2^31 - 16
-        cost = kTileCost + s.kv;
+        cost = p.tile_cost + static_cast<long long>(s.kv) * p.key_cost;
     }
     __device__ __forceinline__ long long prefix(int j) const { return j * cost; }
     __device__ __forceinline__ int at(long long x) const { return static_cast<int>(quotient(x, cost)); }
+    __device__ __forceinline__ int weight(const PagedParams& p, int) const { return p.key_cost; }
 };
 
 // The same where a sequence may have many tiles: under the causal rule tile j of `per` tokens
 // sees (up to) the keys before the new tokens and the first (j + 1) per of those, so a
 // sequence's costs form an arithmetic series, summed in closed form and searched by halving.
+// Its last tile may have one sub-tile of rows only, whose keys cost less.
 struct StepTiles {
-    int n_tiles, per, n, kv, causal;
-    long long before;       // keys before the new tokens
+    int n_tiles, per, fixed, wide, last_weight;
+    long long seen, last_keys;      // keys of tile j < n_tiles - 1: seen + j step; of the last
+    int step;
     __device__ __forceinline__ static int rows(const PagedParams& p) { return p.tile_tokens * p.G; }
     __device__ __forceinline__ void init(const PagedParams& p, const SeqSpan& s)
     {
         per = p.tile_tokens;
-        n = s.n;
-        kv = s.kv;
-        causal = p.a.causal;
-        before = max(s.kv - s.n, 0);
         n_tiles = (s.n + per - 1) / per;
+        fixed = p.tile_cost;
+        wide = p.key_cost;
+        const long long before = max(s.kv - s.n, 0);
+        step = p.a.causal ? per : 0;
+        seen = p.a.causal ? before + per : s.kv;
+        last_keys = p.a.causal ? before + s.n : s.kv;
+        last_weight = 2 * (s.n - (n_tiles - 1) * per) <= per ? p.key_cost_single : wide;
     }
     __device__ __forceinline__ long long prefix(int j) const
     {
-        if (!causal) return j * (static_cast<long long>(kTileCost) + kv);
-        // full tiles before j, and the last one, which ends with the last token
-        long long c = j * (kTileCost + before);
+        if (n_tiles == 0) return 0;
         const long long full = j < n_tiles ? j : n_tiles - 1;
-        c += per * (full * (full + 1) / 2);
-        return j < n_tiles ? c : c + n;
+        const long long keys = full * seen + step * (full * (full - 1) / 2);
+        const long long c = static_cast<long long>(j) * fixed + keys * wide;
+        return j < n_tiles ? c : c + last_keys * last_weight;
     }
     __device__ __forceinline__ int at(long long x) const
     {
-        if (!causal) return static_cast<int>(quotient(x, static_cast<long long>(kTileCost) + kv));
         int lo = 0, hi = n_tiles;               // prefix(lo) <= x < prefix(hi)
+#pragma unroll 1
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (prefix(mid) <= x) lo = mid;
             else hi = mid;
         }
         return lo;
+    }
+    __device__ __forceinline__ int weight(const PagedParams&, int j) const
+    {
+        return j + 1 < n_tiles ? wide : last_weight;
     }
 };
 
@@ -169,14 +197,15 @@ struct PagedWalk {
         head_cost = tiles.prefix(tiles.n_tiles);
         seq_cost = head_cost * p.a.H_kv;
     }
-    // keys before the cut at offset x of a tile that has `keys` keys and cost `cost`
-    __device__ __forceinline__ static int cut(long long x, long long cost, int keys)
+    // keys before the cut at offset x of a tile that has `keys` keys of the given weight
+    __device__ __forceinline__ static int cut(long long x, long long cost, int keys, int fixed,
+                                              int weight)
     {
-        if (x <= 0) return 0;
         if (x >= cost) return keys;
-        const long long k = x - kTileCost;
+        const long long k = x - fixed;
         if (k <= 0) return 0;
-        return static_cast<int>(min(static_cast<long long>(keys), k / kUnit * kUnit));
+        return static_cast<int>(
+            min(static_cast<long long>(keys), quotient(k, weight) / kUnit * kUnit));
     }
     __device__ __forceinline__ bool next(const PagedParams& p, Segment& t)
     {
@@ -197,11 +226,12 @@ struct PagedWalk {
         t.row0 = j * rows;
         t.rows = min(rows, s.n * p.G - t.row0);
         // the last token of the tile sees the most keys
-        const int last = (t.row0 + t.rows - 1) / p.G;
+        const int last = p.token_of(t.row0 + t.rows - 1);
         t.keys = p.a.causal ? min(max(s.kv - s.n + last + 1, 0), s.kv) : s.kv;
         const long long stop = min(end, b);
-        t.k0 = cut(x - a, b - a, t.keys);
-        t.k1 = cut(stop - a, b - a, t.keys);
+        const int weight = tiles.weight(p, j);
+        t.k0 = cut(x - a, b - a, t.keys, p.tile_cost, weight);
+        t.k1 = cut(stop - a, b - a, t.keys, p.tile_cost, weight);
         t.c_first = static_cast<int>(quotient(a, chunk));
         t.c_last = static_cast<int>(quotient(b - 1, chunk));
         x = stop;
@@ -303,15 +333,21 @@ __device__ __forceinline__ float part_weight(float m, float l, float M)
     return ex2(m - M);
 }
 
-// Output row of packed row r of a segment.
-__device__ __forceinline__ long long out_row(const PagedParams& p, const Segment& t, int r)
+// The rows of one tile, as far as its output needs them.
+struct TileRows {
+    int first, row0, rows, hk;      // the sequence's first token row; packed rows; head
+    int c_first, c_last;            // the CTAs that share the tile
+};
+
+// Output row of packed row r of a tile.
+__device__ __forceinline__ long long out_row(const PagedParams& p, const TileRows& t, int r)
 {
-    const int pr = t.row0 + r, tok = pr / p.G;
-    return static_cast<long long>(t.s.first + tok) * p.a.H + t.hk * p.G + (pr - tok * p.G);
+    const int pr = t.row0 + r, tok = p.token_of(pr);
+    return static_cast<long long>(t.first + tok) * p.a.H + t.hk * p.G + (pr - tok * p.G);
 }
 
 template <typename T>
-__device__ __forceinline__ void write_row4(const PagedParams& p, const Segment& t, int r, int c4,
+__device__ __forceinline__ void write_row4(const PagedParams& p, const TileRows& t, int r, int c4,
                                            float4 o, float M, float L)
 {
     const float inv = L == 0.f ? 0.f : 1.f / L;       // a row that saw no key: 0 and -inf
@@ -323,14 +359,120 @@ __device__ __forceinline__ void write_row4(const PagedParams& p, const Segment& 
         p.a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
 }
 
+// Where CTA `cta` keeps its partial of tile t: slot 1 if the tile begins in its part and
+// runs on, slot 0 if it began before.
+__device__ __forceinline__ long long part_slot(const TileRows& t, int cta)
+{
+    return 2ll * cta + (cta == t.c_first ? 1 : 0);
+}
+
+// Counts this CTA in as a contributor of tile t (one thread, the CTA's partial being written
+// and ordered before by a barrier); true in the last one.
+__device__ __forceinline__ bool arrive_last(const PagedParams& p, const TileRows& t)
+{
+    bool last = false;
+    __threadfence();
+    if (in_bounds(t.c_first, 1, kPagedMaxCtas, p.a.status)) {
+        last = atomicAdd(p.counters + t.c_first, 1u) ==
+               static_cast<unsigned>(t.c_last - t.c_first);
+        if (last) p.counters[t.c_first] = 0;           // as the next call expects it
+    }
+    __threadfence();
+    return last;
+}
+
+// The tile's output from all contributors' partials, joined one after the other in CTA order
+// (the running maximum and sum of the softmax once more), by warp `warp` of n_warps.  kLanes
+// lanes share a row (four columns each, and kVec4 times that); kRowsAt times 32 / kLanes rows
+// and kDeep contributors are read at once: a read takes a microsecond while the rest of the
+// GPU streams.  slot_rows: rows a partial slot has; place(r): the row of a slot that holds
+// packed row r.
+template <typename T, int kLanes, int kVec4, int kRowsAt, int kDeep, typename Place>
+__device__ void join_rows(const PagedParams& p, const TileRows& t, int warp, int n_warps,
+                          int slot_rows, Place place)
+{
+    constexpr int kAbreast = 32 / kLanes;
+    const int lane = threadIdx.x & 31, col = lane % kLanes;
+    const int step = n_warps * kAbreast;
+    const int D = p.a.D;
+    const int nc = t.c_last - t.c_first + 1;
+    const unsigned all_rows = 2u * p.grid * slot_rows;
+#pragma unroll 1
+    for (int r0 = warp * kAbreast + lane / kLanes; r0 - lane / kLanes < t.rows; r0 += step * kRowsAt) {
+        float M[kRowsAt], L[kRowsAt];
+        float4 acc[kRowsAt][kVec4];
+        unsigned at0[kRowsAt];                         // row of contributor 0 if it had slot 0
+#pragma unroll
+        for (int b = 0; b < kRowsAt; ++b) {
+            M[b] = -INFINITY;
+            L[b] = 0.f;
+            const int r = r0 + b * step;
+            at0[b] = 2u * t.c_first * slot_rows + place(r < t.rows ? r : 0);
+#pragma unroll
+            for (int u = 0; u < kVec4; ++u) acc[b][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int k = 0; k < nc; k += kDeep) {
+            float2 st[kDeep][kRowsAt];
+            float4 o[kDeep][kRowsAt][kVec4];
+#pragma unroll
+            for (int e = 0; e < kDeep; ++e)
+#pragma unroll
+                for (int b = 0; b < kRowsAt; ++b) {
+                    // contributor 0 has slot 1 of its CTA, the others slot 0 of theirs
+                    const unsigned at = at0[b] + (k + e == 0 ? 1u : 2u * (k + e)) * slot_rows;
+                    const bool real = k + e < nc && r0 + b * step < t.rows &&
+                                      in_bounds(at, 1, all_rows, p.a.status);
+                    st[e][b] = make_float2(-INFINITY, 0.f);
+                    if (real) st[e][b] = __ldcg(reinterpret_cast<const float2*>(p.part_stat) + at);
+                    const float4* src = reinterpret_cast<const float4*>(
+                        p.part_o + static_cast<unsigned long long>(at) * D) + col;
+#pragma unroll
+                    for (int u = 0; u < kVec4; ++u) {
+                        o[e][b][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (real && 4 * (col + kLanes * u) < D) o[e][b][u] = __ldcg(src + kLanes * u);
+                    }
+                }
+#pragma unroll
+            for (int e = 0; e < kDeep; ++e)
+#pragma unroll
+                for (int b = 0; b < kRowsAt; ++b) {
+                    const float2 x = st[e][b];
+                    if (x.y == 0.f) continue;          // no contributor, or one without keys
+                    const float Mn = fmaxf(M[b], x.x);
+                    const float old = part_weight(M[b], L[b], Mn), w = part_weight(x.x, x.y, Mn);
+                    M[b] = Mn;
+                    L[b] = L[b] == 0.f ? w * x.y : fmaf(L[b], old, w * x.y);
+#pragma unroll
+                    for (int u = 0; u < kVec4; ++u) {
+                        acc[b][u].x = fmaf(acc[b][u].x, old, w * o[e][b][u].x);
+                        acc[b][u].y = fmaf(acc[b][u].y, old, w * o[e][b][u].y);
+                        acc[b][u].z = fmaf(acc[b][u].z, old, w * o[e][b][u].z);
+                        acc[b][u].w = fmaf(acc[b][u].w, old, w * o[e][b][u].w);
+                    }
+                }
+        }
+#pragma unroll
+        for (int b = 0; b < kRowsAt; ++b) {
+            const int r = r0 + b * step;
+            if (r >= t.rows) continue;
+#pragma unroll
+            for (int u = 0; u < kVec4; ++u)
+                if (4 * (col + kLanes * u) < D)
+                    write_row4<T>(p, t, r, col + kLanes * u, acc[b][u], M[b], L[b]);
+        }
+    }
+}
+
 // End of a segment, by the whole block: buf[rows][ldo] holds the CTA's unnormalised sums
 // and stat[rows] = (maximum in base-2 units, denominator).  Writes the tile's output, or
 // the CTA's partial and, in the last CTA of the tile, the joined output.
 template <typename T, int kRows, int kThreads, int kVec4 = 1>
-__device__ void finish_segment(const PagedParams& p, const Segment& t, const float* buf, int ldo,
+__device__ void finish_segment(const PagedParams& p, const Segment& seg, const float* buf, int ldo,
                                const float2* stat, int* flag)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const TileRows t{seg.s.first, seg.row0, seg.rows, seg.hk, seg.c_first, seg.c_last};
+    const int tid = threadIdx.x;
     const int v4 = p.a.D / 4;
     if (t.c_first == t.c_last) {
         for (int i = tid; i < t.rows * v4; i += kThreads) {
@@ -341,101 +483,25 @@ __device__ void finish_segment(const PagedParams& p, const Segment& t, const flo
         __syncthreads();
         return;
     }
-    // slot 1: the tile begins in this CTA's part and runs on; slot 0: it began before
-    const int c = blockIdx.x;
-    auto slot_of = [&](int cta) { return 2 * cta + (cta == t.c_first ? 1 : 0); };
-    const long long n_slots = 2ll * p.grid;
-    {
-        const long long slot = slot_of(c);
-        for (int r = tid; r < t.rows; r += kThreads)
-            if (in_bounds(slot * kRows + r, 1, n_slots * kRows, p.a.status))
-                __stcg(reinterpret_cast<float2*>(p.part_stat) + slot * kRows + r, stat[r]);
-        if (t.k1 > t.k0) {
-            for (int i = tid; i < t.rows * v4; i += kThreads) {
-                const int r = i / v4, cc = i - r * v4;
-                const long long at = (slot * kRows + r) * p.a.D + 4 * cc;
-                if (in_bounds(at, 4, n_slots * kRows * p.a.D, p.a.status))
-                    __stcg(reinterpret_cast<float4*>(p.part_o + at),
-                           *reinterpret_cast<const float4*>(buf + r * ldo + 4 * cc));
-            }
+    const long long all_rows = 2ll * p.grid * kRows;
+    const long long at0 = part_slot(t, blockIdx.x) * kRows;
+    for (int r = tid; r < t.rows; r += kThreads)
+        if (in_bounds(at0 + r, 1, all_rows, p.a.status))
+            __stcg(reinterpret_cast<float2*>(p.part_stat) + at0 + r, stat[r]);
+    if (seg.k1 > seg.k0) {
+        for (int i = tid; i < t.rows * v4; i += kThreads) {
+            const int r = i / v4, cc = i - r * v4;
+            const long long at = (at0 + r) * p.a.D + 4 * cc;
+            if (in_bounds(at, 4, all_rows * p.a.D, p.a.status))
+                __stcg(reinterpret_cast<float4*>(p.part_o + at),
+                       *reinterpret_cast<const float4*>(buf + r * ldo + 4 * cc));
         }
-    }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        const unsigned n = static_cast<unsigned>(t.c_last - t.c_first + 1);
-        int last = 0;
-        if (in_bounds(t.c_first, 1, kPagedMaxCtas, p.a.status)) {
-            last = atomicAdd(p.counters + t.c_first, 1u) == n - 1;
-            if (last) p.counters[t.c_first] = 0;       // as the next call expects it
-        }
-        *flag = last;
     }
     __syncthreads();
-    if (*flag) {
-        __threadfence();
-        const int nc = t.c_last - t.c_first + 1;
-        // kVec4 float4 per lane: D <= 128 kVec4
-        for (int r = warp; r < t.rows; r += kThreads / 32) {
-            auto stat_at = [&](int i) -> float2 {
-                const long long at = static_cast<long long>(slot_of(t.c_first + i)) * kRows + r;
-                if (i >= nc || !in_bounds(at, 1, n_slots * kRows, p.a.status))
-                    return make_float2(-INFINITY, 0.f);
-                return __ldcg(reinterpret_cast<const float2*>(p.part_stat) + at);
-            };
-            const float2 mine = stat_at(lane);             // of the first 32 contributors
-            float M = mine.x;
-            for (int i0 = 32; i0 < nc; i0 += 32) M = fmaxf(M, stat_at(i0 + lane).x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            float L = 0.f;
-            float4 acc[kVec4];
-#pragma unroll
-            for (int u = 0; u < kVec4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-            for (int i0 = 0; i0 < nc; i0 += 32) {
-                const float2 st = i0 == 0 ? mine : stat_at(i0 + lane);
-                const float w = part_weight(st.x, st.y, M);
-                L += st.y == 0.f ? 0.f : w * st.y;
-                const unsigned have = __ballot_sync(0xffffffffu, !(st.y == 0.f));
-                const int cnt = min(32, nc - i0);
-                // eight contributors' sums in flight; an empty one wrote none
-#pragma unroll 1
-                for (int i = 0; i < cnt; i += 8) {
-                    float4 o[8][kVec4];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const long long at =
-                            (static_cast<long long>(slot_of(t.c_first + i0 + i + e)) * kRows + r) * p.a.D;
-#pragma unroll
-                        for (int u = 0; u < kVec4; ++u) {
-                            const int cc = lane + 32 * u;
-                            o[e][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (i + e < cnt && ((have >> (i + e)) & 1) && cc < v4 &&
-                                in_bounds(at + 4 * cc, 4, n_slots * kRows * p.a.D, p.a.status))
-                                o[e][u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at + 4 * cc));
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float wi = __shfl_sync(0xffffffffu, w, (i + e) & 31);
-#pragma unroll
-                        for (int u = 0; u < kVec4; ++u) {
-                            acc[u].x = fmaf(wi, o[e][u].x, acc[u].x);
-                            acc[u].y = fmaf(wi, o[e][u].y, acc[u].y);
-                            acc[u].z = fmaf(wi, o[e][u].z, acc[u].z);
-                            acc[u].w = fmaf(wi, o[e][u].w, acc[u].w);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-#pragma unroll
-            for (int u = 0; u < kVec4; ++u)
-                if (lane + 32 * u < v4) write_row4<T>(p, t, r, lane + 32 * u, acc[u], M, L);
-        }
-    }
+    if (tid == 0) *flag = arrive_last(p, t);
+    __syncthreads();
+    if (*flag)
+        join_rows<T, 32, kVec4, 1, 8>(p, t, tid >> 5, kThreads / 32, kRows, [](int r) { return r; });
     __syncthreads();
 }
 
