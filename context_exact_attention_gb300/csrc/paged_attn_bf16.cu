@@ -41,8 +41,7 @@ struct Smem {
     static constexpr int kBuf = kStages * kStage;
     static constexpr int kStatW = kBuf + kRows * kLdo * 4;
     static constexpr int kStat = kStatW + kWarps * kRows * 8;
-    static constexpr int kScratch = kStat + kRows * 8;
-    static constexpr int kFlag = kScratch + 34 * 8;
+    static constexpr int kFlag = kStat + kRows * 8;
     static constexpr int kBytes = kFlag + 16;
 };
 
@@ -94,7 +93,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
     float* buf = reinterpret_cast<float*>(smem + S::kBuf);
     float2* stat_w = reinterpret_cast<float2*>(smem + S::kStatW);
     float2* stat = reinterpret_cast<float2*>(smem + S::kStat);
-    long long* scratch = reinterpret_cast<long long*>(smem + S::kScratch);
     int* flag = reinterpret_cast<int*>(smem + S::kFlag);
     const PagedArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -104,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
     const uint32_t ring = smem_addr(smem) + warp * 2 * S::kTile;
 
     Walk walk;
-    walk.begin<kThreads>(p, scratch);
+    walk.begin(p);
     Segment t{}, nt{};                          // the segment being multiplied, the next one
     bool have = false, have_next = walk.next(p, nt);
     // The copies: step `lk` of segment nt (in_next) or t, up to kStages steps ahead of the
@@ -336,6 +334,7 @@ cudaError_t launch_d(PagedParams& p)
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.tile_cost = 64;
     p.key_cost = 1;
+    p.snap = 2 * kUnit;
     p.min_chunk = 2 * kUnit;
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, D);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);

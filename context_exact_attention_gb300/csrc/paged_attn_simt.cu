@@ -31,7 +31,6 @@ template <int kVec4>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedParams p)
 {
     using Walk = PagedWalk<FlatTiles<kRows>, kUnit>;
-    __shared__ long long scratch[34];
     __shared__ float2 stat_w[kWarps][kRows];
     __shared__ float2 stat[kRows];
     __shared__ int flag;
@@ -44,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     const float* V = static_cast<const float*>(a.v_pages);
 
     Walk walk;
-    walk.begin<kThreads>(p, scratch);
+    walk.begin(p);
     Segment t;
     while (walk.next(p, t)) {
         float4 q[kRows][kVec4], o[kRows][kVec4];
@@ -207,6 +206,7 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.tile_cost = 64;
     p.key_cost = 1;
+    p.snap = 2 * kUnit;
     p.min_chunk = 4 * kUnit;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, a.D);

@@ -49,7 +49,7 @@ struct Layout {
     static constexpr int kStage = kV + kStages * kTile;   // 8 warps x 32 rows x D/2 bf16
     // (a slice holds 32 rows of 32 floats or of D/2 bf16)
     static constexpr int kBar = kStage + 8 * 32 * 128;
-    static constexpr int kSmem = kBar + 2048 + 1024;  // barriers, scratch; alignment slack
+    static constexpr int kSmem = kBar + 2048 + 1024;  // barriers, segments; alignment slack
     __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
     __device__ static constexpr uint32_t col_o(int t) { return 256u + static_cast<uint32_t>(D) * t; }
 };
@@ -77,8 +77,7 @@ enum : int {
 constexpr int kTmemSlot = kBarCount * 8, kAbort = kTmemSlot + 4, kLast = kTmemSlot + 8;
 constexpr int kSegInts = 14;
 constexpr int kSegSlots = kTmemSlot + 16;                   // 2 slots of kSegInts ints
-constexpr int kScratch = (kSegSlots + 2 * kSegInts * 4 + 7) / 8 * 8;
-constexpr int kOddStat = kScratch + 34 * 8;                 // 128 x (maximum, denominator)
+constexpr int kOddStat = (kSegSlots + 2 * kSegInts * 4 + 7) / 8 * 8;   // 128 x (maximum, denominator)
 static_assert(kOddStat + kSub * 8 <= 2048, "barrier area");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -152,7 +151,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* abort_flag = reinterpret_cast<int*>(area + kAbort);
     volatile int* last_flag = reinterpret_cast<volatile int*>(area + kLast);
     volatile int* seg_slot = reinterpret_cast<volatile int*>(area + kSegSlots);
-    long long* scratch = reinterpret_cast<long long*>(area + kScratch);
     auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
     const PagedArgs& a = p.a;
     const int warp = threadIdx.x >> 5;
@@ -190,8 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
         tc_fence_before();
     }
-    Walk walk;
-    walk.begin<kThreads>(p, scratch);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -270,6 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t q_loads[2] = {0, 0};                         // query loads per sub-tile so far
         bool ok = true;
         Segment t;
+        Walk walk;
+        walk.begin(p);
         for (int i = 0; ok; ++i) {
             const bool more = walk.next(p, t);
             Seg s{};
@@ -787,6 +785,7 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     p.key_cost = 8;
     p.key_cost_single = D == 64 ? 5 : 7;
     p.tile_cost = 256 * p.key_cost;
+    p.snap = 3 * kKeys;
     p.min_chunk = 2 * kKeys * p.key_cost;
     const PagedWorkspace w = paged_workspace_of(p.grid, 2 * kSub, D);
     uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);

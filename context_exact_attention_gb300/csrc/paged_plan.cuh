@@ -8,7 +8,7 @@
 // tile as long as its fixed cost and its keys times a weight, and CTA c takes the part
 // [c chunk, (c + 1) chunk) of that axis: whatever the lengths are, every CTA does the same
 // work, and one token over a long cache fills the whole GPU.  Everything is
-// computed from the lengths on the device in each CTA (a scan over the sequences), so a
+// computed from the lengths on the device in each warp (a scan over the sequences), so a
 // captured call follows the lengths that it finds when it is replayed.
 //
 // A tile that lies in one CTA's part is written by that CTA.  Of a tile cut by a part's
@@ -31,6 +31,7 @@ struct PagedParams {
     int G;                  // query heads per key/value head
     int grid;
     int min_chunk;          // smallest part worth a CTA, in cost
+    int snap;               // shortest piece of a cut tile, in keys
     int tile_cost;          // a tile's fixed cost (its queries and output)
     int key_cost;           // of a key
     int key_cost_single;    // StepTiles: of a key of a tile with one sub-tile of rows
@@ -197,89 +198,89 @@ struct PagedWalk {
         head_cost = tiles.prefix(tiles.n_tiles);
         seq_cost = head_cost * p.a.H_kv;
     }
-    // keys before the cut at offset x of a tile that has `keys` keys of the given weight
-    __device__ __forceinline__ static int cut(long long x, long long cost, int keys, int fixed,
-                                              int weight)
+    // Keys before the cut at offset x of a tile that has `keys` keys of the given weight: whole
+    // steps of the kernel, and no piece at either end shorter than `snap` keys (a piece costs a
+    // partial result and its share of the joining).
+    __device__ __forceinline__ static int cut(long long x, int keys, int fixed, int weight, int snap)
     {
-        if (x >= cost) return keys;
         const long long k = x - fixed;
         if (k <= 0) return 0;
-        return static_cast<int>(
-            min(static_cast<long long>(keys), quotient(k, weight) / kUnit * kUnit));
+        const long long n = quotient(k, weight) / kUnit * kUnit;
+        if (n < snap) return 0;
+        return n > keys - snap ? keys : static_cast<int>(n);
     }
     __device__ __forceinline__ bool next(const PagedParams& p, Segment& t)
     {
-        if (x >= end) return false;
-        while (x >= seq0 + seq_cost) {
-            seq0 += seq_cost;
-            if (++g >= p.a.n_seqs) return false;
-            load_seq(p);
+#pragma unroll 1
+        while (x < end) {
+            while (x >= seq0 + seq_cost) {
+                seq0 += seq_cost;
+                if (++g >= p.a.n_seqs) return false;
+                load_seq(p);
+            }
+            const long long rel = x - seq0;
+            t.hk = static_cast<int>(quotient(rel, head_cost));
+            const long long head0 = t.hk * head_cost;
+            const int j = tiles.at(rel - head0);
+            const long long a = seq0 + head0 + tiles.prefix(j), b = seq0 + head0 + tiles.prefix(j + 1);
+            t.g = g;
+            t.s = s;
+            const int rows = Tiles::rows(p);
+            t.row0 = j * rows;
+            t.rows = min(rows, s.n * p.G - t.row0);
+            // the last token of the tile sees the most keys
+            const int last = p.token_of(t.row0 + t.rows - 1);
+            t.keys = p.a.causal ? min(max(s.kv - s.n + last + 1, 0), s.kv) : s.kv;
+            const int weight = tiles.weight(p, j);
+            const int snap = static_cast<int>(
+                min(static_cast<long long>(p.snap), quotient(chunk, 4 * weight)));
+            // The CTAs that touch the tile, without those whose piece has no keys (only the
+            // first and the last can have none); the first keeps a tile without keys.
+            t.c_first = static_cast<int>(quotient(a, chunk));
+            t.c_last = static_cast<int>(quotient(b - 1, chunk));
+            const int c = blockIdx.x;
+            auto before = [&](int cta) -> int {             // keys before that CTA's part
+                return cta <= t.c_first ? 0
+                       : cta > t.c_last ? t.keys
+                                        : cut(cta * chunk - a, t.keys, p.tile_cost, weight, snap);
+            };
+            t.k0 = before(c);
+            t.k1 = before(c + 1);
+            const int first = t.c_first, top = t.c_last;
+            const bool first_empty = first < top && before(first + 1) == 0 && t.keys > 0;
+            const bool last_empty = first < top && (before(top) == t.keys || t.keys == 0);
+            if (first_empty) ++t.c_first;
+            if (last_empty && t.c_last > t.c_first) --t.c_last;
+            x = min(end, b);
+            if (t.keys == 0) t.c_last = t.c_first;
+            if (c >= t.c_first && c <= t.c_last) return true;
         }
-        const long long rel = x - seq0;
-        t.hk = static_cast<int>(quotient(rel, head_cost));
-        const long long head0 = t.hk * head_cost;
-        const int j = tiles.at(rel - head0);
-        const long long a = seq0 + head0 + tiles.prefix(j), b = seq0 + head0 + tiles.prefix(j + 1);
-        t.g = g;
-        t.s = s;
-        const int rows = Tiles::rows(p);
-        t.row0 = j * rows;
-        t.rows = min(rows, s.n * p.G - t.row0);
-        // the last token of the tile sees the most keys
-        const int last = p.token_of(t.row0 + t.rows - 1);
-        t.keys = p.a.causal ? min(max(s.kv - s.n + last + 1, 0), s.kv) : s.kv;
-        const long long stop = min(end, b);
-        const int weight = tiles.weight(p, j);
-        t.k0 = cut(x - a, b - a, t.keys, p.tile_cost, weight);
-        t.k1 = cut(stop - a, b - a, t.keys, p.tile_cost, weight);
-        t.c_first = static_cast<int>(quotient(a, chunk));
-        t.c_last = static_cast<int>(quotient(b - 1, chunk));
-        x = stop;
-        return true;
+        return false;
     }
-    // The same in every thread of the block; scratch: 34 long longs of shared memory.
-    template <int kThreads>
-    __device__ void begin(const PagedParams& p, long long* scratch)
+    // The start of this CTA's part, found by each warp for itself: a lane sums the costs of
+    // its share of the sequences, a scan over the lanes tells whose share holds the start,
+    // and that lane looks for the sequence.
+    __device__ void begin(const PagedParams& p)
     {
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        constexpr int kWarps = kThreads / 32;
-        // pass 0 sums the costs; pass 1 finds the sequence at the start of this CTA's part
-        // (one round of loads when the sequences fit the block)
-        long long total = 0, mine = 0;
+        const int lane = threadIdx.x & 31;
         auto cost_of = [&](int i) -> long long {
-            if (i >= p.a.n_seqs) return 0;
             Tiles t;
             t.init(p, seq_span_of(p.a, i));
             return t.prefix(t.n_tiles) * p.a.H_kv;
         };
-        auto block_scan = [&](long long v, long long& sum) -> long long {   // exclusive
-            long long inc = v;
+        const int per = (p.a.n_seqs + 31) / 32;
+        const int first = min(lane * per, p.a.n_seqs), stop = min(first + per, p.a.n_seqs);
+        long long sum = 0;
+#pragma unroll 2
+        for (int i = first; i < stop; ++i) sum += cost_of(i);
+        long long inc = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            __syncthreads();
-            if (lane == 31) scratch[warp] = inc;
-            __syncthreads();
-            long long before = 0;
-            sum = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const long long z = scratch[w];
-                if (w < warp) before += z;
-                sum += z;
-            }
-            return before + inc - v;
-        };
-        long long excl = 0;
-        for (int base = 0; base < p.a.n_seqs; base += kThreads) {
-            mine = cost_of(base + tid);
-            long long sum;
-            excl = block_scan(mine, sum);
-            total += sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
         }
-        chunk = max((total + p.grid - 1) / p.grid, static_cast<long long>(p.min_chunk));
+        const long long total = __shfl_sync(0xffffffffu, inc, 31);
+        chunk = max(quotient(total + p.grid - 1, p.grid), static_cast<long long>(p.min_chunk));
         x = blockIdx.x * chunk;
         end = min(total, x + chunk);
         g = 0;
@@ -288,26 +289,20 @@ struct PagedWalk {
             x = end;                // nothing for this CTA
             return;
         }
-        if (tid == 0) scratch[32] = 0;
-        __syncthreads();
-        long long before = 0;
-        for (int base = 0; base < p.a.n_seqs; base += kThreads) {
-            long long sum = total;
-            if (p.a.n_seqs > kThreads) {
-                mine = cost_of(base + tid);
-                excl = block_scan(mine, sum);
+        long long at = inc - sum;
+        int i = first;
+        const bool holds = at <= x && x < inc;
+        if (holds) {
+#pragma unroll 1
+            for (; i < stop - 1; ++i) {
+                const long long c = cost_of(i);
+                if (x < at + c) break;
+                at += c;
             }
-            if (x >= before + excl && x < before + excl + mine) {
-                scratch[32] = base + tid;
-                scratch[33] = before + excl;
-            }
-            before += sum;
-            if (x < before) break;
         }
-        __syncthreads();
-        g = static_cast<int>(scratch[32]);
-        seq0 = scratch[33];
-        __syncthreads();
+        const int owner = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
+        g = __shfl_sync(0xffffffffu, i, owner);
+        seq0 = __shfl_sync(0xffffffffu, at, owner);
         load_seq(p);
     }
 };
