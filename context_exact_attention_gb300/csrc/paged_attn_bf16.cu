@@ -333,7 +333,7 @@ cudaError_t launch_d(PagedParams& p)
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.tile_cost = 64;
-    p.key_cost = 1;
+    p.key_shift = 0;
     p.snap = 2 * kUnit;
     p.min_chunk = 2 * kUnit;
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, D);

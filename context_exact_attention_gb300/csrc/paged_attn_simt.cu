@@ -205,7 +205,7 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.tile_cost = 64;
-    p.key_cost = 1;
+    p.key_shift = 0;
     p.snap = 2 * kUnit;
     p.min_chunk = 4 * kUnit;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);

@@ -782,11 +782,13 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     const cudaError_t e = resident_ctas(known, paged_tc_kernel<D>, kThreads, Layout<D>::kSmem, &grid);
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedTcCtas ? grid : kPagedTcCtas;
-    p.key_cost = 8;
-    p.key_cost_single = D == 64 ? 5 : 7;
-    p.tile_cost = 256 * p.key_cost;
+    // a block of a single sub-tile takes half the time of a double one at head dim 64 (1500
+    // cycles to 2700) and nearly the same at 128 (2300 to 2600: K and V loads bound it)
+    p.key_shift = 1;
+    p.key_shift_single = D == 64 ? 0 : 1;
+    p.tile_cost = 256 << p.key_shift;
     p.snap = 3 * kKeys;
-    p.min_chunk = 2 * kKeys * p.key_cost;
+    p.min_chunk = 2 * kKeys << p.key_shift;
     const PagedWorkspace w = paged_workspace_of(p.grid, 2 * kSub, D);
     uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
     p.counters = reinterpret_cast<unsigned int*>(ws);

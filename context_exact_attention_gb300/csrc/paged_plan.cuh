@@ -33,8 +33,8 @@ struct PagedParams {
     int min_chunk;          // smallest part worth a CTA, in cost
     int snap;               // shortest piece of a cut tile, in keys
     int tile_cost;          // a tile's fixed cost (its queries and output)
-    int key_cost;           // of a key
-    int key_cost_single;    // StepTiles: of a key of a tile with one sub-tile of rows
+    int key_shift;          // log2 of a key's cost
+    int key_shift_single;   // StepTiles: the same in a tile with one sub-tile of rows
     int tile_tokens;        // new tokens of a tile (StepTiles)
     int page_shift;         // log2 of the page size, or -1
     unsigned g_magic;       // division by G: see token_of
@@ -117,11 +117,11 @@ struct FlatTiles {
     __device__ __forceinline__ void init(const PagedParams& p, const SeqSpan& s)
     {
         n_tiles = (s.n * p.G + kRows - 1) / kRows;        // n G <= T H < 2^31 - 16
-        cost = p.tile_cost + static_cast<long long>(s.kv) * p.key_cost;
+        cost = p.tile_cost + (static_cast<long long>(s.kv) << p.key_shift);
     }
     __device__ __forceinline__ long long prefix(int j) const { return j * cost; }
     __device__ __forceinline__ int at(long long x) const { return static_cast<int>(quotient(x, cost)); }
-    __device__ __forceinline__ int weight(const PagedParams& p, int) const { return p.key_cost; }
+    __device__ __forceinline__ int shift(const PagedParams& p, int) const { return p.key_shift; }
 };
 
 // The same where a sequence may have many tiles: under the causal rule tile j of `per` tokens
@@ -129,7 +129,7 @@ struct FlatTiles {
 // sequence's costs form an arithmetic series, summed in closed form and searched by halving.
 // Its last tile may have one sub-tile of rows only, whose keys cost less.
 struct StepTiles {
-    int n_tiles, per, fixed, wide, last_weight;
+    int n_tiles, per, fixed, wide, last_shift;
     long long seen, last_keys;      // keys of tile j < n_tiles - 1: seen + j step; of the last
     int step;
     __device__ __forceinline__ static int rows(const PagedParams& p) { return p.tile_tokens * p.G; }
@@ -138,20 +138,20 @@ struct StepTiles {
         per = p.tile_tokens;
         n_tiles = (s.n + per - 1) / per;
         fixed = p.tile_cost;
-        wide = p.key_cost;
+        wide = p.key_shift;
         const long long before = max(s.kv - s.n, 0);
         step = p.a.causal ? per : 0;
         seen = p.a.causal ? before + per : s.kv;
         last_keys = p.a.causal ? before + s.n : s.kv;
-        last_weight = 2 * (s.n - (n_tiles - 1) * per) <= per ? p.key_cost_single : wide;
+        last_shift = 2 * (s.n - (n_tiles - 1) * per) <= per ? p.key_shift_single : wide;
     }
     __device__ __forceinline__ long long prefix(int j) const
     {
         if (n_tiles == 0) return 0;
         const long long full = j < n_tiles ? j : n_tiles - 1;
         const long long keys = full * seen + step * (full * (full - 1) / 2);
-        const long long c = static_cast<long long>(j) * fixed + keys * wide;
-        return j < n_tiles ? c : c + last_keys * last_weight;
+        const long long c = static_cast<long long>(j) * fixed + (keys << wide);
+        return j < n_tiles ? c : c + (last_keys << last_shift);
     }
     __device__ __forceinline__ int at(long long x) const
     {
@@ -164,9 +164,9 @@ struct StepTiles {
         }
         return lo;
     }
-    __device__ __forceinline__ int weight(const PagedParams&, int j) const
+    __device__ __forceinline__ int shift(const PagedParams&, int j) const
     {
-        return j + 1 < n_tiles ? wide : last_weight;
+        return j + 1 < n_tiles ? wide : last_shift;
     }
 };
 
@@ -191,21 +191,21 @@ struct PagedWalk {
     SeqSpan s;
     Tiles tiles;
 
-    __device__ __forceinline__ void load_seq(const PagedParams& p)
+    __device__ __forceinline__ void take_seq(const PagedParams& p)
     {
-        s = seq_span_of(p.a, g);
         tiles.init(p, s);
         head_cost = tiles.prefix(tiles.n_tiles);
         seq_cost = head_cost * p.a.H_kv;
     }
-    // Keys before the cut at offset x of a tile that has `keys` keys of the given weight: whole
+    // Keys before the cut at offset x of a tile that has `keys` keys of cost 2^shift: whole
     // steps of the kernel, and no piece at either end shorter than `snap` keys (a piece costs a
     // partial result and its share of the joining).
-    __device__ __forceinline__ static int cut(long long x, int keys, int fixed, int weight, int snap)
+    __device__ __forceinline__ static int cut(long long x, int keys, int fixed, int shift, int snap)
     {
         const long long k = x - fixed;
         if (k <= 0) return 0;
-        const long long n = quotient(k, weight) / kUnit * kUnit;
+        const long long n = (k >> shift) & -static_cast<long long>(kUnit);
+        static_assert((kUnit & (kUnit - 1)) == 0, "cuts at a power of two");
         if (n < snap) return 0;
         return n > keys - snap ? keys : static_cast<int>(n);
     }
@@ -216,7 +216,8 @@ struct PagedWalk {
             while (x >= seq0 + seq_cost) {
                 seq0 += seq_cost;
                 if (++g >= p.a.n_seqs) return false;
-                load_seq(p);
+                s = seq_span_of(p.a, g);
+                take_seq(p);
             }
             const long long rel = x - seq0;
             t.hk = static_cast<int>(quotient(rel, head_cost));
@@ -231,18 +232,18 @@ struct PagedWalk {
             // the last token of the tile sees the most keys
             const int last = p.token_of(t.row0 + t.rows - 1);
             t.keys = p.a.causal ? min(max(s.kv - s.n + last + 1, 0), s.kv) : s.kv;
-            const int weight = tiles.weight(p, j);
+            const int shift = tiles.shift(p, j);
             const int snap = static_cast<int>(
-                min(static_cast<long long>(p.snap), quotient(chunk, 4 * weight)));
+                min(static_cast<long long>(p.snap), chunk >> (shift + 2)));
             // The CTAs that touch the tile, without those whose piece has no keys (only the
             // first and the last can have none); the first keeps a tile without keys.
-            t.c_first = static_cast<int>(quotient(a, chunk));
-            t.c_last = static_cast<int>(quotient(b - 1, chunk));
             const int c = blockIdx.x;
+            t.c_first = a >= c * chunk ? c : static_cast<int>(quotient(a, chunk));
+            t.c_last = b <= (c + 1) * chunk ? c : static_cast<int>(quotient(b - 1, chunk));
             auto before = [&](int cta) -> int {             // keys before that CTA's part
                 return cta <= t.c_first ? 0
                        : cta > t.c_last ? t.keys
-                                        : cut(cta * chunk - a, t.keys, p.tile_cost, weight, snap);
+                                        : cut(cta * chunk - a, t.keys, p.tile_cost, shift, snap);
             };
             t.k0 = before(c);
             t.k1 = before(c + 1);
@@ -263,9 +264,11 @@ struct PagedWalk {
     __device__ void begin(const PagedParams& p)
     {
         const int lane = threadIdx.x & 31;
+        SeqSpan mine{0, 0, 0};      // the last sequence this lane looked at
         auto cost_of = [&](int i) -> long long {
+            mine = seq_span_of(p.a, i);
             Tiles t;
-            t.init(p, seq_span_of(p.a, i));
+            t.init(p, mine);
             return t.prefix(t.n_tiles) * p.a.H_kv;
         };
         const int per = (p.a.n_seqs + 31) / 32;
@@ -292,18 +295,21 @@ struct PagedWalk {
         long long at = inc - sum;
         int i = first;
         const bool holds = at <= x && x < inc;
-        if (holds) {
+        if (holds && per > 1) {
 #pragma unroll 1
-            for (; i < stop - 1; ++i) {
+            for (;; ++i) {
                 const long long c = cost_of(i);
-                if (x < at + c) break;
+                if (x < at + c || i == stop - 1) break;
                 at += c;
             }
         }
         const int owner = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
         g = __shfl_sync(0xffffffffu, i, owner);
         seq0 = __shfl_sync(0xffffffffu, at, owner);
-        load_seq(p);
+        s.first = __shfl_sync(0xffffffffu, mine.first, owner);
+        s.n = __shfl_sync(0xffffffffu, mine.n, owner);
+        s.kv = __shfl_sync(0xffffffffu, mine.kv, owner);
+        take_seq(p);
     }
 };
 
