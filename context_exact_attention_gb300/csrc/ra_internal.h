@@ -190,7 +190,8 @@ struct RopeArgs {
     const int* page_table;
     long long table_stride, table_elems, page_stride, token_stride, head_stride;
     int num_pages, page_size, max_pages;
-    int tokens;                    // tokens per block (set by the launch)
+    int tokens, step_t, step_h;    // tokens per block, and taken at once; heads at once (set
+                                   // by the launch)
     unsigned int* status;
     cudaStream_t stream;
 };
