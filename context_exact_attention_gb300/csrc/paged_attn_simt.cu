@@ -2,13 +2,14 @@
 //
 // One block holds four query rows of one key/value head in registers (a lane keeps four
 // consecutive columns of each) and its four warps walk the CTA's part of the keys in turns
-// of eight.  A key's row is read by a warp as one coalesced run straight into registers:
-// every element is used for four rows and never goes through shared memory.  The 32 dot
-// products of a turn (8 keys x 4 rows) are partial sums over columns in every lane; a
-// butterfly that halves the values at each step leaves the total of (key, row) in lane
-// 4 key + row with 31 shuffles, where reducing them one by one would take 160.  That lane
-// then owns the score: mask, maximum over the keys (three shuffles), exponential, and the
-// eight weights of a row are read back by shuffle for the value sum.
+// of eight.  A lane copies its own columns of a turn's keys and values into its warp's
+// shared-memory ring asynchronously, turns ahead (no lane reads another's copies, so nothing
+// is synchronised), and uses every element for four rows.  The 32 dot products of a turn (8
+// keys x 4 rows) are partial sums over columns in every lane; a butterfly that halves the
+// values at each step leaves the total of (key, row) in lane 4 key + row with 31 shuffles,
+// where reducing them one by one would take 160.  That lane then owns the score: mask,
+// maximum over the keys (three shuffles), exponential, and the eight weights of a row are
+// read back by shuffle for the value sum.
 //
 // What bounds it: bytes, for up to four rows a head.  A turn moves 8 keys (8 KB at D 128)
 // for about 400 warp instructions, which an SM issues in 100 cycles; HBM delivers them in
@@ -24,6 +25,12 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTurn = 8;                       // keys per warp and turn
 constexpr int kUnit = kTurn * kWarps;
+
+constexpr int kStages = 3;
+
+// A warp's ring: per stage the keys of a turn, then its values, float4 by lane.
+template <int kVec4>
+constexpr int kRing = kStages * 2 * kTurn * kVec4 * 32 * 16;
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
@@ -42,10 +49,63 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     const float* K = static_cast<const float*>(a.k_pages);
     const float* V = static_cast<const float*>(a.v_pages);
 
+    extern __shared__ __align__(16) uint8_t dyn[];
+    uint8_t* ring = dyn + warp * kRing<kVec4> + lane * 16;
+    const uint32_t ring_s = smem_addr(ring);
+    constexpr int kHalf = kTurn * kVec4 * 512;     // bytes of a stage's keys
+
     Walk walk;
     walk.begin(p);
-    Segment t;
-    while (walk.next(p, t)) {
+    Segment t{}, nt{};                          // the segment being worked on, the next one
+    bool have = false, have_next = walk.next(p, nt);
+    // The copies: the warp's turn of the step at key `lk` of segment nt (in_next) or t, up to
+    // kStages steps ahead.  They cross into the next segment but not beyond it.
+    bool in_next = true;
+    int lk = have_next ? nt.k0 : 0;
+    uint32_t issued = 0, used = 0;
+    long long off = -1;                         // lane < 8: where the turn's key lies
+    auto look_up = [&]() {
+        const int key = lk + kTurn * warp + lane;
+        const int k1 = in_next ? (have_next ? nt.k1 : 0) : t.k1;
+        off = -1;
+        if (lane < kTurn && key < k1)
+            off = key_offset(p, in_next ? nt.g : t.g, in_next ? nt.hk : t.hk, key);
+    };
+    auto loadable = [&]() { return lk < (in_next ? (have_next ? nt.k1 : 0) : t.k1); };
+    auto issue = [&]() {
+        const uint32_t dst = ring_s + (issued % kStages) * (2 * kHalf);
+#pragma unroll
+        for (int j = 0; j < kTurn; ++j) {
+            const long long oj = __shfl_sync(0xffffffffu, off, j);
+#pragma unroll
+            for (int u = 0; u < kVec4; ++u) {
+                const int c = 4 * (lane + 32 * u);
+                const bool real = oj >= 0 && c < D && in_bounds(oj + c, 4, a.page_elems, a.status);
+                const long long at = real ? oj + c : 0;
+                cp_async16(dst + (j * kVec4 + u) * 512, K + at, real);
+                cp_async16(dst + kHalf + (j * kVec4 + u) * 512, V + at, real);
+            }
+        }
+        cp_async_commit();
+        ++issued;
+        lk += kUnit;
+        if (!in_next && lk >= t.k1) {
+            in_next = true;
+            lk = have_next ? nt.k0 : 0;
+        }
+        look_up();
+    };
+    look_up();
+#pragma unroll 1
+    for (;;) {
+        if (have) finish_segment<float, kRows, kThreads, kVec4>(p, t, &buf[0][0], kVec4 * 128, stat, &flag);
+        have = have_next;
+        if (!have) break;
+        t = nt;
+        have_next = walk.next(p, nt);
+        in_next = lk >= t.k1;
+        if (in_next) lk = have_next ? nt.k0 : 0;
+        look_up();
         float4 q[kRows][kVec4], o[kRows][kVec4];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
@@ -70,39 +130,38 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             seen = a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
         }
         float m = -INFINITY, l = 0.f;      // of row my_row; l over this lane's keys only
-        for (int k = t.k0 + kTurn * warp; k < t.k1; k += kUnit) {
-            long long off = -1;
-            if (lane < kTurn && k + lane < t.k1) off = key_offset(p, t.g, t.hk, k + lane);
-            float4 kk[kTurn][kVec4], vv[kTurn][kVec4];
-#pragma unroll
-            for (int j = 0; j < kTurn; ++j) {
-                const long long oj = __shfl_sync(0xffffffffu, off, j);
-#pragma unroll
-                for (int u = 0; u < kVec4; ++u) {
-                    const int c = 4 * (lane + 32 * u);
-                    kk[j][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    vv[j][u] = kk[j][u];
-                    if (oj >= 0 && c < D && in_bounds(oj + c, 4, a.page_elems, a.status)) {
-                        kk[j][u] = load4(K + oj + c);
-                        vv[j][u] = load4(V + oj + c);
-                    }
-                }
-            }
+        for (int k = t.k0 + kTurn * warp; k - kTurn * warp < t.k1; k += kUnit) {
+#pragma unroll 1
+            while (issued - used < kStages && loadable()) issue();
+            if (issued - used == kStages) cp_async_wait<kStages - 1>();
+            else cp_async_wait<0>();
+            const uint8_t* stage = ring + (used % kStages) * (2 * kHalf);
+            ++used;
+            auto key_at = [&](int j, int u) {
+                return *reinterpret_cast<const float4*>(stage + (j * kVec4 + u) * 512);
+            };
+            auto value_at = [&](int j, int u) {
+                return *reinterpret_cast<const float4*>(stage + kHalf + (j * kVec4 + u) * 512);
+            };
             float s[32];
 #pragma unroll
-            for (int j = 0; j < kTurn; ++j)
+            for (int j = 0; j < kTurn; ++j) {
+                float4 kk[kVec4];
+#pragma unroll
+                for (int u = 0; u < kVec4; ++u) kk[u] = key_at(j, u);
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {
                     float x = 0.f;
 #pragma unroll
                     for (int u = 0; u < kVec4; ++u) {
-                        x = fmaf(q[r][u].x, kk[j][u].x, x);
-                        x = fmaf(q[r][u].y, kk[j][u].y, x);
-                        x = fmaf(q[r][u].z, kk[j][u].z, x);
-                        x = fmaf(q[r][u].w, kk[j][u].w, x);
+                        x = fmaf(q[r][u].x, kk[u].x, x);
+                        x = fmaf(q[r][u].y, kk[u].y, x);
+                        x = fmaf(q[r][u].z, kk[u].z, x);
+                        x = fmaf(q[r][u].w, kk[u].w, x);
                     }
                     s[4 * j + r] = x;
                 }
+            }
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) {
                 const bool up = lane & w;
@@ -139,7 +198,10 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kTurn; ++j)
+            for (int j = 0; j < kTurn; ++j) {
+                float4 vv[kVec4];
+#pragma unroll
+                for (int u = 0; u < kVec4; ++u) vv[u] = value_at(j, u);
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {
                     const float w = __shfl_sync(0xffffffffu, pe, 4 * j + r);
@@ -147,12 +209,13 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
                     if (!((vis >> (4 * j + r)) & 1)) continue;
 #pragma unroll
                     for (int u = 0; u < kVec4; ++u) {
-                        o[r][u].x = fmaf(w, vv[j][u].x, o[r][u].x);
-                        o[r][u].y = fmaf(w, vv[j][u].y, o[r][u].y);
-                        o[r][u].z = fmaf(w, vv[j][u].z, o[r][u].z);
-                        o[r][u].w = fmaf(w, vv[j][u].w, o[r][u].w);
+                        o[r][u].x = fmaf(w, vv[u].x, o[r][u].x);
+                        o[r][u].y = fmaf(w, vv[u].y, o[r][u].y);
+                        o[r][u].z = fmaf(w, vv[u].z, o[r][u].z);
+                        o[r][u].w = fmaf(w, vv[u].w, o[r][u].w);
                     }
                 }
+            }
         }
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
@@ -188,8 +251,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             }
             __syncthreads();
         }
-        finish_segment<float, kRows, kThreads, kVec4>(p, t, &buf[0][0], kVec4 * 128, stat, &flag);
     }
+    cp_async_wait<0>();
 }
 
 }  // namespace
@@ -200,8 +263,8 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     fill_params(&p, a);
     static std::atomic<int> known1[kMaxDevices], known2[kMaxDevices];
     int grid = 0;
-    const cudaError_t e = a.D <= 128 ? resident_ctas(known1, paged_simt_kernel<1>, kThreads, 0, &grid)
-                                     : resident_ctas(known2, paged_simt_kernel<2>, kThreads, 0, &grid);
+    const cudaError_t e = a.D <= 128 ? resident_ctas(known1, paged_simt_kernel<1>, kThreads, kWarps * kRing<1>, &grid)
+                                     : resident_ctas(known2, paged_simt_kernel<2>, kThreads, kWarps * kRing<2>, &grid);
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.tile_cost = 64;
@@ -214,9 +277,9 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
     if (a.D <= 128)
-        paged_simt_kernel<1><<<p.grid, kThreads, 0, a.stream>>>(p);
+        paged_simt_kernel<1><<<p.grid, kThreads, kWarps * kRing<1>, a.stream>>>(p);
     else
-        paged_simt_kernel<2><<<p.grid, kThreads, 0, a.stream>>>(p);
+        paged_simt_kernel<2><<<p.grid, kThreads, kWarps * kRing<2>, a.stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -506,6 +506,20 @@ __device__ void finish_segment(const PagedParams& p, const Segment& seg, const f
     __syncthreads();
 }
 
+// Asynchronous 16-byte copies into shared memory.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real)
+{
+    const int n = real ? 16 : 0;                              // 0: the 16 bytes become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Element offset of key `key` of head hk of a sequence in the pages, or -1 (a page index
 // outside the cache: the key and its value read as zeros).
 __device__ __forceinline__ long long key_offset(const PagedParams& p, int g, int hk, int key)
