@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -753,15 +754,19 @@ def rope_table(rot_dim: int, base: float = 10000.0, style: str = "half", scaling
 
 # The calls below are short on the GPU (a decoding step's are a few microseconds), so what
 # they do on the host counts: no context managers unless the call leaves the current device
-# or stream, integers for pointers, descriptors filled by position.
+# or stream, integers for pointers, descriptors packed by format instead of field by field
+# (the formats are RopeDesc's and PagedDesc's layouts).
+_ROPE_DESC = struct.Struct("=7i4xQi4xQ2i4q")
+_PAGED_DESC = struct.Struct("=8i4q3Q2i")
+
 
 def _same_device(first, *others):
-    """The device that all the given tensors lie on (Nones are left out)."""
-    device = first.device
-    if device.type != "cuda":
+    """The index of the device that all the given tensors lie on (Nones are left out)."""
+    device = first.get_device()
+    if device < 0:
         raise ValueError("tensors must be CUDA tensors")
     for t in others:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != device:
             raise ValueError("all tensors must be on one device")
     return device
 
@@ -769,13 +774,14 @@ def _same_device(first, *others):
 def _launch_on(device, stream, body):
     """body(stream handle) with `device` current and, if a stream is given, `stream` current
     as well (so that what body allocates belongs to it)."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return body(torch.cuda.current_stream(device).cuda_stream)
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device != device:
+    if stream is None:
+        if device == torch.cuda.current_device():
+            return body(torch._C._cuda_getCurrentRawStream(device))
+        stream = torch.cuda.current_stream(device)
+    elif stream.device.index != device:
         raise ValueError("stream belongs to another device than the tensors")
-    with torch.cuda.device(device), torch.cuda.stream(s):
-        return body(s.cuda_stream)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
 def _call_fast(name, *args):
@@ -785,14 +791,15 @@ def _call_fast(name, *args):
 
 
 def _addr(t):
-    return t.data_ptr() if t is not None else None
+    return t.data_ptr() if t is not None else 0
 
 
 def _index_tensor(t, name, dim, sizes=None):
-    if t.dtype != torch.int32 or t.dim() != dim or (sizes and tuple(t.shape) != sizes):
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != dim or (sizes is not None and shape != sizes):
         raise ValueError(f"{name} must be a {dim}-D int32 CUDA tensor"
                          + (f" of shape {list(sizes)}" if sizes else ""))
-    if t.stride(-1) != 1 and t.numel() > 1:
+    if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
@@ -814,9 +821,9 @@ def _token_stride(t, name, dim):
 
 
 def _float_code(dtype, name):
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return RA_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return RA_F32
     raise ValueError(f"{name} must be bf16 or fp32")
 
@@ -859,10 +866,10 @@ def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out
                       _token_stride(qo, "q_out", dim)) if q is not None else (0, 0, 0)
         H_kv, ks, kos = (k.shape[-2], _token_stride(k, "k", dim),
                          _token_stride(ko, "k_out", dim)) if k is not None else (0, 0, 0)
-        d = RopeDesc(B, L, H, H_kv, ref.shape[-1], P, LAYOUTS[layout], _addr(cu_seqlens),
-                     cu_seqlens.numel() - 1 if packed else 0, _addr(positions), offset, code,
-                     qs, ks, qos, kos)
-        _call_fast(name, ctypes.byref(d), rope._c, _addr(q), _addr(k), _addr(qo), _addr(ko), s)
+        d = _ROPE_DESC.pack(B, L, H, H_kv, ref.shape[-1], P, LAYOUTS[layout], _addr(cu_seqlens),
+                            cu_seqlens.numel() - 1 if packed else 0, _addr(positions), offset,
+                            code, qs, ks, qos, kos)
+        _call_fast(name, d, rope._c, _addr(q), _addr(k), _addr(qo), _addr(ko), s)
         return qo, ko
 
     return _launch_on(device, stream, body)
@@ -897,16 +904,17 @@ def _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal):
     if stride[3] != 1 and shape[3] > 1:
         raise ValueError("the head vectors of the pages must be contiguous")
     code = _float_code(k_pages.dtype, "the pages")
-    n_seqs = kv_lens.numel()
     _index_tensor(kv_lens, "kv_lens", 1)
+    n_seqs = kv_lens.shape[0]
     _index_tensor(cu_new, "cu_new", 1, (n_seqs + 1,))
     _index_tensor(page_table, "page_table", 2)
     rows, cols = page_table.shape
     if rows != n_seqs:
         raise ValueError("page_table must have a row for every sequence")
-    return PagedDesc(T, n_seqs, H, shape[2], shape[3], shape[0], shape[1], cols, stride[0],
-                     stride[1], stride[2], page_table.stride(0) if n_seqs > 1 else cols,
-                     page_table.data_ptr(), cu_new.data_ptr(), kv_lens.data_ptr(), code, causal)
+    return _PAGED_DESC.pack(T, n_seqs, H, shape[2], shape[3], shape[0], shape[1], cols, stride[0],
+                            stride[1], stride[2], page_table.stride(0) if n_seqs > 1 else cols,
+                            page_table.data_ptr(), cu_new.data_ptr(), kv_lens.data_ptr(), code,
+                            causal)
 
 
 def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
@@ -937,7 +945,7 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
                 qo = torch.zeros(q.shape, dtype=q.dtype, device=device)
             qs, qos = _token_stride(q, "q", 3), _token_stride(qo, "q_out", 3)
         if T > 0:
-            _call_fast("paged_kv_append", ctypes.byref(d), rope._c if rope is not None else None,
+            _call_fast("paged_kv_append", d, rope._c if rope is not None else None,
                        _addr(q), qs, k.data_ptr(), _token_stride(k, "k", 3), v.data_ptr(),
                        _token_stride(v, "v", 3), _addr(qo), qos, k_pages.data_ptr(),
                        v_pages.data_ptr(), s)
@@ -982,7 +990,7 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
             ls = torch.zeros((T, H), dtype=torch.float32, device=device)
         if T > 0:
             ws = workspace if workspace is not None else paged_attn_workspace(D, q.dtype, device)
-            _call_fast("paged_attn_fwd", ctypes.byref(d), q.data_ptr(), _token_stride(q, "q", 3),
+            _call_fast("paged_attn_fwd", d, q.data_ptr(), _token_stride(q, "q", 3),
                        k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(), _addr(ls),
                        ws.data_ptr(), ws.numel() * ws.element_size(), s)
         return o, ls

@@ -269,3 +269,19 @@ def test_workspace_sizes(lib):
     assert f(64, 0) > 0 and f(128, 0) > f(64, 0)
     assert f(96, 0) == 0 and f(256, 0) == 0 and f(64, 2) == 0
     assert f(4, 1) > 0 and f(256, 1) > 0 and f(6, 1) == 0 and f(260, 1) == 0 and f(0, 1) == 0
+
+
+def test_packed_descriptors_are_the_structures():
+    """The byte formats that the binding packs are the structures' layouts."""
+    rope_fields = [f[0] for f in cea.RopeDesc._fields_]
+    values = list(range(1, len(rope_fields) + 1))
+    packed = cea._ROPE_DESC.pack(*values)
+    assert len(packed) == ctypes.sizeof(cea.RopeDesc)
+    d = cea.RopeDesc.from_buffer_copy(packed)
+    assert [getattr(d, f) for f in rope_fields] == values
+    paged_fields = [f[0] for f in cea.PagedDesc._fields_]
+    values = list(range(1, len(paged_fields) + 1))
+    packed = cea._PAGED_DESC.pack(*values)
+    assert len(packed) == ctypes.sizeof(cea.PagedDesc)
+    d = cea.PagedDesc.from_buffer_copy(packed)
+    assert [getattr(d, f) for f in paged_fields] == values
