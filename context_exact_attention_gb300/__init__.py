@@ -10,6 +10,7 @@ Layout: q, k, v, out are contiguous [B, L, H, D]; lse is fp32 [B, L, H].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -771,17 +772,22 @@ def _same_device(first, *others):
     return device
 
 
-def _launch_on(device, stream, body):
-    """body(stream handle) with `device` current and, if a stream is given, `stream` current
-    as well (so that what body allocates belongs to it)."""
-    if stream is None:
-        if device == torch.cuda.current_device():
-            return body(torch._C._cuda_getCurrentRawStream(device))
-        stream = torch.cuda.current_stream(device)
-    elif stream.device.index != device:
+def _stream_here(device, stream):
+    """The handle of the stream to launch on if it is the current one of the current device,
+    else None: the caller then enters _entered(device, stream) and calls itself again, so
+    that what it allocates belongs to that stream."""
+    if stream is None and device == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(device)
+    return None
+
+
+@contextlib.contextmanager
+def _entered(device, stream):
+    if stream is not None and stream.device.index != device:
         raise ValueError("stream belongs to another device than the tensors")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
+    with torch.cuda.device(device):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            yield
 
 
 def _call_fast(name, *args):
@@ -803,21 +809,21 @@ def _index_tensor(t, name, dim, sizes=None):
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
-def _token_stride(t, name, dim):
+def _token_stride(t, shape, name):
     """Elements between tokens of [..., H, D] rows whose heads lie side by side (a view of a
-    fused projection output is one such)."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != dim:
-        raise ValueError(f"{name} must have {dim} dimensions")
-    H, D = shape[-2:]
+    fused projection output is one such); shape is t's."""
+    stride = t.stride()
+    H, D = shape[-2], shape[-1]
     if stride[-1] != 1 and D > 1 or stride[-2] != D and H > 1:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if dim == 3:
+    if len(shape) == 3:
         return stride[0] if shape[0] > 1 else H * D
-    B, L = shape[:2]
-    if B > 1 and L > 1 and stride[0] != L * stride[1]:
-        raise ValueError(f"{name}: batches must follow one another at the token stride")
-    return stride[1] if L > 1 else stride[0] if B > 1 else H * D
+    B, L = shape[0], shape[1]
+    if L > 1:
+        if B > 1 and stride[0] != L * stride[1]:
+            raise ValueError(f"{name}: batches must follow one another at the token stride")
+        return stride[1]
+    return stride[0] if B > 1 else H * D
 
 
 def _float_code(dtype, name):
@@ -834,45 +840,59 @@ def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    device = _same_device(ref, q, k, rope.phases, positions, cu_seqlens, q_out, k_out)
-    code = _float_code(ref.dtype, "q and k")
+    device = _same_device(ref, k, rope.phases, positions, cu_seqlens, q_out, k_out)
+    s = _stream_here(device, stream)
+    if s is None:
+        with _entered(device, stream):
+            return _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out,
+                              k_out, None)
+    dtype = ref.dtype
+    code = _float_code(dtype, "q and k")
     packed = layout == "packed"
-    dim = 3 if packed else 4
-    if ref.dim() != dim:
+    shape = ref.shape
+    if len(shape) != (3 if packed else 4):
         raise ValueError("q and k must be [L, H, D] (packed layout) or [B, L, H, D]")
-    lead = ref.shape[:-2]
-    B, L = (1, lead[0]) if packed else lead
-    if q is not None and k is not None and (k.shape[:-2] != lead or q.shape[-1] != k.shape[-1]
-                                            or q.dtype != k.dtype):
-        raise ValueError("q and k must agree in every dimension but the heads, and in dtype")
+    B, L, D = (1, shape[0], shape[2]) if packed else (shape[0], shape[1], shape[3])
+    n_seqs = 0
     if packed != (cu_seqlens is not None):
         raise ValueError("cu_seqlens belongs to the packed layout, which needs it")
     if packed:
         _index_tensor(cu_seqlens, "cu_seqlens", 1)
+        n_seqs = cu_seqlens.shape[0] - 1
     if positions is not None:
         _index_tensor(positions, "positions", 2, (B, L))
         if not positions.is_contiguous():
             raise ValueError("positions must be contiguous")
-    for x, o in ((q, q_out), (k, k_out)):
-        if o is not None and (x is None or o.shape != x.shape or o.dtype != x.dtype):
+    H = H_kv = qs = ks = qos = kos = 0
+    if q is not None:
+        H = shape[-2]
+        qs = _token_stride(q, shape, "q")
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=dtype, device=device)
+        elif q_out.shape != shape or q_out.dtype is not dtype:
             raise ValueError("outputs must be shaped and typed like their inputs")
-
-    def body(s):
-        qo = torch.empty(q.shape, dtype=q.dtype, device=device) if q is not None and q_out is None else q_out
-        ko = torch.empty(k.shape, dtype=k.dtype, device=device) if k is not None and k_out is None else k_out
-        if B == 0 or L == 0:
-            return qo, ko
-        H, qs, qos = (q.shape[-2], _token_stride(q, "q", dim),
-                      _token_stride(qo, "q_out", dim)) if q is not None else (0, 0, 0)
-        H_kv, ks, kos = (k.shape[-2], _token_stride(k, "k", dim),
-                         _token_stride(ko, "k_out", dim)) if k is not None else (0, 0, 0)
-        d = _ROPE_DESC.pack(B, L, H, H_kv, ref.shape[-1], P, LAYOUTS[layout], _addr(cu_seqlens),
-                            cu_seqlens.numel() - 1 if packed else 0, _addr(positions), offset,
-                            code, qs, ks, qos, kos)
-        _call_fast(name, d, rope._c, _addr(q), _addr(k), _addr(qo), _addr(ko), s)
-        return qo, ko
-
-    return _launch_on(device, stream, body)
+        qos = _token_stride(q_out, shape, "q_out")
+    elif q_out is not None:
+        raise ValueError("an output without its input")
+    if k is not None:
+        k_shape = k.shape
+        H_kv = k_shape[-2]
+        if len(k_shape) != len(shape) or k_shape[0] != shape[0] or k_shape[-1] != D \
+                or not packed and k_shape[1] != L or k.dtype is not dtype:
+            raise ValueError("q and k must agree in every dimension but the heads, and in dtype")
+        ks = _token_stride(k, k_shape, "k")
+        if k_out is None:
+            k_out = torch.empty(k_shape, dtype=dtype, device=device)
+        elif k_out.shape != k_shape or k_out.dtype is not dtype:
+            raise ValueError("outputs must be shaped and typed like their inputs")
+        kos = _token_stride(k_out, k_shape, "k_out")
+    elif k_out is not None:
+        raise ValueError("an output without its input")
+    if B > 0 and L > 0:
+        d = _ROPE_DESC.pack(B, L, H, H_kv, D, P, LAYOUTS[layout], _addr(cu_seqlens), n_seqs,
+                            _addr(positions), offset, code, qs, ks, qos, kos)
+        _call_fast(name, d, rope._c, _addr(q), _addr(k), _addr(q_out), _addr(k_out), s)
+    return q_out, k_out
 
 
 def rope_fwd(q, k, rope: RopeTable, positions=None, offset: int = 0, layout: str = "contiguous",
@@ -926,32 +946,38 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
     and returned.  Pages and tokens may be strided views (see ra_paged_desc)."""
     device = _same_device(k, v, k_pages, v_pages, page_table, cu_new, kv_lens, q, q_out,
                           rope.phases if rope is not None else None)
-    T, H_kv, D = k.shape if k.dim() == 3 else (0, 0, 0)
-    if k.shape != v.shape or (H_kv, D) != tuple(k_pages.shape[2:]) or k.dtype != k_pages.dtype \
-            or v.dtype != k.dtype:
+    s = _stream_here(device, stream)
+    if s is None:
+        with _entered(device, stream):
+            return paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens, rope, q,
+                                   q_out)
+    shape, dtype = k.shape, k.dtype
+    pages = k_pages.shape
+    if len(shape) != 3 or v.shape != shape or len(pages) != 4 or shape[1] != pages[2] \
+            or shape[2] != pages[3] or dtype is not k_pages.dtype or v.dtype is not dtype:
         raise ValueError("k and v must be [T, H_kv, D], with the heads and dtype of the pages")
-    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype):
-        raise ValueError("q must be [T, H, D] with k's tokens, head dim and dtype")
-    if q_out is not None and (q is None or q_out.shape != q.shape or q_out.dtype != q.dtype):
+    T = shape[0]
+    H = qs = qos = 0
+    if q is not None:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != shape[2] or q.dtype is not dtype:
+            raise ValueError("q must be [T, H, D] with k's tokens, head dim and dtype")
+        H = q_shape[1]
+        qs = _token_stride(q, q_shape, "q")
+        if q_out is None:
+            q_out = torch.zeros(q_shape, dtype=dtype, device=device)
+        elif q_out.shape != q_shape or q_out.dtype is not dtype:
+            raise ValueError("q_out must be shaped and typed like q")
+        qos = _token_stride(q_out, q_shape, "q_out")
+    elif q_out is not None:
         raise ValueError("q_out must be shaped and typed like q")
-    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T,
-                    q.shape[1] if q is not None else 0, 0)
-
-    def body(s):
-        qo = q_out
-        qs = qos = 0
-        if q is not None:
-            if qo is None:
-                qo = torch.zeros(q.shape, dtype=q.dtype, device=device)
-            qs, qos = _token_stride(q, "q", 3), _token_stride(qo, "q_out", 3)
-        if T > 0:
-            _call_fast("paged_kv_append", d, rope._c if rope is not None else None,
-                       _addr(q), qs, k.data_ptr(), _token_stride(k, "k", 3), v.data_ptr(),
-                       _token_stride(v, "v", 3), _addr(qo), qos, k_pages.data_ptr(),
-                       v_pages.data_ptr(), s)
-        return qo
-
-    return _launch_on(device, stream, body)
+    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, 0)
+    if T > 0:
+        _call_fast("paged_kv_append", d, rope._c if rope is not None else None, _addr(q), qs,
+                   k.data_ptr(), _token_stride(k, shape, "k"), v.data_ptr(),
+                   _token_stride(v, shape, "v"), _addr(q_out), qos, k_pages.data_ptr(),
+                   v_pages.data_ptr(), s)
+    return q_out
 
 
 def paged_attn_workspace(D: int, dtype=torch.bfloat16, device=None):
@@ -973,29 +999,32 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
     allocates and zeroes one for this call).  Returns (out [T, H, D], lse fp32 [T, H]); rows
     behind the last sequence are left as they are (zero in an out allocated here)."""
     device = _same_device(q, k_pages, v_pages, page_table, cu_new, kv_lens, out, lse, workspace)
-    if q.dim() != 3 or q.dtype != k_pages.dtype or q.shape[2] != k_pages.shape[-1]:
+    s = _stream_here(device, stream)
+    if s is None:
+        with _entered(device, stream):
+            return paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal, out,
+                                  lse, want_lse, workspace)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or dtype is not k_pages.dtype or shape[2] != k_pages.shape[-1]:
         raise ValueError("q must be [T, H, D] with the head dim and dtype of the pages")
-    T, H, D = q.shape
+    T, H, D = shape
     d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, 1 if causal else 0)
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous()):
+    if out is None:
+        out = torch.zeros(shape, dtype=dtype, device=device)
+    elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous and shaped and typed like q")
-    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32
-                            or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous fp32 [T, H] tensor")
-
-    def body(s):
-        o = torch.zeros((T, H, D), dtype=q.dtype, device=device) if out is None else out
-        ls = lse
-        if ls is None and want_lse:
-            ls = torch.zeros((T, H), dtype=torch.float32, device=device)
-        if T > 0:
-            ws = workspace if workspace is not None else paged_attn_workspace(D, q.dtype, device)
-            _call_fast("paged_attn_fwd", d, q.data_ptr(), _token_stride(q, "q", 3),
-                       k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(), _addr(ls),
-                       ws.data_ptr(), ws.numel() * ws.element_size(), s)
-        return o, ls
-
-    return _launch_on(device, stream, body)
+    if lse is not None:
+        if lse.shape != (T, H) or lse.dtype is not torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 [T, H] tensor")
+    elif want_lse:
+        lse = torch.zeros((T, H), dtype=torch.float32, device=device)
+    if T > 0:
+        if workspace is None:
+            workspace = paged_attn_workspace(D, dtype, device)
+        _call_fast("paged_attn_fwd", d, q.data_ptr(), _token_stride(q, shape, "q"),
+                   k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _addr(lse),
+                   workspace.data_ptr(), workspace.nbytes, s)
+    return out, lse
 
 
 def check_status(stream=None) -> int:
