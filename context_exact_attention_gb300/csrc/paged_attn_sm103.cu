@@ -680,12 +680,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const long long at0 = part_slot(tile, blockIdx.x) * 2 * kSub + tq * kSub;
                 if (valid && mine && in_bounds(at0 + row, 1, all_rows, a.status))
                     __stcg(reinterpret_cast<float2*>(p.part_stat) + at0 + row, make_float2(m, l));
-                if (!empty && mine && __any_sync(0xffffffffu, valid)) {
+                if (mine && __any_sync(0xffffffffu, valid)) {
                     const unsigned rows_in = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + 32 * c, o);
+                        uint32_t o[32] = {};                   // zeros if it saw no key
+                        if (!empty) tmem_ld32(tO + 32 * c, o);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int kHalf = D / 2;
                 constexpr int kChunks = kHalf / 8;             // 16-byte chunks per staged row
                 constexpr int kRowsPerStore = 32 / kChunks;
-                const float inv = l == 0.f ? 0.f : 1.f / l;    // a row that saw no key: 0
+                const float inv = inverse_of(l);
                 const long long my_row = valid ? out_row(p, tile, in_tile) : -1;
 #pragma unroll 1
                 for (int hh = 0; hh < 2; ++hh) {
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 if (valid && a.lse != nullptr && in_bounds(my_row, 1, a.lse_elems, a.status))
-                    a.lse[my_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPagedLn2;
+                    a.lse[my_row] = lse_of(m, l);
             }
         }
     }

@@ -330,8 +330,8 @@ __device__ __forceinline__ void store4(T* dst, float4 v)
 // m = -inf and l = NaN, and passes its NaN on.
 __device__ __forceinline__ float part_weight(float m, float l, float M)
 {
-    if (m == -INFINITY) return l == 0.f ? 0.f : 1.f;
-    return ex2(m - M);
+    const float none = l == 0.f ? 0.f : 1.f;
+    return m == -INFINITY ? none : ex2(m - M);
 }
 
 // The rows of one tile, as far as its output needs them.
@@ -347,17 +347,26 @@ __device__ __forceinline__ long long out_row(const PagedParams& p, const TileRow
     return static_cast<long long>(t.first + tok) * p.a.H + t.hk * p.G + (pr - tok * p.G);
 }
 
+// 1 / L and the log-sum-exp of a row with maximum M (base 2) and denominator L; 0 and -inf
+// for a row that saw no key.  (The approximate reciprocal and logarithm are good to an ulp and
+// to 2^-22; their exact forms' branches cost the joining loop below more than its reads.)
+__device__ __forceinline__ float inverse_of(float L) { return L == 0.f ? 0.f : __fdividef(1.f, L); }
+__device__ __forceinline__ float lse_of(float M, float L)
+{
+    return L == 0.f ? -INFINITY : (M + __log2f(L)) * kPagedLn2;
+}
+
 template <typename T>
 __device__ __forceinline__ void write_row4(const PagedParams& p, const TileRows& t, int r, int c4,
                                            float4 o, float M, float L)
 {
-    const float inv = L == 0.f ? 0.f : 1.f / L;       // a row that saw no key: 0 and -inf
+    const float inv = inverse_of(L), lse = lse_of(M, L);
     const long long row = out_row(p, t, r);
     const long long idx = row * p.a.D + 4 * c4;
     if (in_bounds(idx, 4, p.a.out_elems, p.a.status))
         store4(static_cast<T*>(p.a.out) + idx, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     if (c4 == 0 && p.a.lse != nullptr && in_bounds(row, 1, p.a.lse_elems, p.a.status))
-        p.a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
+        p.a.lse[row] = lse;
 }
 
 // Where CTA `cta` keeps its partial of tile t: slot 1 if the tile begins in its part and
@@ -398,6 +407,13 @@ __device__ void join_rows(const PagedParams& p, const TileRows& t, int warp, int
     const int D = p.a.D;
     const int nc = t.c_last - t.c_first + 1;
     const unsigned all_rows = 2u * p.grid * slot_rows;
+    // columns of this lane: four at 4 (col + kLanes u), or none
+    int at_col[kVec4];
+#pragma unroll
+    for (int u = 0; u < kVec4; ++u) {
+        const int c = 4 * (col + kLanes * u);
+        at_col[u] = c < D ? c : -1;
+    }
 #pragma unroll 1
     for (int r0 = warp * kAbreast + lane / kLanes; r0 - lane / kLanes < t.rows; r0 += step * kRowsAt) {
         float M[kRowsAt], L[kRowsAt];
@@ -407,8 +423,8 @@ __device__ void join_rows(const PagedParams& p, const TileRows& t, int warp, int
         for (int b = 0; b < kRowsAt; ++b) {
             M[b] = -INFINITY;
             L[b] = 0.f;
-            const int r = r0 + b * step;
-            at0[b] = 2u * t.c_first * slot_rows + place(r < t.rows ? r : 0);
+            // (rows behind the last one repeat it and are not written)
+            at0[b] = 2u * t.c_first * slot_rows + place(min(r0 + b * step, t.rows - 1));
 #pragma unroll
             for (int u = 0; u < kVec4; ++u) acc[b][u] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -416,42 +432,56 @@ __device__ void join_rows(const PagedParams& p, const TileRows& t, int warp, int
         for (int k = 0; k < nc; k += kDeep) {
             float2 st[kDeep][kRowsAt];
             float4 o[kDeep][kRowsAt][kVec4];
+            // all reads first, under no condition but the contributors' number
 #pragma unroll
-            for (int e = 0; e < kDeep; ++e)
+            for (int e = 0; e < kDeep; ++e) {
+                // contributor 0 has slot 1 of its CTA, the others slot 0 of theirs
+                const bool real = k + e < nc;
+                const unsigned slot = (k + e == 0 ? 1u : 2u * (k + e)) * slot_rows;
 #pragma unroll
                 for (int b = 0; b < kRowsAt; ++b) {
-                    // contributor 0 has slot 1 of its CTA, the others slot 0 of theirs
-                    const unsigned at = at0[b] + (k + e == 0 ? 1u : 2u * (k + e)) * slot_rows;
-                    const bool real = k + e < nc && r0 + b * step < t.rows &&
-                                      in_bounds(at, 1, all_rows, p.a.status);
+                    const unsigned at = at0[b] + slot;
+                    const bool in = real && in_bounds(at, 1, all_rows, p.a.status);
                     st[e][b] = make_float2(-INFINITY, 0.f);
-                    if (real) st[e][b] = __ldcg(reinterpret_cast<const float2*>(p.part_stat) + at);
-                    const float4* src = reinterpret_cast<const float4*>(
-                        p.part_o + static_cast<unsigned long long>(at) * D) + col;
+                    if (in) st[e][b] = __ldcg(reinterpret_cast<const float2*>(p.part_stat) + at);
+                    const float* src = p.part_o + static_cast<unsigned long long>(at) * D;
 #pragma unroll
                     for (int u = 0; u < kVec4; ++u) {
                         o[e][b][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (real && 4 * (col + kLanes * u) < D) o[e][b][u] = __ldcg(src + kLanes * u);
+                        if (in)
+                            o[e][b][u] = __ldcg(reinterpret_cast<const float4*>(src + max(at_col[u], 0)));
                     }
                 }
+            }
 #pragma unroll
-            for (int e = 0; e < kDeep; ++e)
+            for (int b = 0; b < kRowsAt; ++b) {
+                float Mn = M[b];
 #pragma unroll
-                for (int b = 0; b < kRowsAt; ++b) {
+                for (int e = 0; e < kDeep; ++e) Mn = fmaxf(Mn, st[e][b].x);
+                const float old = part_weight(M[b], L[b], Mn);
+                M[b] = Mn;
+                L[b] *= old;
+#pragma unroll
+                for (int u = 0; u < kVec4; ++u) {
+                    acc[b][u].x *= old;
+                    acc[b][u].y *= old;
+                    acc[b][u].z *= old;
+                    acc[b][u].w *= old;
+                }
+#pragma unroll
+                for (int e = 0; e < kDeep; ++e) {
                     const float2 x = st[e][b];
-                    if (x.y == 0.f) continue;          // no contributor, or one without keys
-                    const float Mn = fmaxf(M[b], x.x);
-                    const float old = part_weight(M[b], L[b], Mn), w = part_weight(x.x, x.y, Mn);
-                    M[b] = Mn;
-                    L[b] = L[b] == 0.f ? w * x.y : fmaf(L[b], old, w * x.y);
+                    const float w = part_weight(x.x, x.y, Mn);
+                    L[b] = fmaf(w, x.y, L[b]);
 #pragma unroll
                     for (int u = 0; u < kVec4; ++u) {
-                        acc[b][u].x = fmaf(acc[b][u].x, old, w * o[e][b][u].x);
-                        acc[b][u].y = fmaf(acc[b][u].y, old, w * o[e][b][u].y);
-                        acc[b][u].z = fmaf(acc[b][u].z, old, w * o[e][b][u].z);
-                        acc[b][u].w = fmaf(acc[b][u].w, old, w * o[e][b][u].w);
+                        acc[b][u].x = fmaf(w, o[e][b][u].x, acc[b][u].x);
+                        acc[b][u].y = fmaf(w, o[e][b][u].y, acc[b][u].y);
+                        acc[b][u].z = fmaf(w, o[e][b][u].z, acc[b][u].z);
+                        acc[b][u].w = fmaf(w, o[e][b][u].w, acc[b][u].w);
                     }
                 }
+            }
         }
 #pragma unroll
         for (int b = 0; b < kRowsAt; ++b) {
@@ -459,8 +489,7 @@ __device__ void join_rows(const PagedParams& p, const TileRows& t, int warp, int
             if (r >= t.rows) continue;
 #pragma unroll
             for (int u = 0; u < kVec4; ++u)
-                if (4 * (col + kLanes * u) < D)
-                    write_row4<T>(p, t, r, col + kLanes * u, acc[b][u], M[b], L[b]);
+                if (at_col[u] >= 0) write_row4<T>(p, t, r, col + kLanes * u, acc[b][u], M[b], L[b]);
         }
     }
 }
@@ -489,14 +518,12 @@ __device__ void finish_segment(const PagedParams& p, const Segment& seg, const f
     for (int r = tid; r < t.rows; r += kThreads)
         if (in_bounds(at0 + r, 1, all_rows, p.a.status))
             __stcg(reinterpret_cast<float2*>(p.part_stat) + at0 + r, stat[r]);
-    if (seg.k1 > seg.k0) {
-        for (int i = tid; i < t.rows * v4; i += kThreads) {
-            const int r = i / v4, cc = i - r * v4;
-            const long long at = (at0 + r) * p.a.D + 4 * cc;
-            if (in_bounds(at, 4, all_rows * p.a.D, p.a.status))
-                __stcg(reinterpret_cast<float4*>(p.part_o + at),
-                       *reinterpret_cast<const float4*>(buf + r * ldo + 4 * cc));
-        }
+    for (int i = tid; i < t.rows * v4; i += kThreads) {        // (zeros if it saw no key)
+        const int r = i / v4, cc = i - r * v4;
+        const long long at = (at0 + r) * p.a.D + 4 * cc;
+        if (in_bounds(at, 4, all_rows * p.a.D, p.a.status))
+            __stcg(reinterpret_cast<float4*>(p.part_o + at),
+                   *reinterpret_cast<const float4*>(buf + r * ldo + 4 * cc));
     }
     __syncthreads();
     if (tid == 0) *flag = arrive_last(p, t);
