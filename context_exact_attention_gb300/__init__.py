@@ -817,13 +817,18 @@ def _token_stride(t, shape, name):
     if stride[-1] != 1 and D > 1 or stride[-2] != D and H > 1:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if len(shape) == 3:
-        return stride[0] if shape[0] > 1 else H * D
-    B, L = shape[0], shape[1]
-    if L > 1:
-        if B > 1 and stride[0] != L * stride[1]:
-            raise ValueError(f"{name}: batches must follow one another at the token stride")
-        return stride[1]
-    return stride[0] if B > 1 else H * D
+        step = stride[0] if shape[0] > 1 else H * D
+    else:
+        B, L = shape[0], shape[1]
+        if L > 1:
+            if B > 1 and stride[0] != L * stride[1]:
+                raise ValueError(f"{name}: batches must follow one another at the token stride")
+            step = stride[1]
+        else:
+            step = stride[0] if B > 1 else H * D
+    if step < H * D:            # broadcast (0, which the library would read as contiguous)
+        raise ValueError(f"{name}: tokens must not overlap")
+    return step
 
 
 def _float_code(dtype, name):
@@ -1021,6 +1026,8 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
     if T > 0:
         if workspace is None:
             workspace = paged_attn_workspace(D, dtype, device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         _call_fast("paged_attn_fwd", d, q.data_ptr(), _token_stride(q, shape, "q"),
                    k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _addr(lse),
                    workspace.data_ptr(), workspace.nbytes, s)

@@ -7,8 +7,8 @@
 // call are laid end to end, sequence by sequence, head by head, on one axis of cost, each
 // tile as long as its fixed cost and its keys times a weight, and CTA c takes the part
 // [c chunk, (c + 1) chunk) of that axis: whatever the lengths are, every CTA does the same
-// work, and one token over a long cache fills the whole GPU.  Everything is
-// computed from the lengths on the device in each warp (a scan over the sequences), so a
+// work, and one token over a long cache fills the whole GPU.  Everything is computed from the
+// lengths on the device, by each warp that needs it (a scan over the sequences), so a
 // captured call follows the lengths that it finds when it is replayed.
 //
 // A tile that lies in one CTA's part is written by that CTA.  Of a tile cut by a part's
@@ -25,6 +25,8 @@
 namespace ra {
 
 constexpr float kPagedLn2 = 0.6931471805599453f;
+constexpr long long kMostKeys = 0x7fffffffll - 1023;
+
 // Kernel-side copy of PagedArgs, with the split.
 struct PagedParams {
     PagedArgs a;
@@ -46,12 +48,12 @@ struct PagedParams {
     }
     float scale_log2;       // log2(e) / sqrt(D): scores in base-2 units
     unsigned int* counters; // [kPagedMaxCtas], zero between calls
-    float* part_stat;       // [2 grid][rows][2]: maximum, denominator
-    float* part_o;          // [2 grid][rows][D]
+    float* part_stat;       // [2 grid][rows of a tile][2]: maximum, denominator
+    float* part_o;          // [2 grid][rows of a tile][D]
 };
 
 // The workspace, in bytes: work counters, then the statistics and sums of two partial tiles
-// for every CTA.  (rows packed rows of a tile; the sums lie as each kernel likes.)
+// for every CTA.
 struct PagedWorkspace {
     unsigned long long stat, o, total;
 };
@@ -95,7 +97,8 @@ __device__ __forceinline__ SeqSpan seq_span_of(const PagedArgs& a, int g)
     const int kv = checked_ldg(a.kv_lens, g, a.n_seqs, a.status);
     s.first = min(max(lo, 0), a.T);
     s.n = min(max(hi, s.first), a.T) - s.first;
-    const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
+    // (kMostKeys: key indices plus a step of the kernels stay below 2^31)
+    const long long cap = min(static_cast<long long>(a.max_pages) * a.page_size, kMostKeys);
     s.kv = static_cast<int>(min(static_cast<long long>(max(kv, 0)), cap));
     return s;
 }

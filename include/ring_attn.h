@@ -634,7 +634,7 @@ ra_status rope_bwd(const ra_rope_desc* desc, const ra_rope* rope, const void* dq
  * Whatever these arrays hold, no access leaves the tensors: a page index outside
  * [0, num_pages) stores nothing in the append and reads as zero keys and values in the
  * attention, and positions at or beyond max_pages * page_size are not stored; the attention
- * takes kv_lens above that as that.
+ * takes kv_lens above that (or above 2^31 - 1024) as that.
  */
 typedef struct {
     int T, n_seqs, H, H_kv, D;
@@ -656,8 +656,8 @@ typedef struct {
  * q, k, v: [T, H, D] and [T, H_kv, D], head vectors contiguous, tokens *_stride elements
  * apart (0: contiguous), so that all three may be views of a fused projection output.
  * q, q_out: both NULL, or q_out as q (in place allowed).  The pages must overlap nothing
- * else; k_pages and v_pages may alternate in one buffer.  If two rows map to one slot,
- * either's vectors may be the ones kept.  D * element size a multiple of 16 bytes, D <= 256.
+ * else; k_pages and v_pages may alternate in one buffer.  If two rows map to one slot, what
+ * it holds afterwards is, 16 bytes by 16 bytes, from either of them.  D * element size a multiple of 16 bytes, D <= 256.
  * Errors as rope_fwd.
  */
 ra_status paged_kv_append(const ra_paged_desc* desc, const ra_rope* rope, const void* q,
@@ -680,8 +680,9 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  * keys are shared out evenly over the GPU whatever the lengths are.  (out, lse) is a partial
  * that attn_merge_partials can join with another over other keys.  A row that sees no key
  * gets 0 and -inf.  Slots behind a sequence's last key are never used, whatever they hold.
- * In the tensor-core kernels (bf16) a value row that is not finite may also reach rows of
- * the same call that stand up to 127 positions before it.
+ * A key that a row does not see never reaches it.  A value that is not finite, of a new token
+ * of a call with several new tokens per sequence, may in bf16 also reach earlier new rows of
+ * its sequence (0 times infinity in the matrix product, as in ring_attn_fwd).
  *
  * q: [T, H, D], tokens q_stride elements apart (0: contiguous); out: [T, H, D] contiguous;
  * lse: fp32 [T, H] or NULL.  D 64 or 128 (RA_BF16), a multiple of 4 up to 256 (RA_F32).

@@ -42,6 +42,14 @@ ATTEND = {
     "big pages": ([(150, 600), (1, 513)], 4, 4, 64, 256, BF, "slots", 0),
     "pages of 24": ([(150, 600), (1, 513)], 4, 2, 128, 24, BF, "slots", 0),
     "pages of 8": ([(140, 140), (40, 777)], 4, 2, 128, 8, BF, "by_page", 0),
+    "a hundred heads a group": ([(2, 150), (5, 40)], 100, 1, 64, 16, BF, "slots", 1),
+    "chunks, more new than keys": ([(200, 50), (130, 0), (40, 300)], 4, 1, 64, 16, BF, "slots", 2),
+    "pages of 384": ([(90, 900), (140, 385)], 4, 2, 128, 384, BF, "slots", 0),
+    "chunks by head": ([(70, 300), (33, 40)], 4, 2, 128, 16, BF, "by_head", 0),
+    "chunks by slot": ([(70, 300), (33, 40)], 4, 2, 64, 32, BF, "by_slot", 0),
+    "a chunk, a long context": ([(40, 12000)], 4, 2, 128, 128, BF, "heads", 0),
+    "many short prompts": ([((i * 7) % 60, (i * 7) % 60 + i % 5) for i in range(150)], 8, 2, 64, 8, BF,
+                           "slots", 5),
     "more heads than a tile": ([(2, 150), (40, 90)], 160, 1, 64, 16, BF, "slots", 0),
     "fp32": ([(1, 90), (7, 40), (1, 1), (0, 3)], 6, 2, 128, 16, F32, "slots", 1),
     "fp32 wide": ([(2, 130), (1, 3)], 5, 1, 256, 8, F32, "heads", 0),
@@ -100,6 +108,17 @@ def test_infinite_and_nan_inputs_stay_in_their_rows():
     ref = clean.reference()
     real = slice(2, 6)
     assert_attends(out[real], lse[real], tuple(x[real] for x in ref))
+
+
+def test_a_key_of_a_later_token_that_is_not_finite():
+    """In a chunk: the last tokens' keys are NaN and infinite, earlier rows do not see them."""
+    c = Cache([(150, 400)], 4, 2, 128, 16, seed=20)
+    clean = c.reference()
+    for pos, x in ((398, float("nan")), (399, float("inf"))):
+        c.k[c.table[0, pos // 16], pos % 16] = x
+    out, lse = attend(c)
+    assert out[148:].isnan().all()
+    assert_attends(out[:148], lse[:148], tuple(x[:148] for x in clean))
 
 
 def test_strided_queries():
@@ -400,14 +419,23 @@ def test_binding_refusals():
         lambda: cea.paged_kv_append(k.float(), k.float(), kp, vp, t, cu, kv),
         lambda: cea.paged_kv_append(k, k, kp, vp, t, cu, kv, q=q[:1]),
         lambda: cea.paged_kv_append(k, k, kp, vp, t, cu, kv, q_out=q),
+        lambda: cea.paged_attn_fwd(q[:1].expand(2, 4, 64), kp, vp, t, cu, kv),
+        lambda: cea.paged_attn_fwd(q, kp, vp, t, cu, kv, workspace=cea.paged_attn_workspace(
+            64, BF, DEV).view(-1, 2)[:, 0]),
+        lambda: cea.paged_kv_append(k[:1].expand(2, 2, 64), k, kp, vp, t, cu, kv),
+        lambda: cea.paged_kv_append(k, k[:, :1].expand(2, 2, 64), kp, vp, t, cu, kv),
         lambda: cea.paged_attn_workspace(96), lambda: cea.paged_attn_workspace(64, torch.half),
     ]
     for f in bad:
         with pytest.raises(ValueError):
             f()
     short = torch.zeros(1024, dtype=torch.uint8, device=DEV)
-    with pytest.raises(cea.RingAttnError):
-        cea.paged_attn_fwd(q, kp, vp, t, cu, kv, workspace=short)
+    same = kp[:1].expand(kp.shape)                 # every page the same memory
+    for f in (lambda: cea.paged_attn_fwd(q, kp, vp, t, cu, kv, workspace=short),
+              lambda: cea.paged_kv_append(k, k, kp, kp, t, cu, kv),
+              lambda: cea.paged_kv_append(k, k, same, same, t, cu, kv)):
+        with pytest.raises(cea.RingAttnError):
+            f()
     none = torch.zeros(0, 4, 64, dtype=BF, device=DEV)
     zero = torch.zeros(2, dtype=torch.int32, device=DEV)
     assert cea.paged_attn_fwd(none, kp, vp, t, zero, kv)[0].shape == (0, 4, 64)

@@ -206,6 +206,10 @@ def test_binding_refusals():
         lambda: cea.rope_fwd(x, None, t, q_out=x.bfloat16()),
         lambda: cea.rope_fwd(x, None, t, k_out=x),
         lambda: cea.rope_fwd(x.transpose(2, 3), None, t),
+        lambda: cea.rope_fwd(x[:, :1].expand(1, 4, 2, 64), None, t),         # broadcast tokens
+        lambda: cea.rope_fwd(x[:, :, :1].expand(1, 4, 2, 64), None, t),      # broadcast heads
+        lambda: cea.rope_fwd(x, None, t, q_out=x[:, :1].expand(1, 4, 2, 64)),
+        lambda: cea.rope_bwd(x[:1].expand(2, 4, 2, 64), None, t),            # broadcast batch
         lambda: cea.rope_table(63), lambda: cea.rope_table(64, style="third"),
         lambda: cea.rope_table(64, scaling="more"),
         lambda: cea.rope_table(64, inv_freq=[1.0]),
