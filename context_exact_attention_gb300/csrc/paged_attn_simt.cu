@@ -15,6 +15,9 @@
 // for about 400 warp instructions, which an SM issues in 100 cycles; HBM delivers them in
 // about 350.  More rows per head (long prompts in fp32) are taken four at a time and
 // re-read the keys, which then come from L2.
+// Measured: 16 single tokens over 100 to 4000 keys of 2 heads of 128 (91 MB) in 28 us, 3.2 TB/s:
+// each CTA has only seven turns, and the call's fixed parts (plan, first reads, joining,
+// launch: about 10 us) show.  Loading straight into registers, a turn at a time, took 33 to 37.
 #include "paged_plan.cuh"
 
 namespace ra {

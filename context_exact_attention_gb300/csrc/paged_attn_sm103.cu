@@ -25,6 +25,17 @@
 // is NaN), which only the last block of a sequence needs.
 //
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D).
+//
+// Measured (1.9 GHz cycles): a block of two sub-tiles takes 2500 cycles at head dim 128, of
+// which the four products are 2048, and 2700 at 64, where each sub-tile's softmax (1750) and
+// its turn at the issuing warp bound it; a block of a single sub-tile 2300 at 128 (the K and V
+// loads: 64 KB at an SM's share of HBM) and 1500 at 64.  A chunk of 2048 tokens ending at
+// 32768, 32 heads over 8, takes 625 to 635 us (1.68 to 1.70 PFLOP/s; 690 to 720 us back to
+// back at the power cap); 32 sequences of 5 proposed tokens over up to 8192 keys 54 us
+// (5.1 TB/s).  Outside the blocks a CTA spends 6000 cycles before the first, 2500 to 4800 on
+// an output, 3000 to 8000 on a partial, and a joining CTA 6000 (40 rows) to 24000 (256 rows).
+// The weights go into P V as one bf16 each (2^-9 to 2^-8 relative): a second part, which the
+// kernel for few rows adds, would double the product that bounds this one.
 #include <cuda.h>
 
 #include "paged_plan.cuh"
@@ -802,10 +813,19 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
 
 bool paged_tc_applies(const PagedArgs& a)
 {
-    // A page must cover whole 8-row swizzle atoms of a 128-key block, or whole blocks, and a
-    // sub-tile at least one token.
+    // A page must cover whole 8-row swizzle atoms of a 128-key block, or whole blocks, a
+    // sub-tile at least one token, and the strides fit a tensor map (2^40 bytes).
+    const long long most = 1ll << 39;
+    if (a.q_stride >= most || a.page_stride >= most || a.token_stride >= most || a.head_stride >= most)
+        return false;
     const bool pages = a.page_size % 8 == 0 && (kKeys % a.page_size == 0 || a.page_size % kKeys == 0);
     if (a.elem != 2 || !pages || a.H / a.H_kv > kSub) return false;
+    // More than one 16-row tile per sequence and key head on average (the lengths are not known
+    // here).  Measured, few-rows kernel against this one, head dim 128, 8 key heads: 32
+    // sequences of up to 8000 keys, 16 rows 108 us against 100, 20 rows 182 against 102, 64
+    // rows 360 against 101; 64 sequences of up to 500 keys, 16 rows 25 against 39, 20 rows 39
+    // against 39, 64 rows 74 against 39; one of 32768, 16 rows 42 against 40, 64 rows 62
+    // against 41; head dim 64, 32 sequences: 16 rows 64 against 72, 20 rows 96 against 72.
     return static_cast<long long>(a.T) * (a.H / a.H_kv) > 16ll * a.n_seqs;
 }
 

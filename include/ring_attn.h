@@ -690,8 +690,9 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  * by the caller before its first use; every call leaves it ready for the next.  Calls that
  * share a workspace must not overlap on the GPU (two captured graphs that share one must be
  * replayed in order).  After a call that timed out (ra_check_status) zero it again.
- * Scores and softmax in fp32; the bf16 kernels round the weights to bf16 for the value
- * product, whose sums are fp32; out is rounded once.  Repeated calls on the same inputs give
+ * Scores and softmax in fp32; for the value product, whose sums are fp32, bf16 calls round a
+ * weight to two bf16 parts (2^-17) if sequences bring few rows and to one (2^-8 at most) if
+ * they bring many; out is rounded once.  Repeated calls on the same inputs give
  * the same bits; the split over the GPU, and with it the last bits, depends on all lengths of
  * the call.  Limits: T * H <= 2^31 - 256.  Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED (dtype,
  * D), RA_ERR_NOT_DIVISIBLE (H % H_kv), RA_ERR_MISALIGNED, RA_ERR_CUDA.
