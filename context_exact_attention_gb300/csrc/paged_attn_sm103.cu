@@ -7,8 +7,9 @@
 // all of them.  The roles are those of the dense forward (attn_bf16_sm103.cu):
 //   warp 0      producer: walks the CTA's segments, publishes each to the other warps
 //               through a two-slot ring in shared memory, and loads the query sub-tiles
-//               and the 128-key blocks of K and V by TMA, one box per page (one lane each,
-//               the page-table entries fetched a block ahead);
+//               and the 128-key blocks of K by TMA, in boxes of keys that share a page
+//               (one lane each, the page-table entries fetched a block ahead);
+//   warp 2      loads the blocks of V in the same way;
 //   warp 1      issues S_t = Q_t K^T and O_t += P_t V;
 //   warps 4-7, 8-11  softmax of sub-tile 0, 1: one thread per row.
 // The sub-tiles ping-pong, and the next segment's loads and first products overlap the
@@ -220,32 +221,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto phase_of = [](uint32_t n) -> uint32_t { return (n / kStages) & 1; };
 
     // Loads the blocks of a segment into the K or the V ring and counts them in N, the blocks
-    // loaded so far (whole warp; false: a wait ran out).  Lane: box lane / kBoxes of the block's
-    // pages, columns 64 (lane mod kBoxes).
+    // loaded so far (whole warp; false: a wait ran out).  Lane: box lane / kBoxes of the block,
+    // columns 64 (lane mod kBoxes).
     auto load_blocks = [&](const Seg& s, const CUtensorMap* map, int ring, int full, int empty,
                            uint32_t& N, bool leader) -> bool {
         const uint64_t policy = s.once ? l2_policy_evict_first() : l2_policy_evict_last();
-        const int box_rows = min(a.page_size, kKeys);
+        const int box_rows = p.box_rows;
         const int my_box = lane / Lay::kBoxes, my_col = lane % Lay::kBoxes;
-        const bool loads = my_box < kKeys / box_rows;         // at most 16 pages a block
+        const bool loads = my_box < kKeys / box_rows;         // at most 16 boxes a block
         const uint32_t to = my_col * 16384 + my_box * box_rows * 128;
-        // the page of this lane's box of the block at key kb: an index outside the cache
-        // (zeros) behind the last key and for an entry that names no page
-        auto page_of = [&](int kb) -> int {
+        // the page and slot of this lane's box of the block at key kb: an index outside the
+        // cache (zeros) behind the last key and for an entry that names no page
+        auto page_of = [&](int kb, int& in_page) -> int {
             const int key = kb + my_box * box_rows;
+            const int col = p.page_shift >= 0 ? key >> p.page_shift : key / a.page_size;
             int page = -1;
-            if (loads && key < s.kv) {
-                const int col = p.page_shift >= 0 ? key >> p.page_shift : key / a.page_size;
+            if (loads && key < s.kv)
                 page = checked_ldg(a.page_table, s.g * a.table_stride + col, a.table_elems, a.status);
-            }
+            in_page = key - col * a.page_size;
             return static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages) ? page
                                                                                   : a.num_pages;
         };
-        int page = page_of(s.k0);
+        int in_page = 0, in_next = 0;
+        int page = page_of(s.k0, in_page);
         for (int n = 0; n < s.n_blocks; ++n, ++N) {
             const int kb = s.k0 + n * kKeys;
-            const int in_page = a.page_size > kKeys ? kb % a.page_size : 0;
-            const int page_next = n + 1 < s.n_blocks ? page_of(kb + kKeys) : 0;
+            const int page_next = n + 1 < s.n_blocks ? page_of(kb + kKeys, in_next) : 0;
             const int st = stage_of(N);
             if (!__all_sync(0xffffffffu, mbar_wait(bar(empty + st), phase_of(N) ^ 1, wc)))
                 return false;
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_4d(sbase + ring + st * Lay::kTile + to, map, bar(full + st), my_col * 64,
                             s.hk, in_page, page, policy);
             page = page_next;
+            in_page = in_next;
         }
         return true;
     };
@@ -813,13 +815,12 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
 
 bool paged_tc_applies(const PagedArgs& a)
 {
-    // A page must cover whole 8-row swizzle atoms of a 128-key block, or whole blocks, a
-    // sub-tile at least one token, and the strides fit a tensor map (2^40 bytes).
+    // A page must hold whole 8-row swizzle atoms, a sub-tile at least one token, and the
+    // strides must fit a tensor map (2^40 bytes).
     const long long most = 1ll << 39;
     if (a.q_stride >= most || a.page_stride >= most || a.token_stride >= most || a.head_stride >= most)
         return false;
-    const bool pages = a.page_size % 8 == 0 && (kKeys % a.page_size == 0 || a.page_size % kKeys == 0);
-    if (a.elem != 2 || !pages || a.H / a.H_kv > kSub) return false;
+    if (a.elem != 2 || a.page_size % 8 != 0 || a.H / a.H_kv > kSub) return false;
     // More than one 16-row tile per sequence and key head on average (the lengths are not known
     // here).  Measured, few-rows kernel against this one, head dim 128, 8 key heads: 32
     // sequences of up to 8000 keys, 16 rows 108 us against 100, 20 rows 182 against 102, 64
@@ -835,6 +836,10 @@ cudaError_t launch_paged_tc(const PagedArgs& a)
     fill_params(&p, a);
     const int sub_tokens = kSub / p.G;
     p.tile_tokens = 2 * sub_tokens;
+    // a block is loaded in boxes of as many keys as divide both it and a page: a box never
+    // crosses a page (24 slots: boxes of 8)
+    p.box_rows = a.page_size & -a.page_size;
+    if (p.box_rows > kKeys) p.box_rows = kKeys;
     using ull = unsigned long long;
     const ull D = static_cast<ull>(a.D);
     CUtensorMap tq, tk, tv;
@@ -847,7 +852,7 @@ cudaError_t launch_paged_tc(const PagedArgs& a)
     const ull ks[3] = {a.H_kv > 1 ? 2ull * a.head_stride : 2 * D,
                        a.page_size > 1 ? 2ull * a.token_stride : 2 * D,
                        a.num_pages > 1 ? 2ull * a.page_stride : 2 * D};
-    const unsigned kb[4] = {64, 1, static_cast<unsigned>(a.page_size < kKeys ? a.page_size : kKeys), 1};
+    const unsigned kb[4] = {64, 1, static_cast<unsigned>(p.box_rows), 1};
     if (!encode_bf16_map(&tq, a.q, 3, qd, qs, qb) || !encode_bf16_map(&tk, a.k_pages, 4, kd, ks, kb) ||
         !encode_bf16_map(&tv, a.v_pages, 4, kd, ks, kb))
         return cudaErrorInvalidValue;

@@ -39,6 +39,7 @@ struct PagedParams {
     int key_shift_single;   // StepTiles: the same in a tile with one sub-tile of rows
     int tile_tokens;        // new tokens of a tile (StepTiles)
     int page_shift;         // log2 of the page size, or -1
+    int box_rows;           // keys of one tensor-map box (tensor-core kernel)
     unsigned g_magic;       // division by G: see token_of
     int g_shift;
     // r / G of a packed row (r < 2^31), by multiplication

@@ -225,7 +225,7 @@ cudaError_t launch_paged(const PagedArgs& a);        // chooses among:
 cudaError_t launch_paged_simt(const PagedArgs& a);   // fp32
 cudaError_t launch_paged_bf16(const PagedArgs& a);   // bf16, few rows per key/value head
 // bf16, many rows: CTAs, and tensor maps of q ({D, H, T}, boxes of 64 x G x tokens) and of
-// the pages ({D, H_kv, page_size, num_pages}, boxes of 64 x 1 x min(page_size, 128) x 1).
+// the pages ({D, H_kv, page_size, num_pages}, boxes of 64 x 1 x keys of one page x 1).
 bool paged_tc_applies(const PagedArgs& a);
 cudaError_t launch_paged_tc(const PagedArgs& a);
 

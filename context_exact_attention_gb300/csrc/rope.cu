@@ -21,8 +21,8 @@
 // in shared memory, and then stream the tokens' heads, two rows in flight each.  A thread
 // keeps one item of a head vector -- a 16-byte vector of each half of the pairs (half style),
 // a vector of whole pairs (interleaved), or a vector of the dims behind `rot` -- and walks
-// over the tokens, so that only its pointers move.  Head vectors whose pairs do not fill
-// 16-byte vectors go one pair at a time through the same code (kVec false).
+// over the tokens, so that only its pointers move.  In the half style a rot/2 that is no
+// multiple of the vector takes pieces of the width that divides it, down to single elements.
 // Measured: 32768 tokens of 64 heads of 128 dims in bf16 in 161 to 164 us, 6.5 to 6.7 TB/s
 // (the measured copy rate is 6.69); before the items kept their columns and the sines lay
 // where neighbouring lanes read them side by side it was 214 us, bound by instructions.
@@ -148,79 +148,85 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v)
     return pack_bf16x2(lo, hi);
 }
 
-// Rotates the 16-byte vectors of an item.  cs, sn: the item's cosines and sines, four at a
-// time, `step` groups of four apart.
-template <typename T, bool kHalfStyle>
-__device__ __forceinline__ void rotate_vec(uint4& x0, uint4& x1, const float4* cs, const float4* sn,
-                                           int step)
+// A piece of N elements, moved in one access.
+template <typename T, int N>
+struct alignas(N * sizeof(T)) Piece {
+    T e[N];
+};
+
+// Rotates an item: pieces x0, x1 of N pairs' first and second elements (half style), or x0 with
+// N / 2 whole pairs, the first `pairs` of which turn (interleaved).  cs, sn: the item's cosines
+// and sines in groups of kGroup, `step` floats apart.
+template <typename T, bool kHalfStyle, int N, int kGroup>
+__device__ __forceinline__ void rotate_item(Piece<T, N>& x0, Piece<T, N>& x1, const float* cs,
+                                            const float* sn, int step, int pairs)
 {
-    uint32_t* a = reinterpret_cast<uint32_t*>(&x0);
-    uint32_t* b = reinterpret_cast<uint32_t*>(&x1);
-    if constexpr (sizeof(T) == 2 && kHalfStyle) {
+    using Floats = Piece<float, kGroup>;
+    constexpr int kPairs = kHalfStyle ? N : N / 2;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const float4 c = cs[q * step], s = sn[q * step];
-            uint64_t ya, yb;
-            turn2(unpack2(a[2 * q]), unpack2(b[2 * q]), f2pack(c.x, c.y), f2pack(s.x, s.y), ya, yb);
-            a[2 * q] = pack2(ya);
-            b[2 * q] = pack2(yb);
-            turn2(unpack2(a[2 * q + 1]), unpack2(b[2 * q + 1]), f2pack(c.z, c.w), f2pack(s.z, s.w),
-                  ya, yb);
-            a[2 * q + 1] = pack2(ya);
-            b[2 * q + 1] = pack2(yb);
-        }
-    } else if constexpr (sizeof(T) == 2) {
-        const float4 c = cs[0], s = sn[0];
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    for (int g = 0; g < kPairs / kGroup; ++g) {
+        const Floats c = *reinterpret_cast<const Floats*>(cs + g * step);
+        const Floats s = *reinterpret_cast<const Floats*>(sn + g * step);
+        if constexpr (kHalfStyle && sizeof(T) == 2 && kGroup >= 2) {
+            uint32_t* a = reinterpret_cast<uint32_t*>(&x0.e[g * kGroup]);
+            uint32_t* b = reinterpret_cast<uint32_t*>(&x1.e[g * kGroup]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float xa = __uint_as_float(a[i] << 16), xb = __uint_as_float(a[i] & 0xffff0000u);
-            a[i] = pack_bf16x2(fmaf(xa, cc[i], -(xb * ss[i])), fmaf(xb, cc[i], xa * ss[i]));
-        }
-    } else if constexpr (kHalfStyle) {
-        const float4 c = cs[0], s = sn[0];
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+            for (int i = 0; i < kGroup / 2; ++i) {
+                uint64_t ya, yb;
+                turn2(unpack2(a[i]), unpack2(b[i]), f2pack(c.e[2 * i], c.e[2 * i + 1]),
+                      f2pack(s.e[2 * i], s.e[2 * i + 1]), ya, yb);
+                a[i] = pack2(ya);
+                b[i] = pack2(yb);
+            }
+        } else if constexpr (!kHalfStyle && sizeof(T) == 2) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x0.e[2 * g * kGroup]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float xa = __uint_as_float(a[i]), xb = __uint_as_float(b[i]);
-            a[i] = __float_as_uint(fmaf(xa, cc[i], -(xb * ss[i])));
-            b[i] = __float_as_uint(fmaf(xb, cc[i], xa * ss[i]));
-        }
-    } else {
-        const float2 c = *reinterpret_cast<const float2*>(cs), s = *reinterpret_cast<const float2*>(sn);
-        const float cc[2] = {c.x, c.y}, ss[2] = {s.x, s.y};
+            for (int i = 0; i < kGroup; ++i) {
+                const float xa = __uint_as_float(w[i] << 16), xb = __uint_as_float(w[i] & 0xffff0000u);
+                const uint32_t y = pack_bf16x2(fmaf(xa, c.e[i], -(xb * s.e[i])),
+                                               fmaf(xb, c.e[i], xa * s.e[i]));
+                w[i] = g * kGroup + i < pairs ? y : w[i];
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float xa = __uint_as_float(a[2 * i]), xb = __uint_as_float(a[2 * i + 1]);
-            a[2 * i] = __float_as_uint(fmaf(xa, cc[i], -(xb * ss[i])));
-            a[2 * i + 1] = __float_as_uint(fmaf(xb, cc[i], xa * ss[i]));
+            for (int i = 0; i < kGroup; ++i) {
+                const int j = g * kGroup + i;
+                T& ea = kHalfStyle ? x0.e[j] : x0.e[(2 * j) % N];
+                T& eb = kHalfStyle ? x1.e[j] : x0.e[(2 * j + 1) % N];
+                const float xa = to_f(ea), xb = to_f(eb);
+                const T ya = from_f<T>(fmaf(xa, c.e[i], -(xb * s.e[i])));
+                const T yb = from_f<T>(fmaf(xb, c.e[i], xa * s.e[i]));
+                if (kHalfStyle || j < pairs) {
+                    ea = ya;
+                    eb = yb;
+                }
+            }
         }
     }
 }
 
-// kVec: items are 16-byte vectors; otherwise single pairs (and single elements behind
-// `rot`).  kPaged: the heads are q's (to q_out), k's (rotated, to the pages) and v's (to the
-// pages).
-template <typename T, bool kHalfStyle, bool kVec, bool kPaged>
+// N: elements of a piece (a 16-byte vector, or in the half style fewer where half of `rot` is
+// no multiple of that).  Interleaved, an item is one vector and the one that `rot` ends in
+// turns its first pairs only.  kPaged: the heads are q's (to q_out), k's (rotated, to the
+// pages) and v's (to the pages).
+template <typename T, bool kHalfStyle, int N, bool kPaged>
 __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__ RopeArgs a)
 {
-    constexpr int kFull = 16 / sizeof(T);          // elements of a 16-byte vector
-    // elements of a rotated item's piece, and the pairs of an item
-    constexpr int kN = kVec ? kFull : (kHalfStyle ? 1 : 2);
-    constexpr int kPairs = kHalfStyle ? kN : kN / 2;
-    constexpr int kPassN = kVec ? kFull : 1;       // elements of an item behind `rot`
+    constexpr int kPairs = kHalfStyle ? N : N / 2;
     // sines and cosines lie in groups of kGroup (what one read of an item takes), group g of
     // an item behind group g of all items before it, so that neighbouring lanes read
     // neighbouring groups
     constexpr int kGroup = kPairs < 4 ? kPairs : 4;
+    using Vec = Piece<T, N>;
 
     __shared__ alignas(16) float cos_s[kMaxPairs];
     __shared__ alignas(16) float sin_s[kMaxPairs];
     __shared__ TokenPos tok_s[kMaxTokens];
 
     const int half = a.rot / 2;
-    const int rot_items = half / kPairs;
-    const int n_items = rot_items + (a.D - a.rot) / kPassN;
+    const int rot_items = (half + kPairs - 1) / kPairs;
+    const int n_items = rot_items + (a.D - a.rot) / N;
+    const int cs_row = rot_items * kPairs;         // sines and cosines of a token
     const int heads = a.H + (kPaged ? 2 : 1) * a.H_kv;
     const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
     const int n_tok = static_cast<int>(min(static_cast<long long>(a.tokens), a.rows - t0));
@@ -233,7 +239,7 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
     const int first_tok = row / step_h;
     const bool works = first_tok < step_t;
     const bool rotates = item < rot_items;
-    const int c0 = rotates ? item * kN : a.rot + (item - rot_items) * kPassN;
+    const int c0 = kHalfStyle && !rotates ? a.rot + (item - rot_items) * N : item * N;
 
     int h = row - first_tok * step_h, tok = first_tok;
     const T* src = nullptr;
@@ -259,28 +265,21 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
         src = static_cast<const T*>(s) + si + c0;
         dst = static_cast<T*>(d) + di + c0;
     };
-    struct Piece {
-        uint4 x0, x1;           // kVec: the vectors; else elements in x0.x and x1.x (x0.y)
+    struct Row {
+        Vec x0, x1;             // x1: half style, rotated items
         T* dst;
         long long di;
         int tok, kind;          // tok: n_tok if there is none
     };
-    auto fetch = [&](Piece& r) {
+    auto fetch = [&](Row& r) {
         r.tok = tok;
         if (tok >= n_tok) return;
         r.kind = kind;
         r.dst = dst;
         r.di = di;
         if (in_bounds(si, a.D, kind == 0 ? a.q_elems : kind == 1 ? a.k_elems : a.v_elems, a.status)) {
-            if constexpr (kVec) {
-                r.x0 = *reinterpret_cast<const uint4*>(src);
-                if (kHalfStyle && rotates) r.x1 = *reinterpret_cast<const uint4*>(src + half);
-            } else {
-                T* e0 = reinterpret_cast<T*>(&r.x0);
-                T* e1 = reinterpret_cast<T*>(&r.x1);
-                e0[0] = src[0];
-                if (rotates) e1[0] = src[kHalfStyle ? half : 1];
-            }
+            r.x0 = *reinterpret_cast<const Vec*>(src);
+            if (kHalfStyle && rotates) r.x1 = *reinterpret_cast<const Vec*>(src + half);
         }
         src += src_step;
         dst += dst_step;
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
             }
         }
     };
-    auto finish = [&](Piece& r) {
+    auto finish = [&](Row& r) {
         if (r.tok >= n_tok) return;
         const TokenPos p = tok_s[r.tok];
         T* out = r.dst;
@@ -309,31 +308,19 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
         }
         if (!in_bounds(at, a.D, r.kind == 0 ? a.q_out_elems : a.k_out_elems, a.status)) return;
         // (the paged append's values stay as they are)
-        const bool turns = rotates && (!kPaged || r.kind < 2);
-        const int at_cs = r.tok * half + item * kGroup;
-        if constexpr (kVec) {
-            if (turns)
-                rotate_vec<T, kHalfStyle>(r.x0, r.x1, reinterpret_cast<const float4*>(cos_s + at_cs),
-                                          reinterpret_cast<const float4*>(sin_s + at_cs), rot_items);
-            *reinterpret_cast<uint4*>(out) = r.x0;
-            if (kHalfStyle && rotates) *reinterpret_cast<uint4*>(out + half) = r.x1;
-        } else {
-            T* e0 = reinterpret_cast<T*>(&r.x0);
-            T* e1 = reinterpret_cast<T*>(&r.x1);
-            if (turns) {
-                const float xa = to_f(e0[0]), xb = to_f(e1[0]), c = cos_s[at_cs], s = sin_s[at_cs];
-                e0[0] = from_f<T>(fmaf(xa, c, -(xb * s)));
-                e1[0] = from_f<T>(fmaf(xb, c, xa * s));
-            }
-            out[0] = e0[0];
-            if (rotates) out[kHalfStyle ? half : 1] = e1[0];
+        if (rotates && (!kPaged || r.kind < 2)) {
+            const int cs = r.tok * cs_row + item * kGroup;
+            rotate_item<T, kHalfStyle, N, kGroup>(r.x0, r.x1, cos_s + cs, sin_s + cs,
+                                                  rot_items * kGroup, half - item * kPairs);
         }
+        *reinterpret_cast<Vec*>(out) = r.x0;
+        if (kHalfStyle && rotates) *reinterpret_cast<Vec*>(out + half) = r.x1;
     };
 
     if (!works || h >= heads) tok = n_tok;
     if (tok < n_tok) enter();
     // the first rows are on their way while the positions and angles are worked out
-    Piece r[kAhead];
+    Row r[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) fetch(r[u]);
 
@@ -352,7 +339,7 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
         float s, c;
         sincospif(x, &s, &c);
         const int of = pair / kPairs, in = pair % kPairs;
-        const int at = tk * half + ((in / kGroup) * rot_items + of) * kGroup + in % kGroup;
+        const int at = tk * cs_row + ((in / kGroup) * rot_items + of) * kGroup + in % kGroup;
         cos_s[at] = c * a.amplitude;
         sin_s[at] = s * a.amplitude * a.sign;
     }
@@ -368,13 +355,13 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
     }
 }
 
-template <typename T, bool kHalfStyle, bool kVec>
+template <typename T, bool kHalfStyle, int N>
 cudaError_t launch(RopeArgs& a, int sms)
 {
+    constexpr int kPairs = kHalfStyle ? N : N / 2;
     const int half = a.rot / 2, heads = a.H + (a.paged ? 2 : 1) * a.H_kv;
-    constexpr int kN = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;
-    const int pairs = kHalfStyle ? kN : (kN > 1 ? kN / 2 : 1);
-    const int items = half / pairs + (a.D - a.rot) / kN;          // at most 256
+    const int rot_items = (half + kPairs - 1) / kPairs, cs_row = rot_items * kPairs;
+    const int items = rot_items + (a.D - a.rot) / N;              // at most 256
     // Threads: a token's heads in equal parts of at most 256 threads, so that no part runs
     // with idle rows, or several tokens of few heads at once.  Measured: 48 heads of 8 items
     // (15,000 tokens appended) take 61 us in two parts of 24 rows; 68 in one of 48 (fewer
@@ -394,7 +381,7 @@ cudaError_t launch(RopeArgs& a, int sms)
     // eight blocks per SM while there are rows for them.
     int most = half > 0 ? 256 / half : kMaxTokens;
     if (most < a.step_t) most = a.step_t;
-    if (half > 0 && most > kMaxPairs / half) most = kMaxPairs / half;
+    if (half > 0 && most > kMaxPairs / cs_row) most = kMaxPairs / cs_row;
     if (most > kMaxTokens) most = kMaxTokens;
     long long per = a.rows / (8ll * sms);
     if (per < 1) per = 1;
@@ -402,8 +389,8 @@ cudaError_t launch(RopeArgs& a, int sms)
     const long long blocks = (a.rows + a.tokens - 1) / a.tokens;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (a.paged) rope_kernel<T, kHalfStyle, kVec, true><<<grid, threads, 0, a.stream>>>(a);
-    else rope_kernel<T, kHalfStyle, kVec, false><<<grid, threads, 0, a.stream>>>(a);
+    if (a.paged) rope_kernel<T, kHalfStyle, N, true><<<grid, threads, 0, a.stream>>>(a);
+    else rope_kernel<T, kHalfStyle, N, false><<<grid, threads, 0, a.stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -411,11 +398,15 @@ template <typename T>
 cudaError_t launch_t(RopeArgs& a, int sms)
 {
     constexpr int kFull = 16 / sizeof(T);
-    // whole 16-byte vectors of pairs: each half (half style) or the rotated part
-    // (interleaved) a multiple of the vector
-    if (a.half_style)
-        return a.rot % (2 * kFull) == 0 ? launch<T, true, true>(a, sms) : launch<T, true, false>(a, sms);
-    return a.rot % kFull == 0 ? launch<T, false, true>(a, sms) : launch<T, false, false>(a, sms);
+    if (!a.half_style) return launch<T, false, kFull>(a, sms);
+    // the widest pieces that each half is whole pieces of (then the dims behind `rot` are too:
+    // D is a multiple of kFull)
+    const int half = a.rot / 2;
+    if (half % kFull == 0) return launch<T, true, kFull>(a, sms);
+    if (half % (kFull / 2) == 0) return launch<T, true, kFull / 2>(a, sms);
+    if constexpr (kFull == 8)
+        if (half % 2 == 0) return launch<T, true, 2>(a, sms);
+    return launch<T, true, 1>(a, sms);
 }
 
 }  // namespace

@@ -35,6 +35,11 @@ CASES = [
     (3, 16, 2, 0, 80, 40, "half", "zigzag", 2, torch.bfloat16),      # 20 a half: pair by pair
     (1, 101, 0, 3, 72, 70, "interleaved", "packed", 1, torch.bfloat16),
     (1, 101, 6, 2, 256, 64, "interleaved", "packed", 1, torch.bfloat16),
+    (1, 101, 3, 2, 128, 2, "interleaved", "packed", 1, torch.bfloat16),
+    (2, 9, 3, 1, 64, 24, "half", "contiguous", 1, torch.bfloat16),   # 12 a half: pieces of four
+    (2, 9, 3, 1, 80, 20, "half", "contiguous", 1, torch.bfloat16),   # 10: pieces of two
+    (2, 9, 3, 1, 128, 126, "half", "contiguous", 1, torch.bfloat16), # 63: single elements
+    (2, 9, 3, 1, 128, 122, "interleaved", "contiguous", 1, torch.float32),
     (1, 60, 2, 2, 256, 2, "half", "contiguous", 1, torch.bfloat16),  # one pair, 254 passing
     (2, 33, 3, 1, 64, 48, "half", "contiguous", 1, torch.float32),
     (1, 101, 3, 1, 100, 100, "half", "packed", 1, torch.float32),    # 50 a half
@@ -128,6 +133,19 @@ def test_views_of_a_fused_projection():
     assert cea.check_status() == 0
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
     assert torch.equal(dev[:, :, H + H_kv:].cpu(), qkv[:, :, H + H_kv:])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("style", ["half", "interleaved"])
+def test_dims_behind_the_rotation_pass_whatever_they_are(dtype, style):
+    """NaN and infinities behind `rot`, in the vector that the rotation ends in too."""
+    x = torch.randn(1, 6, 2, 64, generator=torch.Generator().manual_seed(9)).to(dtype)
+    x[..., 54:] = torch.tensor([float("nan"), float("inf"), -float("inf"), -0.0, 1e30] * 2).to(dtype)
+    got, _ = cea.rope_fwd(x.to(DEV), None, cea.rope_table(54, style=style, amplitude=3.0, device=DEV),
+                          offset=5)
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    assert torch.equal(got[..., 54:].cpu().view(bits), x[..., 54:].view(bits))
+    assert torch.isfinite(got[..., :54]).all()
 
 
 def test_rows_of_no_sequence_are_left():
