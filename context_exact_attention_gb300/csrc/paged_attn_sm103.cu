@@ -801,7 +801,12 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     p.key_shift_single = D == 64 ? 0 : 1;
     p.tile_cost = 256 << p.key_shift;
     p.snap = 3 * kKeys;
-    p.min_chunk = 2 * kKeys << p.key_shift;
+    p.min_chunk = 3 * kKeys << p.key_shift;
+    // 10 cycles a unit: 6000 cycles a partial of two sub-tiles, 2000 of a single one.  Measured
+    // with the rule that this feeds and without: 297 tokens over 11606 keys of 2 heads 52 us
+    // against 59 (69 with parts of 2 blocks at least instead of 3), 8 tokens over 4000 keys of 8
+    // heads 20 against 22.
+    p.join_cost = static_cast<long long>(p.a.T) * p.G > static_cast<long long>(kSub) * p.a.n_seqs ? 600 : 200;
     const PagedWorkspace w = paged_workspace_of(p.grid, 2 * kSub, D);
     uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
     p.counters = reinterpret_cast<unsigned int*>(ws);
