@@ -22,7 +22,7 @@
 // keeps one item of a head vector -- a 16-byte vector of each half of the pairs (half style),
 // a vector of whole pairs (interleaved), or a vector of the dims behind `rot` -- and walks
 // over the tokens, so that only its pointers move.  In the half style a rot/2 that is no
-// multiple of the vector takes pieces of the width that divides it, down to single elements.
+// multiple of the vector takes pieces of half of one, or rope_shift_kernel below.
 // Measured: 32768 tokens of 64 heads of 128 dims in bf16 in 161 to 164 us, 6.5 to 6.7 TB/s
 // (the measured copy rate is 6.69); before the items kept their columns and the sines lay
 // where neighbouring lanes read them side by side it was 214 us, bound by instructions.
@@ -112,6 +112,14 @@ __device__ __forceinline__ TokenPos token_pos(const RopeArgs& a, long long t)
         r.pos += a.position_offset;
         return r;
     }
+}
+
+// Sine and cosine of position times phase.
+__device__ __forceinline__ void angle_of(unsigned long long phase, long long pos, float& s, float& c)
+{
+    const unsigned long long turn = phase * static_cast<unsigned long long>(pos);
+    // upper 32 bits as a signed number: [-2^31, 2^31) is [-1, 1) half turns
+    sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
 }
 
 template <typename T>
@@ -205,7 +213,7 @@ __device__ __forceinline__ void rotate_item(Piece<T, N>& x0, Piece<T, N>& x1, co
     }
 }
 
-// N: elements of a piece (a 16-byte vector, or in the half style fewer where half of `rot` is
+// N: elements of a piece (a 16-byte vector, or in the half style half of one where half of `rot` is
 // no multiple of that).  Interleaved, an item is one vector and the one that `rot` ends in
 // turns its first pairs only.  kPaged: the heads are q's (to q_out), k's (rotated, to the
 // pages) and v's (to the pages).
@@ -333,11 +341,8 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
         const int tk = i / half, pair = i - tk * half;
         unsigned long long ph = 0;
         if (in_bounds(pair, 1, half, a.status)) ph = __ldg(a.phases + pair);
-        const unsigned long long turn = ph * static_cast<unsigned long long>(tok_s[tk].pos);
-        // upper 32 bits as a signed number: [-2^31, 2^31) is [-1, 1) half turns
-        const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;
         float s, c;
-        sincospif(x, &s, &c);
+        angle_of(ph, tok_s[tk].pos, s, c);
         const int of = pair / kPairs, in = pair % kPairs;
         const int at = tk * cs_row + ((in / kGroup) * rot_items + of) * kGroup + in % kGroup;
         cos_s[at] = c * a.amplitude;
@@ -353,6 +358,156 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
             fetch(r[u]);
         }
     }
+}
+
+// ---- half style, rot / 2 no multiple of 8 bytes ----
+//
+// The partners of a vector's elements then straddle two vectors of the row.  A lane takes one
+// vector of the row, reads the two that hold its partners behind it (its first-half elements)
+// or before it (its second-half ones) -- the same lines, from L1 -- and shifts them into place
+// by whole words and half words, `half` modulo the vector's length being the same for all.
+// A row's lanes are in one warp, which has read everything before it stores, so rotating in
+// place is safe.  Per element: y = x C + partner S, with C and S laid out by element in
+// shared memory (S = -sin in the first half, +sin in the second).  What bounds it: the
+// instructions, five reads and the shifts per vector.
+constexpr int kShiftFloats = 2048;      // cosines of one block: tokens * D
+
+// The kFull elements from element s on of the two vectors a, b.
+template <typename T>
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int s)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    constexpr int kWord = 4 / sizeof(T);            // elements of a word
+    if (s & (2 * kWord)) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (s & kWord) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (kWord == 2 && (s & 1)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T, bool kPaged>
+__global__ void __launch_bounds__(256) rope_shift_kernel(const __grid_constant__ RopeArgs a)
+{
+    constexpr int kFull = 16 / sizeof(T);
+    __shared__ alignas(16) float c_s[kShiftFloats];
+    __shared__ alignas(16) float s_s[kShiftFloats];
+    __shared__ TokenPos tok_s[kMaxTokens];
+    const int half = a.rot / 2, D = a.D;
+    const int items = D / kFull;                    // at most 32
+    const int heads = a.H + (kPaged ? 2 : 1) * a.H_kv;
+    const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
+    const int n_tok = static_cast<int>(min(static_cast<long long>(a.tokens), a.rows - t0));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
+
+    for (int i = warp; i < n_tok; i += n_warps) {
+        const TokenPos p = token_pos<kPaged>(a, t0 + i);
+        if (lane == 0) tok_s[i] = p;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_tok * half; i += blockDim.x) {
+        const int tk = i / half, pair = i - tk * half;
+        unsigned long long ph = 0;
+        if (in_bounds(pair, 1, half, a.status)) ph = __ldg(a.phases + pair);
+        float s, c;
+        angle_of(ph, tok_s[tk].pos, s, c);
+        c *= a.amplitude;
+        s *= a.amplitude * a.sign;
+        c_s[tk * D + pair] = c_s[tk * D + half + pair] = c;
+        s_s[tk * D + pair] = -s;
+        s_s[tk * D + half + pair] = s;
+    }
+    __syncthreads();
+
+    const int abreast = 32 / items;                 // rows of a warp at a time
+    const int sub = lane / items, v = lane - sub * items;
+    const bool works = sub < abreast;
+    const int rows = n_tok * heads;
+    // partners behind the vector start at element e0 + half, those before it at e0 - half
+    const int e0 = v * kFull, shift = half % kFull;
+    const int behind = v + half / kFull, ahead = v - half / kFull - 1;
+    const bool first = e0 < half, second = e0 + kFull > half && e0 < a.rot;
+    for (int base = warp * abreast; base < rows; base += n_warps * abreast) {
+        const int r = base + sub;
+        const bool go = works && r < rows;
+        const int tk = go ? r / heads : 0, h = go ? r - tk * heads : 0;
+        const int kind = h < a.H ? 0 : h < a.H + a.H_kv ? 1 : 2;
+        const int hh = h - (kind == 0 ? 0 : kind == 1 ? a.H : a.H + a.H_kv);
+        const long long t = t0 + tk;
+        const TokenPos p = tok_s[tk];
+        const long long si = t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) +
+                             static_cast<long long>(hh) * D;
+        const bool to_page = kPaged && kind > 0;
+        const long long di = to_page ? p.slot + hh * a.head_stride
+                                     : t * (kind == 0 ? a.q_out_stride : a.k_out_stride) +
+                                           static_cast<long long>(hh) * D;
+        const bool write = go && (to_page ? p.slot >= 0 : p.live) &&
+                           in_bounds(si, D, kind == 0 ? a.q_elems : kind == 1 ? a.k_elems : a.v_elems,
+                                     a.status) &&
+                           in_bounds(di, D, kind == 0 ? a.q_out_elems : a.k_out_elems, a.status);
+        uint4 x = make_uint4(0, 0, 0, 0), after = x, before = x;
+        if (write) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + si);
+            x = src[v];
+            if (kind < 2 && first)
+                after = shifted<T>(src[min(behind, items - 1)], src[min(behind + 1, items - 1)], shift);
+            if (kind < 2 && second)
+                before = shifted<T>(src[max(ahead, 0)], src[max(ahead + 1, 0)], kFull - shift);
+        }
+        __syncwarp();
+        if (!write) continue;
+        if (kind < 2) {
+            T* e = reinterpret_cast<T*>(&x);
+            const T* pa = reinterpret_cast<const T*>(&after);
+            const T* pb = reinterpret_cast<const T*>(&before);
+            const float* c = c_s + tk * D + e0;
+            const float* s = s_s + tk * D + e0;
+#pragma unroll
+            for (int g = 0; g < kFull / 4; ++g) {
+                const float4 c4 = *reinterpret_cast<const float4*>(c + 4 * g);
+                const float4 s4 = *reinterpret_cast<const float4*>(s + 4 * g);
+                const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 4 * g + i;
+                    const float partner = to_f(e0 + j < half ? pa[j] : pb[j]);
+                    const T y = from_f<T>(fmaf(to_f(e[j]), cc[i], partner * ss[i]));
+                    if (e0 + j < a.rot) e[j] = y;
+                }
+            }
+        }
+        T* out = static_cast<T*>(kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out) + di;
+        reinterpret_cast<uint4*>(out)[v] = x;
+    }
+}
+
+template <typename T>
+cudaError_t launch_shift(RopeArgs& a, int sms)
+{
+    const int items = a.D / (16 / static_cast<int>(sizeof(T)));
+    const int heads = a.H + (a.paged ? 2 : 1) * a.H_kv;
+    // a token's heads by whole warps, up to eight
+    int warps = (heads + 32 / items - 1) / (32 / items);
+    if (warps > 8) warps = 8;
+    int most = kShiftFloats / a.D;
+    if (most > kMaxTokens) most = kMaxTokens;
+    long long per = a.rows / (8ll * sms);
+    if (per < 1) per = 1;
+    a.tokens = static_cast<int>(per < most ? per : most);
+    const long long blocks = (a.rows + a.tokens - 1) / a.tokens;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const unsigned grid = static_cast<unsigned>(blocks);
+    if (a.paged) rope_shift_kernel<T, true><<<grid, 32 * warps, 0, a.stream>>>(a);
+    else rope_shift_kernel<T, false><<<grid, 32 * warps, 0, a.stream>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename T, bool kHalfStyle, int N>
@@ -399,14 +554,19 @@ cudaError_t launch_t(RopeArgs& a, int sms)
 {
     constexpr int kFull = 16 / sizeof(T);
     if (!a.half_style) return launch<T, false, kFull>(a, sms);
-    // the widest pieces that each half is whole pieces of (then the dims behind `rot` are too:
-    // D is a multiple of kFull)
+    // half style: pieces of 16 or 8 bytes if each half is whole ones.  Else vectors with shifted
+    // partners (8913 tokens of 16 heads of 128 dims, bf16, 63 pairs: 29 us, piece by piece of 2
+    // bytes 43; 20 heads of 80, 10 pairs: 26, by 4 bytes 38; fp32, 10 heads of 128, 63 pairs: 29,
+    // by 4 bytes 35 -- while with 12 pairs of 64 dims in bf16 pieces of 8 bytes take 21.7 and
+    // this 23, with 50 of 100 in fp32 17 and 29) if a row fits a warp, as all in bf16 do; the
+    // wide rows of fp32 take single elements.
     const int half = a.rot / 2;
     if (half % kFull == 0) return launch<T, true, kFull>(a, sms);
     if (half % (kFull / 2) == 0) return launch<T, true, kFull / 2>(a, sms);
-    if constexpr (kFull == 8)
-        if (half % 2 == 0) return launch<T, true, 2>(a, sms);
-    return launch<T, true, 1>(a, sms);
+    if constexpr (sizeof(T) == 4) {
+        if (a.D > 32 * kFull) return launch<T, true, 1>(a, sms);
+    }
+    return launch_shift<T>(a, sms);
 }
 
 }  // namespace

@@ -32,19 +32,31 @@ CASES = [
     (2, 37, 5, 1, 128, 128, "half", "contiguous", 1, torch.bfloat16),
     (2, 37, 4, 4, 128, 128, "interleaved", "contiguous", 1, torch.bfloat16),
     (1, 48, 3, 2, 96, 32, "half", "zigzag", 3, torch.bfloat16),
-    (3, 16, 2, 0, 80, 40, "half", "zigzag", 2, torch.bfloat16),      # 20 a half: pair by pair
+    (3, 16, 2, 0, 80, 40, "half", "zigzag", 2, torch.bfloat16),      # 20 a half
     (1, 101, 0, 3, 72, 70, "interleaved", "packed", 1, torch.bfloat16),
     (1, 101, 6, 2, 256, 64, "interleaved", "packed", 1, torch.bfloat16),
     (1, 101, 3, 2, 128, 2, "interleaved", "packed", 1, torch.bfloat16),
-    (2, 9, 3, 1, 64, 24, "half", "contiguous", 1, torch.bfloat16),   # 12 a half: pieces of four
-    (2, 9, 3, 1, 80, 20, "half", "contiguous", 1, torch.bfloat16),   # 10: pieces of two
-    (2, 9, 3, 1, 128, 126, "half", "contiguous", 1, torch.bfloat16), # 63: single elements
+    (2, 9, 3, 1, 64, 24, "half", "contiguous", 1, torch.bfloat16),   # 12 a half
+    (2, 9, 3, 1, 80, 20, "half", "contiguous", 1, torch.bfloat16),   # 10
+    (2, 9, 3, 1, 128, 126, "half", "contiguous", 1, torch.bfloat16), # 63
     (2, 9, 3, 1, 128, 122, "interleaved", "contiguous", 1, torch.float32),
     (1, 60, 2, 2, 256, 2, "half", "contiguous", 1, torch.bfloat16),  # one pair, 254 passing
     (2, 33, 3, 1, 64, 48, "half", "contiguous", 1, torch.float32),
     (1, 101, 3, 1, 100, 100, "half", "packed", 1, torch.float32),    # 50 a half
     (1, 40, 3, 1, 4, 4, "interleaved", "zigzag", 2, torch.float32),
     (1, 2500, 7, 3, 128, 64, "half", "contiguous", 1, torch.float32),
+    # halves that end inside a vector: every remainder, rows of one to 32 vectors, no full warp
+    (1, 33, 1, 1, 8, 2, "half", "contiguous", 1, torch.bfloat16),
+    (1, 33, 1, 1, 8, 6, "half", "contiguous", 1, torch.bfloat16),
+    (2, 19, 5, 2, 24, 20, "half", "contiguous", 1, torch.bfloat16),
+    (1, 37, 3, 1, 256, 254, "half", "contiguous", 1, torch.bfloat16),
+    (1, 37, 3, 1, 256, 246, "half", "contiguous", 1, torch.bfloat16),
+    (1, 3000, 5, 3, 96, 90, "half", "packed", 1, torch.bfloat16),
+    (1, 33, 2, 1, 4, 2, "half", "contiguous", 1, torch.float32),
+    (1, 33, 3, 1, 128, 122, "half", "contiguous", 1, torch.float32),
+    (1, 34, 3, 1, 128, 124, "half", "contiguous", 1, torch.float32),
+    (1, 33, 3, 1, 132, 130, "half", "contiguous", 1, torch.float32),  # more than 32 vectors
+    (1, 33, 3, 1, 256, 252, "half", "contiguous", 1, torch.float32),
 ]
 
 
