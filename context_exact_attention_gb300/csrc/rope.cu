@@ -489,6 +489,44 @@ __global__ void __launch_bounds__(256) rope_shift_kernel(const __grid_constant__
     }
 }
 
+// Blocks of `threads` threads that the GPU holds at once.
+template <typename Kernel>
+cudaError_t slots_of(std::atomic<int>* known, Kernel kernel, int threads, int sms, int* slots)
+{
+    int ctas = 0;                                   // of 128 threads
+    const cudaError_t e = resident_ctas(known, kernel, 128, 0, &ctas);
+    if (e != cudaSuccess) return e;
+    const int per_sm = ctas / sms * 128 / threads;
+    *slots = sms * (per_sm > 0 ? per_sm : 1);
+    return cudaSuccess;
+}
+
+// Tokens of a block, up to `most`: the number whose blocks are done first, taking that the
+// blocks go in waves of `slots`, that a block takes as long as kFixed rows of a thread (start,
+// first reads, positions) besides its rows and angles, and that the last wave, where it is not
+// full, takes as long as a full one.  Measured, against eight blocks per SM whatever the heads
+// are: 8191 tokens of 16 heads of 96 in fp32 22 us and 23.6, 8913 of 20 heads of 64 (12 pairs,
+// bf16) 17 and 22, 8406 of 2 heads of 80 4.7 and 6.4; large calls the same.
+int best_tokens(const RopeArgs& a, int most, int threads, int heads, int half, int slots)
+{
+    constexpr int kFixed = 3;
+    int best = 1;
+    long long least = 0;
+    for (int t = 1; t <= most; ++t) {
+        const long long blocks = (a.rows + t - 1) / t;
+        const int rows = (t + a.step_t - 1) / a.step_t * ((heads + a.step_h - 1) / a.step_h);
+        const int angles = (t * half + threads - 1) / threads, tokens = (32 * t + threads - 1) / threads;
+        // halves of a row
+        const long long cost = (blocks + slots - 1) / slots * (2 * (kFixed + rows) + angles + tokens);
+        if (t == 1 || cost < least) {
+            least = cost;
+            best = t;
+        }
+        if (blocks <= slots) break;                 // one wave: longer blocks take longer
+    }
+    return best;
+}
+
 template <typename T>
 cudaError_t launch_shift(RopeArgs& a, int sms)
 {
@@ -499,9 +537,15 @@ cudaError_t launch_shift(RopeArgs& a, int sms)
     if (warps > 8) warps = 8;
     int most = kShiftFloats / a.D;
     if (most > kMaxTokens) most = kMaxTokens;
-    long long per = a.rows / (8ll * sms);
-    if (per < 1) per = 1;
-    a.tokens = static_cast<int>(per < most ? per : most);
+    a.step_h = warps * (32 / items);                // rows of a pass
+    a.step_t = 1;
+    int slots = 0;
+    static std::atomic<int> known[2][kMaxDevices];
+    const cudaError_t e =
+        a.paged ? slots_of(known[1], rope_shift_kernel<T, true>, 32 * warps, sms, &slots)
+                : slots_of(known[0], rope_shift_kernel<T, false>, 32 * warps, sms, &slots);
+    if (e != cudaSuccess) return e;
+    a.tokens = best_tokens(a, most, 32 * warps, heads, a.rot / 2, slots);
     const long long blocks = (a.rows + a.tokens - 1) / a.tokens;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(blocks);
@@ -532,15 +576,19 @@ cudaError_t launch(RopeArgs& a, int sms)
         a.step_t = 1;
     }
     const int threads = (a.step_h * a.step_t * items + 31) / 32 * 32;
-    // Tokens: as many as give every thread about one sine and cosine, but no fewer than
-    // eight blocks per SM while there are rows for them.
+    // Tokens of a block: up to as many as give every thread about one sine and cosine, or one
+    // pass over the tokens side by side.
     int most = half > 0 ? 256 / half : kMaxTokens;
     if (most < a.step_t) most = a.step_t;
     if (half > 0 && most > kMaxPairs / cs_row) most = kMaxPairs / cs_row;
     if (most > kMaxTokens) most = kMaxTokens;
-    long long per = a.rows / (8ll * sms);
-    if (per < 1) per = 1;
-    a.tokens = static_cast<int>(per < most ? per : most);
+    int slots = 0;
+    static std::atomic<int> known[2][kMaxDevices];
+    const cudaError_t e =
+        a.paged ? slots_of(known[1], rope_kernel<T, kHalfStyle, N, true>, threads, sms, &slots)
+                : slots_of(known[0], rope_kernel<T, kHalfStyle, N, false>, threads, sms, &slots);
+    if (e != cudaSuccess) return e;
+    a.tokens = best_tokens(a, most, threads, heads, half, slots);
     const long long blocks = (a.rows + a.tokens - 1) / a.tokens;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(blocks);
@@ -555,11 +603,11 @@ cudaError_t launch_t(RopeArgs& a, int sms)
     constexpr int kFull = 16 / sizeof(T);
     if (!a.half_style) return launch<T, false, kFull>(a, sms);
     // half style: pieces of 16 or 8 bytes if each half is whole ones.  Else vectors with shifted
-    // partners (8913 tokens of 16 heads of 128 dims, bf16, 63 pairs: 29 us, piece by piece of 2
-    // bytes 43; 20 heads of 80, 10 pairs: 26, by 4 bytes 38; fp32, 10 heads of 128, 63 pairs: 29,
-    // by 4 bytes 35 -- while with 12 pairs of 64 dims in bf16 pieces of 8 bytes take 21.7 and
-    // this 23, with 50 of 100 in fp32 17 and 29) if a row fits a warp, as all in bf16 do; the
-    // wide rows of fp32 take single elements.
+    // partners (8913 tokens of 16 heads of 128 dims, bf16, 63 pairs: 28 us, piece by piece of 2
+    // bytes 43; 20 heads of 80, 10 pairs: 25, by 4 bytes 38; fp32, 10 heads of 128, 63 pairs: 28,
+    // by 4 bytes 35 -- while with 12 pairs of 64 dims in bf16 pieces of 8 bytes take 17 and this
+    // 23, with 50 of 100 in fp32 17 and 29) if a row fits a warp, as all in bf16 do; the wide
+    // rows of fp32 take single elements.
     const int half = a.rot / 2;
     if (half % kFull == 0) return launch<T, true, kFull>(a, sms);
     if (half % (kFull / 2) == 0) return launch<T, true, kFull / 2>(a, sms);
