@@ -19,8 +19,8 @@
 // takes a few tokens.  Its threads first send for the rows they will rotate first, then work
 // out the tokens' positions and their tokens * rot/2 sines and cosines, once for all heads,
 // in shared memory, and then stream the tokens' heads, two rows in flight each.  A thread
-// keeps one item of a head vector -- a 16-byte vector of each half of the pairs (half style),
-// a vector of whole pairs (interleaved), or a vector of the dims behind `rot` -- and walks
+// keeps one item of a head vector -- a 16-byte vector of each half of the pairs, or a vector of
+// the dims behind `rot` (half style), or two vectors of whole pairs (interleaved) -- and walks
 // over the tokens, so that only its pointers move.  In the half style a rot/2 that is no
 // multiple of the vector takes pieces of half of one, or rope_shift_kernel below.
 // Measured: 32768 tokens of 64 heads of 128 dims in bf16 in 161 to 164 us, 6.5 to 6.7 TB/s
@@ -213,10 +213,24 @@ __device__ __forceinline__ void rotate_item(Piece<T, N>& x0, Piece<T, N>& x1, co
     }
 }
 
-// N: elements of a piece (a 16-byte vector, or in the half style half of one where half of `rot` is
-// no multiple of that).  Interleaved, an item is one vector and the one that `rot` ends in
-// turns its first pairs only.  kPaged: the heads are q's (to q_out), k's (rotated, to the
-// pages) and v's (to the pages).
+// How a head vector is shared out.  Half style: the rotating items are a piece of each half,
+// the others a piece behind `rot`.  Interleaved: item i of `all` is vectors i and i + all of
+// the `rotating` = D / N vectors of the head, of which each turns what lies before `rot`.
+// Measured with two vectors an item and with one: 8191 tokens of 16 heads of 96 in fp32 19.8 us
+// and 22.3, 1458 of 32 heads of 80 in bf16 5.2 and 6.5; single tokens 3.1 and 3.0.
+struct RopeItems {
+    int rotating, all;
+};
+template <bool kHalfStyle, int N>
+__host__ __device__ __forceinline__ RopeItems items_of(const RopeArgs& a)
+{
+    if (kHalfStyle) return {a.rot / 2 / N, a.rot / 2 / N + (a.D - a.rot) / N};
+    return {a.D / N, (a.D / N + 1) / 2};
+}
+
+// N: elements of a piece (a 16-byte vector, or in the half style half of one where half of `rot`
+// is no multiple of that).  kPaged: the heads are q's (to q_out), k's (rotated, to the pages)
+// and v's (to the pages).
 template <typename T, bool kHalfStyle, int N, bool kPaged>
 __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__ RopeArgs a)
 {
@@ -232,8 +246,8 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
     __shared__ TokenPos tok_s[kMaxTokens];
 
     const int half = a.rot / 2;
-    const int rot_items = (half + kPairs - 1) / kPairs;
-    const int n_items = rot_items + (a.D - a.rot) / N;
+    const RopeItems it = items_of<kHalfStyle, N>(a);
+    const int rot_items = it.rotating, n_items = it.all;
     const int cs_row = rot_items * kPairs;         // sines and cosines of a token
     const int heads = a.H + (kPaged ? 2 : 1) * a.H_kv;
     const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
@@ -247,6 +261,9 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
     const int first_tok = row / step_h;
     const bool works = first_tok < step_t;
     const bool rotates = item < rot_items;
+    // the item's second piece
+    const int apart = kHalfStyle ? half : n_items * N;
+    const bool two = kHalfStyle ? rotates : item + n_items < rot_items;
     const int c0 = kHalfStyle && !rotates ? a.rot + (item - rot_items) * N : item * N;
 
     int h = row - first_tok * step_h, tok = first_tok;
@@ -287,7 +304,7 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
         r.di = di;
         if (in_bounds(si, a.D, kind == 0 ? a.q_elems : kind == 1 ? a.k_elems : a.v_elems, a.status)) {
             r.x0 = *reinterpret_cast<const Vec*>(src);
-            if (kHalfStyle && rotates) r.x1 = *reinterpret_cast<const Vec*>(src + half);
+            if (two) r.x1 = *reinterpret_cast<const Vec*>(src + apart);
         }
         src += src_step;
         dst += dst_step;
@@ -320,9 +337,15 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
             const int cs = r.tok * cs_row + item * kGroup;
             rotate_item<T, kHalfStyle, N, kGroup>(r.x0, r.x1, cos_s + cs, sin_s + cs,
                                                   rot_items * kGroup, half - item * kPairs);
+            if (!kHalfStyle && two) {
+                const int cs1 = cs + n_items * kGroup;
+                rotate_item<T, kHalfStyle, N, kGroup>(r.x1, r.x0, cos_s + cs1, sin_s + cs1,
+                                                      rot_items * kGroup,
+                                                      half - (item + n_items) * kPairs);
+            }
         }
         *reinterpret_cast<Vec*>(out) = r.x0;
-        if (kHalfStyle && rotates) *reinterpret_cast<Vec*>(out + half) = r.x1;
+        if (two) *reinterpret_cast<Vec*>(out + apart) = r.x1;
     };
 
     if (!works || h >= heads) tok = n_tok;
@@ -505,8 +528,8 @@ cudaError_t slots_of(std::atomic<int>* known, Kernel kernel, int threads, int sm
 // blocks go in waves of `slots`, that a block takes as long as kFixed rows of a thread (start,
 // first reads, positions) besides its rows and angles, and that the last wave, where it is not
 // full, takes as long as a full one.  Measured, against eight blocks per SM whatever the heads
-// are: 8191 tokens of 16 heads of 96 in fp32 22 us and 23.6, 8913 of 20 heads of 64 (12 pairs,
-// bf16) 17 and 22, 8406 of 2 heads of 80 4.7 and 6.4; large calls the same.
+// are: 8191 tokens of 16 heads of 96 in fp32 22 us and 23.6 (one vector an item), 8913 of 20
+// heads of 64 (12 pairs, bf16) 17 and 22, 8406 of 2 heads of 80 4.7 and 6.4; large calls the same.
 int best_tokens(const RopeArgs& a, int most, int threads, int heads, int half, int slots)
 {
     constexpr int kFixed = 3;
@@ -559,13 +582,12 @@ cudaError_t launch(RopeArgs& a, int sms)
 {
     constexpr int kPairs = kHalfStyle ? N : N / 2;
     const int half = a.rot / 2, heads = a.H + (a.paged ? 2 : 1) * a.H_kv;
-    const int rot_items = (half + kPairs - 1) / kPairs, cs_row = rot_items * kPairs;
-    const int items = rot_items + (a.D - a.rot) / N;              // at most 256
+    const RopeItems it = items_of<kHalfStyle, N>(a);
+    const int cs_row = it.rotating * kPairs, items = it.all;      // at most 256 items
     // Threads: a token's heads in equal parts of at most 256 threads, so that no part runs
     // with idle rows, or several tokens of few heads at once.  Measured: 48 heads of 8 items
     // (15,000 tokens appended) take 61 us in two parts of 24 rows; 68 in one of 48 (fewer
-    // blocks per SM), 73 to 79 in parts of 32 and 16.  (16 heads of 24 items in one part of
-    // 384 threads would take 22 us instead of 24.)
+    // blocks per SM), 73 to 79 in parts of 32 and 16.
     if (heads * items <= 128) {
         a.step_h = heads;
         a.step_t = 256 / (heads * items);
@@ -580,7 +602,7 @@ cudaError_t launch(RopeArgs& a, int sms)
     // pass over the tokens side by side.
     int most = half > 0 ? 256 / half : kMaxTokens;
     if (most < a.step_t) most = a.step_t;
-    if (half > 0 && most > kMaxPairs / cs_row) most = kMaxPairs / cs_row;
+    if (cs_row > 0 && most > kMaxPairs / cs_row) most = kMaxPairs / cs_row;
     if (most > kMaxTokens) most = kMaxTokens;
     int slots = 0;
     static std::atomic<int> known[2][kMaxDevices];
