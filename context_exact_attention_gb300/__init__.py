@@ -861,6 +861,8 @@ def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out
     n_seqs = 0
     if packed != (cu_seqlens is not None):
         raise ValueError("cu_seqlens belongs to the packed layout, which needs it")
+    if not -2 ** 31 <= offset < 2 ** 31:
+        raise ValueError("offset must fit 32 bits")
     if packed:
         _index_tensor(cu_seqlens, "cu_seqlens", 1)
         n_seqs = cu_seqlens.shape[0] - 1

@@ -657,8 +657,8 @@ typedef struct {
  * apart (0: contiguous), so that all three may be views of a fused projection output.
  * q, q_out: both NULL, or q_out as q (in place allowed).  The pages must overlap nothing
  * else; k_pages and v_pages may alternate in one buffer.  If two rows map to one slot, what
- * it holds afterwards is, 16 bytes by 16 bytes, from either of them.  D * element size a multiple of 16 bytes, D <= 256.
- * Errors as rope_fwd.
+ * it holds afterwards is, element by element, from either of them.  D * element size a
+ * multiple of 16 bytes, D <= 256.  Errors as rope_fwd.
  */
 ra_status paged_kv_append(const ra_paged_desc* desc, const ra_rope* rope, const void* q,
                           long long q_stride, const void* k, long long k_stride, const void* v,

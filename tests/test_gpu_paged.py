@@ -190,6 +190,10 @@ APPEND = {
     "fp32": ([(17, 40), (1, 31)], 3, 1, 100, 16, F32, "slots", 0, 50, "half"),
     "early": ([(6, 2), (3, 0), (1, 9)], 2, 1, 64, 16, BF, "slots", 0, 64, "half"),
     "unrotated": ([(7, 30)], 2, 2, 256, 16, F32, "heads", 0, 0, "half"),
+    "interleaved wide": ([(40, 70), (2, 9)], 1, 1, 256, 16, BF, "slots", 1, 254, "interleaved"),
+    "interleaved odd": ([(9, 40), (1, 3)], 4, 2, 72, 16, BF, "slots", 0, 62, "interleaved"),
+    "half odd wide": ([(9, 40), (1, 3)], 4, 2, 256, 16, BF, "by_page", 0, 250, "half"),
+    "half of 8 bytes": ([(9, 40), (1, 3)], 4, 2, 64, 16, BF, "slots", 0, 24, "half"),
 }
 
 

@@ -200,6 +200,37 @@ def test_malformed_boundaries_stay_in_bounds(cu, monkeypatch):
     assert cea.check_status() == 0
 
 
+@pytest.mark.parametrize("rot,D,style,dtype", [
+    (126, 128, "half", torch.bfloat16), (20, 80, "half", torch.bfloat16), (2, 8, "half", torch.bfloat16),
+    (24, 64, "half", torch.bfloat16), (122, 128, "half", torch.float32), (130, 132, "half", torch.float32),
+    (62, 72, "interleaved", torch.bfloat16), (46, 100, "interleaved", torch.float32)])
+def test_in_place_and_checked_indices(rot, D, style, dtype, monkeypatch):
+    """Rows of a fused buffer, more than a wave of blocks of them, rotated in place and by the
+    index-checked build: the same bits, and nothing outside q and k changes."""
+    g = torch.Generator().manual_seed(rot)
+    H, H_kv, L = 3, 2, 3001
+    buf = torch.randn(1, L, H + 2 * H_kv, D, generator=g).to(dtype).to(DEV)
+    was = buf.clone()
+    table = cea.rope_table(rot, style=style, device=DEV)
+    q, k = buf[:, :, :H], buf[:, :, H:H + H_kv]
+    want = cea.rope_fwd(q, k, table, offset=-7)
+    angle = torch.arange(-7, L - 7, dtype=torch.float64)[:, None] * freqs(rot)
+    for x, y in zip((q, k), want):
+        ref, mag = rotate64(x[0].double().cpu(), angle, rot, style)
+        assert_rotated(y[0], ref, mag)
+    normal = cea.load_library()
+    monkeypatch.setattr(cea, "_lib", cea.load_debug_library(build_if_missing=True))
+    for x, y in zip(cea.rope_fwd(q, k, table, offset=-7), want):
+        assert torch.equal(x, y)
+    assert cea.check_status() == 0
+    monkeypatch.setattr(cea, "_lib", normal)
+    cea.rope_fwd(q, k, table, offset=-7, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(buf[:, :, H + H_kv:], was[:, :, H + H_kv:])
+    with pytest.raises(ValueError):
+        cea.rope_fwd(q, k, table, offset=2 ** 31)
+
+
 def test_captured_and_other_stream():
     x = torch.randn(2, 50, 4, 128, generator=torch.Generator().manual_seed(6)).to(
         torch.bfloat16).to(DEV)
