@@ -399,14 +399,15 @@ __device__ __forceinline__ long long part_slot(const TileRows& t, int cta)
 // and ordered before by a barrier); true in the last one.
 __device__ __forceinline__ bool arrive_last(const PagedParams& p, const TileRows& t)
 {
-    bool last = false;
-    __threadfence();
-    if (in_bounds(t.c_first, 1, kPagedMaxCtas, p.a.status)) {
-        last = atomicAdd(p.counters + t.c_first, 1u) ==
-               static_cast<unsigned>(t.c_last - t.c_first);
-        if (last) p.counters[t.c_first] = 0;           // as the next call expects it
-    }
-    __threadfence();
+    if (!in_bounds(t.c_first, 1, kPagedMaxCtas, p.a.status)) return false;
+    // releases what the barrier before ordered, the whole CTA's partial, and acquires the others'
+    unsigned before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                 : "=r"(before)
+                 : "l"(p.counters + t.c_first)
+                 : "memory");
+    const bool last = before == static_cast<unsigned>(t.c_last - t.c_first);
+    if (last) p.counters[t.c_first] = 0;               // as the next call expects it
     return last;
 }
 
