@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     __shared__ float2 stat_w[kWarps][kRows];
     __shared__ float2 stat[kRows];
     __shared__ int flag;
-    __shared__ alignas(16) float buf[kRows][kVec4 * 128];
+    __shared__ alignas(16) float4 part[kWarps][kRows][kVec4 * 32];   // the warps' sums; then the tile's
     const PagedArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = a.D;
@@ -99,9 +99,29 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
         look_up();
     };
     look_up();
+    // the queries of segment nt, fetched a segment ahead
+    float4 q_next[kRows][kVec4];
+    auto fetch_q = [&]() {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+            for (int u = 0; u < kVec4; ++u) {
+                const int c = 4 * (lane + 32 * u);
+                q_next[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (have_next && r < nt.rows && c < D) {
+                    const int pr = nt.row0 + r, tok = p.token_of(pr);
+                    const long long at = (nt.s.first + tok) * a.q_stride +
+                                         static_cast<long long>(nt.hk * p.G + (pr - tok * p.G)) * D + c;
+                    if (in_bounds(at, 4, a.q_elems, a.status)) q_next[r][u] = load4(Q + at);
+                }
+            }
+        }
+    };
+    fetch_q();
 #pragma unroll 1
     for (;;) {
-        if (have) finish_segment<float, kRows, kThreads, kVec4>(p, t, &buf[0][0], kVec4 * 128, stat, &flag);
+        if (have)
+            finish_segment<float, kRows, kThreads, kVec4>(p, t, &part[0][0][0].x, kVec4 * 128, stat, &flag);
         have = have_next;
         if (!have) break;
         t = nt;
@@ -109,22 +129,20 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
         in_next = lk >= t.k1;
         if (in_next) lk = have_next ? nt.k0 : 0;
         look_up();
-        float4 q[kRows][kVec4], o[kRows][kVec4];
+        // pairs of columns: (0, 1) and (2, 3) of the four
+        uint64_t q[kRows][kVec4][2], o[kRows][kVec4][2];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
 #pragma unroll
             for (int u = 0; u < kVec4; ++u) {
-                const int c = 4 * (lane + 32 * u);
-                q[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                o[r][u] = q[r][u];
-                if (r < t.rows && c < D) {
-                    const int pr = t.row0 + r, tok = p.token_of(pr);
-                    const long long at = (t.s.first + tok) * a.q_stride +
-                                         static_cast<long long>(t.hk * p.G + (pr - tok * p.G)) * D + c;
-                    if (in_bounds(at, 4, a.q_elems, a.status)) q[r][u] = load4(Q + at);
-                }
+                q[r][u][0] = f2pack(q_next[r][u].x, q_next[r][u].y);
+                q[r][u][1] = f2pack(q_next[r][u].z, q_next[r][u].w);
+                o[r][u][0] = o[r][u][1] = 0;
             }
         }
+        fetch_q();
+        // bits 4 j + r of the rows that the tile has
+        const unsigned rows_in = 0x11111111u * ((1u << t.rows) - 1);
         // this lane's score is of row lane & 3: the keys it sees are [0, seen)
         const int my_row = lane & 3, my_key = lane >> 2;
         int seen = 0;
@@ -141,28 +159,29 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             const uint8_t* stage = ring + (used % kStages) * (2 * kHalf);
             ++used;
             auto key_at = [&](int j, int u) {
-                return *reinterpret_cast<const float4*>(stage + (j * kVec4 + u) * 512);
+                return *reinterpret_cast<const ulonglong2*>(stage + (j * kVec4 + u) * 512);
             };
             auto value_at = [&](int j, int u) {
-                return *reinterpret_cast<const float4*>(stage + kHalf + (j * kVec4 + u) * 512);
+                return *reinterpret_cast<const ulonglong2*>(stage + kHalf + (j * kVec4 + u) * 512);
             };
             float s[32];
 #pragma unroll
             for (int j = 0; j < kTurn; ++j) {
-                float4 kk[kVec4];
+                ulonglong2 kk[kVec4];
 #pragma unroll
                 for (int u = 0; u < kVec4; ++u) kk[u] = key_at(j, u);
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {
-                    float x = 0.f;
+                    uint64_t x = fmul2(q[r][0][0], kk[0].x);
+                    x = ffma2(q[r][0][1], kk[0].y, x);
 #pragma unroll
-                    for (int u = 0; u < kVec4; ++u) {
-                        x = fmaf(q[r][u].x, kk[u].x, x);
-                        x = fmaf(q[r][u].y, kk[u].y, x);
-                        x = fmaf(q[r][u].z, kk[u].z, x);
-                        x = fmaf(q[r][u].w, kk[u].w, x);
+                    for (int u = 1; u < kVec4; ++u) {
+                        x = ffma2(q[r][u][0], kk[u].x, x);
+                        x = ffma2(q[r][u][1], kk[u].y, x);
                     }
-                    s[4 * j + r] = x;
+                    float lo, hi;
+                    f2unpack(x, lo, hi);
+                    s[4 * j + r] = lo + hi;
                 }
             }
 #pragma unroll
@@ -193,67 +212,73 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
                     const float ar = __shfl_sync(0xffffffffu, alpha, r);
 #pragma unroll
                     for (int u = 0; u < kVec4; ++u) {
-                        o[r][u].x *= ar;
-                        o[r][u].y *= ar;
-                        o[r][u].z *= ar;
-                        o[r][u].w *= ar;
+                        o[r][u][0] = fmul2(o[r][u][0], f2pack(ar, ar));
+                        o[r][u][1] = fmul2(o[r][u][1], f2pack(ar, ar));
                     }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < kTurn; ++j) {
-                float4 vv[kVec4];
+            // the values of key j, to the rows in `rows` (a bit each)
+            auto add_value = [&](int j, unsigned rows) {
+                ulonglong2 vv[kVec4];
 #pragma unroll
                 for (int u = 0; u < kVec4; ++u) vv[u] = value_at(j, u);
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {
                     const float w = __shfl_sync(0xffffffffu, pe, 4 * j + r);
-                    // a value that the row does not see stays out even if it is not finite
-                    if (!((vis >> (4 * j + r)) & 1)) continue;
+                    if (!((rows >> r) & 1)) continue;
 #pragma unroll
                     for (int u = 0; u < kVec4; ++u) {
-                        o[r][u].x = fmaf(w, vv[u].x, o[r][u].x);
-                        o[r][u].y = fmaf(w, vv[u].y, o[r][u].y);
-                        o[r][u].z = fmaf(w, vv[u].z, o[r][u].z);
-                        o[r][u].w = fmaf(w, vv[u].w, o[r][u].w);
+                        o[r][u][0] = ffma2(f2pack(w, w), vv[u].x, o[r][u][0]);
+                        o[r][u][1] = ffma2(f2pack(w, w), vv[u].y, o[r][u][1]);
                     }
                 }
+            };
+            if ((~vis & rows_in) == 0) {
+#pragma unroll
+                for (int j = 0; j < kTurn; ++j) add_value(j, 15);
+            } else {
+                // a value that a row does not see stays out even if it is not finite
+#pragma unroll 1
+                for (int j = 0; j < kTurn; ++j) add_value(j, vis >> (4 * j));
             }
         }
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
         // the four warps' results, joined in warp order
         if (lane < kRows) stat_w[warp][lane] = make_float2(m, l);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+            for (int u = 0; u < kVec4; ++u) {
+                float4 x;
+                f2unpack(o[r][u][0], x.x, x.y);
+                f2unpack(o[r][u][1], x.z, x.w);
+                part[warp][r][lane + 32 * u] = x;
+            }
+        }
         __syncthreads();
-        if (threadIdx.x < kRows) {
+#pragma unroll
+        for (int i = threadIdx.x; i < kRows * kVec4 * 32; i += kThreads) {
+            const int r = i / (kVec4 * 32), c = i % (kVec4 * 32);
             float M = -INFINITY, L = 0.f;
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat_w[w][threadIdx.x].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat_w[w][r].x);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float2 st = stat_w[w][threadIdx.x];
-                if (!(st.y == 0.f)) L += part_weight(st.x, st.y, M) * st.y;
+                const float2 st = stat_w[w][r];
+                const float f = part_weight(st.x, st.y, M);
+                if (!(st.y == 0.f)) L += f * st.y;
+                const float4 y = part[w][r][c];
+                x.x = fmaf(f, y.x, x.x);
+                x.y = fmaf(f, y.y, x.y);
+                x.z = fmaf(f, y.z, x.z);
+                x.w = fmaf(f, y.w, x.w);
             }
-            stat[threadIdx.x] = make_float2(M, L);
+            part[0][r][c] = x;                     // (which only this thread has read)
+            if (c == 0) stat[r] = make_float2(M, L);
         }
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w) {
-            if (warp == w) {
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    const float f = part_weight(stat_w[w][r].x, stat_w[w][r].y, stat[r].x);
-#pragma unroll
-                    for (int u = 0; u < kVec4; ++u) {
-                        float4* dst = reinterpret_cast<float4*>(&buf[r][4 * (lane + 32 * u)]);
-                        float4 x = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *dst;
-                        x.x = fmaf(f, o[r][u].x, x.x);
-                        x.y = fmaf(f, o[r][u].y, x.y);
-                        x.z = fmaf(f, o[r][u].z, x.z);
-                        x.w = fmaf(f, o[r][u].w, x.w);
-                        *dst = x;
-                    }
-                }
-            }
-            __syncthreads();
-        }
     }
     cp_async_wait<0>();
 }
