@@ -11,12 +11,15 @@
 // maximum over the keys (three shuffles), exponential, and the eight weights of a row are
 // read back by shuffle for the value sum.
 //
-// What bounds it: bytes, for up to four rows a head.  A turn moves 8 keys (8 KB at D 128)
-// for about 400 warp instructions, which an SM issues in 100 cycles; HBM delivers them in
-// about 350.  More rows per head (long prompts in fp32) are taken four at a time and
-// re-read the keys, which then come from L2.
-// Measured: 16 single tokens over 100 to 4000 keys of 2 heads of 128 (91 MB) in 28 us, 3.2 TB/s:
-// each CTA has only seven turns, and the call's fixed parts (plan, first reads, joining,
+// What bounds it: bytes, for up to four rows a head and long contexts.  A turn moves 8 keys (8
+// KB at D 128), which HBM delivers to an SM in about 350 cycles, for about 600 warp
+// instructions of one dependent chain, some 3000 cycles; so it takes many warps, and three
+// blocks of two stages do better than two of three (same bytes in flight): 40 tokens over 405
+// keys of 8 heads of 64, G 5, 41 us against 48, 195 tokens over 4763 keys of 8 heads 240
+// against 273, the case below 26.5 against 26.3.  More rows per head (long prompts in fp32) are
+// taken four at a time and re-read the keys, which then come from L2.
+// Measured: 16 single tokens over 100 to 4000 keys of 2 heads of 128 (91 MB) in 26 us, 3.5 TB/s:
+// each warp has only five turns, and the call's fixed parts (plan, first reads, joining,
 // launch: about 10 us) show.  Loading straight into registers, a turn at a time, took 33 to 37.
 #include "paged_plan.cuh"
 
@@ -29,7 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTurn = 8;                       // keys per warp and turn
 constexpr int kUnit = kTurn * kWarps;
 
-constexpr int kStages = 3;
+constexpr int kStages = 2;                     // of a warp's ring: turns in flight
 
 // A warp's ring: per stage the keys of a turn, then its values, float4 by lane.
 template <int kVec4>
@@ -38,7 +41,7 @@ constexpr int kRing = kStages * 2 * kTurn * kVec4 * 32 * 16;
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
 template <int kVec4>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedParams p)
+__global__ void __launch_bounds__(kThreads, kVec4 == 1 ? 3 : 1) paged_simt_kernel(const __grid_constant__ PagedParams p)
 {
     using Walk = PagedWalk<FlatTiles<kRows>, kUnit>;
     __shared__ float2 stat_w[kWarps][kRows];
