@@ -28,6 +28,8 @@
 // chain of code that runs once (plan 2, first reads 1.5, sums and partial 2, joining 1.5,
 // launch 2).  It was 16 us while the walk and the copies were compiled into several places:
 // a call this short is bound by fetching instructions.
+#include <algorithm>
+
 #include "paged_plan.cuh"
 
 namespace ra {
@@ -340,10 +342,22 @@ cudaError_t launch_d(PagedParams& p)
     const cudaError_t e =
         resident_ctas(known, paged_bf16_kernel<D>, kThreads, Smem<D>::kBytes, &grid);
     if (e != cudaSuccess) return e;
+    // With so few tiles that each would fall into 24 parts or more, one block an SM: it copies
+    // nearly as fast as two and halves the joining (one token over 131072 keys of 8 heads 89 us
+    // against 93, 36000 of 4 heads of 64 dims 19.5 against 21.4; 32 tiles in 10 parts each, 38
+    // us, would take 40).
+    const long long tiles =
+        static_cast<long long>(a.H_kv) *
+        std::max<long long>(a.n_seqs, (static_cast<long long>(a.T) * p.G + kRows - 1) / kRows);
+    if (tiles * 24 <= grid) grid /= 2;
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.tile_cost = 64;
     p.key_shift = 0;
     p.snap = 2 * kUnit;
+    // 12 keys' time (0.1 us).  Measured with 6, 12, 24 and 40: one token over 120000 keys of one
+    // head 39, 35, 36, 40 us, 8000 keys of 8 heads 18.8, 18.2, 17.6, 19.0, 2000 of 8 heads 10.1,
+    // 10.1, 13.7, 14.0.
+    p.join_cost = 12;
     p.min_chunk = 2 * kUnit;
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, D);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);

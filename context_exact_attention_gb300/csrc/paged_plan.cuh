@@ -33,7 +33,7 @@ struct PagedParams {
     int G;                  // query heads per key/value head
     int grid;
     int min_chunk;          // smallest part worth a CTA, in cost
-    int join_cost;          // StepTiles: of joining one more partial of a tile
+    int join_cost;          // of joining one more partial of a tile
     int snap;               // shortest piece of a cut tile, in keys
     int tile_cost;          // a tile's fixed cost (its queries and output)
     int key_shift;          // log2 of a key's cost
@@ -116,7 +116,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b)
 // counts all the keys (sequences with few new tokens see nearly all in every tile).
 template <int kRows>
 struct FlatTiles {
-    static constexpr bool kJoinRule = false;
+    static constexpr bool kLongest = true;
     int n_tiles;
     long long cost;         // of one tile
     __device__ __forceinline__ static int rows(const PagedParams&) { return kRows; }
@@ -135,7 +135,7 @@ struct FlatTiles {
 // sequence's costs form an arithmetic series, summed in closed form and searched by halving.
 // Its last tile may have one sub-tile of rows only, whose keys cost less.
 struct StepTiles {
-    static constexpr bool kJoinRule = true;
+    static constexpr bool kLongest = false;
     int n_tiles, per, fixed, wide, last_shift;
     long long seen, last_keys;      // keys of tile j < n_tiles - 1: seen + j step; of the last
     int step;
@@ -272,12 +272,14 @@ struct PagedWalk {
     {
         const int lane = threadIdx.x & 31;
         SeqSpan mine{0, 0, 0};      // the last sequence this lane looked at
+        int longest = 0;            // keys of a sequence with new tokens
         float n_tiles = 0.f;
         auto cost_of = [&](int i) -> long long {
             mine = seq_span_of(p.a, i);
             Tiles t;
             t.init(p, mine);
-            if (Tiles::kJoinRule) n_tiles += static_cast<float>(t.n_tiles) * p.a.H_kv;
+            if (Tiles::kLongest) longest = mine.n > 0 ? max(longest, mine.kv) : longest;
+            else n_tiles += static_cast<float>(t.n_tiles) * p.a.H_kv;
             return t.prefix(t.n_tiles) * p.a.H_kv;
         };
         const int per = (p.a.n_seqs + 31) / 32;
@@ -293,11 +295,16 @@ struct PagedWalk {
         }
         const long long total = __shfl_sync(0xffffffffu, inc, 31);
         chunk = max(quotient(total + p.grid - 1, p.grid), static_cast<long long>(p.min_chunk));
-        if (Tiles::kJoinRule) {
-            // A tile of cost t in parts of x takes x for the parts, which run side by side, and
-            // join_cost t / x for joining them, one after the other: least at
-            // x = sqrt(join_cost t).  (Tiles of up to 16 rows join at a tenth of the cost, and
-            // the rule's own instructions would take as long as it saves.)
+        // A tile of cost t in parts of x takes x for the parts, which run side by side, and
+        // join_cost t / x for joining them, one after the other: least at x = sqrt(join_cost t).
+        if constexpr (Tiles::kLongest) {
+            // the longest tile's t, since the call ends with it (one token of 8 heads that share
+            // a key head, 40000 keys: 26 us, and 63 in as many parts as there are CTAs)
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            const float tile = static_cast<float>(longest) * static_cast<float>(p.join_cost << p.key_shift);
+            chunk = max(chunk, static_cast<long long>(sqrtf(tile)));
+        } else {
+            // the mean tile's
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) n_tiles += __shfl_xor_sync(0xffffffffu, n_tiles, o);
             const float tile = static_cast<float>(total) / fmaxf(n_tiles, 1.f);
