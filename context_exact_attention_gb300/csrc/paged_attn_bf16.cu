@@ -381,13 +381,15 @@ cudaError_t launch_paged_bf16(const PagedArgs& a)
 
 cudaError_t launch_paged(const PagedArgs& a)
 {
-    if (a.elem != 2) return launch_paged_simt(a);
+    if (a.elem != 2) return paged_rows_applies(a) ? launch_paged_rows(a) : launch_paged_simt(a);
     return paged_tc_applies(a) ? launch_paged_tc(a) : launch_paged_bf16(a);
 }
 
 unsigned long long paged_workspace_bytes(int D, int elem)
 {
-    if (elem != 2) return paged_workspace_of(kPagedMaxCtas, 4, D).total;
+    if (elem != 2)
+        return std::max(paged_workspace_of(kPagedMaxCtas, 4, D).total,
+                        paged_workspace_of(kPagedRowsCtas, 64, D).total);
     const unsigned long long few = paged_workspace_of(kPagedMaxCtas, kRows, D).total;
     const unsigned long long many = paged_workspace_of(kPagedTcCtas, 256, D).total;
     return few > many ? few : many;

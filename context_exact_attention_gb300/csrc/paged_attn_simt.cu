@@ -1,4 +1,5 @@
-// paged_attn_simt.cu -- paged_attn_fwd without tensor cores: fp32 caches.
+// paged_attn_simt.cu -- paged_attn_fwd without tensor cores: fp32 caches, few query rows per
+// key/value head.
 //
 // One block holds four query rows of one key/value head in registers (a lane keeps four
 // consecutive columns of each) and its four warps walk the CTA's part of the keys in turns
@@ -16,8 +17,8 @@
 // instructions of one dependent chain, some 3000 cycles; so it takes many warps, and three
 // blocks of two stages do better than two of three (same bytes in flight): 40 tokens over 405
 // keys of 8 heads of 64, G 5, 41 us against 48, 195 tokens over 4763 keys of 8 heads 240
-// against 273, the case below 26.5 against 26.3.  More rows per head (long prompts in fp32) are
-// taken four at a time and re-read the keys, which then come from L2.
+// against 273, the case below 26.5 against 26.3.  More rows per head are taken four at a
+// time and re-read the keys, which then come from L2 (many more: paged_attn_simt_rows.cu).
 // Measured: 16 single tokens over 100 to 4000 keys of 2 heads of 128 (91 MB) in 26 us, 3.5 TB/s:
 // each warp has only five turns, and the call's fixed parts (plan, first reads, joining,
 // launch: about 10 us) show.  Loading straight into registers, a turn at a time, took 33 to 37.

@@ -556,7 +556,8 @@ __device__ void finish_segment(const PagedParams& p, const Segment& seg, const f
     if (tid == 0) *flag = arrive_last(p, t);
     __syncthreads();
     if (*flag)
-        join_rows<T, 32, kVec4, 1, 8>(p, t, tid >> 5, kThreads / 32, kRows, [](int r) { return r; });
+        join_rows<T, 32, kVec4, kRows >= 64 ? 8 / kVec4 : 1, kRows >= 64 ? 2 : 8>(
+            p, t, tid >> 5, kThreads / 32, kRows, [](int r) { return r; });
     __syncthreads();
 }
 

@@ -219,10 +219,13 @@ struct PagedArgs {
 };
 // CTAs a call may launch (the workspace holds two partial results for each).
 constexpr int kPagedMaxCtas = 1024;
+constexpr int kPagedRowsCtas = 320;   // of the fp32 kernel for many rows
 constexpr int kPagedTcCtas = 160;     // of the tensor-core kernel (one per SM)
 unsigned long long paged_workspace_bytes(int D, int elem);
 cudaError_t launch_paged(const PagedArgs& a);        // chooses among:
-cudaError_t launch_paged_simt(const PagedArgs& a);   // fp32
+cudaError_t launch_paged_simt(const PagedArgs& a);   // fp32, few rows per key/value head
+bool paged_rows_applies(const PagedArgs& a);
+cudaError_t launch_paged_rows(const PagedArgs& a);   // fp32, many rows
 cudaError_t launch_paged_bf16(const PagedArgs& a);   // bf16, few rows per key/value head
 // bf16, many rows: CTAs, and tensor maps of q ({D, H, T}, boxes of 64 x G x tokens) and of
 // the pages ({D, H_kv, page_size, num_pages}, boxes of 64 x 1 x keys of one page x 1).

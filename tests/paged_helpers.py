@@ -12,8 +12,10 @@ attention: a score is a sum of D exact (bf16) or rounded (fp32) products, off by
   and the rounding of its argument u |score| (below S u): a weight is off by a relative
   e = (D + 8) u S + 2^-21.  Summing n weights adds at most (n / 16 + 64) u (no thread adds
   more than n / 16 of them in a row).  The quotient is off by twice that times the average
-  of |v| under the weights, A_v.  The tensor-core kernels also round the weights to bf16:
-  2^-8 A_v.
+  of |v| under the weights, A_v; in fp32, where a thread may add the weighted values of all n
+  keys one after the other (n - 1 roundings, each below u times a partial sum of at most the
+  weights' sum times A_v), by n u A_v more.  The tensor-core kernels also round the weights to
+  bf16: 2^-8 A_v.
 """
 import math
 
@@ -129,7 +131,7 @@ class Cache:
                 Av = w @ v[:, h // G].abs()
                 Smax = S.amax(-1) if kv else torch.zeros(n, dtype=torch.float64)
                 e = (D + 8) * U * Smax + 2.0 ** -21 + (kv / 16 + 64) * U
-                low = 2.0 ** -8 if self.dtype == torch.bfloat16 else 0.0
+                low = 2.0 ** -8 if self.dtype == torch.bfloat16 else kv * U
                 o = out[r0:r0 + n, h]
                 tol[r0:r0 + n, h] = ((2 * e + low * (1 + 2.0 ** -7))[:, None] * Av
                                      + half_step(self.dtype) * (o.abs() + (2 * e + low)[:, None] * Av)

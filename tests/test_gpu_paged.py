@@ -55,6 +55,15 @@ ATTEND = {
     "fp32 wide": ([(2, 130), (1, 3)], 5, 1, 256, 8, F32, "heads", 0),
     "fp32 narrow": ([(3, 70), (2, 1)], 4, 4, 20, 5, F32, "by_slot", 0),
     "fp32 long": ([(1, 9000), (30, 500)], 2, 1, 64, 64, F32, "slots", 0),
+    # many rows
+    "fp32 prompts": ([(170, 170), (200, 333), (1, 5), (0, 40), (131, 131)], 4, 2, 128, 16, F32, "slots", 3),
+    "fp32 chunk": ([(401, 900)], 1, 1, 100, 24, F32, "heads", 0),
+    "fp32 chunk, a long context": ([(200, 7000)], 4, 2, 64, 64, F32, "by_page", 0),
+    "fp32 prompts wide": ([(130, 200), (260, 260)], 3, 1, 256, 8, F32, "by_slot", 1),
+    "fp32 prompts 192": ([(399, 391), (90, 0)], 4, 1, 192, 16, F32, "slots", 0),
+    "fp32 prompts narrow": ([(500, 63), (400, 465)], 2, 1, 4, 1, F32, "slots", 2),
+    "fp32 group of sixty-four": ([(9, 40), (20, 20)], 64, 1, 36, 16, F32, "by_head", 0),
+    "fp32 group of nine": ([(90, 200), (64, 64)], 18, 2, 68, 3, F32, "slots", 0),
 }
 
 
@@ -143,7 +152,7 @@ def test_shared_pages_and_a_wider_table():
     assert_attends(out, lse, c.reference())
 
 
-@pytest.mark.parametrize("dtype,D,n,H", [(BF, 128, 1, 4), (BF, 64, 70, 4), (F32, 32, 3, 4)])
+@pytest.mark.parametrize("dtype,D,n,H", [(BF, 128, 1, 4), (BF, 64, 70, 4), (F32, 32, 3, 4), (F32, 32, 700, 4)])
 def test_page_indices_outside_the_cache_read_as_zeros(dtype, D, n, H, monkeypatch):
     c = Cache([(n, 200), (1, 90)], H, 2, D, 16, dtype, seed=8)
     for i, (g, j) in enumerate(((0, 0), (0, 5), (1, 2))):
@@ -178,6 +187,30 @@ def test_malformed_lengths_stay_in_bounds(dtype, page, cu, kv, monkeypatch):
         assert cea.check_status() == 0
         cea.paged_attn_fwd(c.q.to(DEV), kp, vp, c.table.to(DEV), dcu, dkv)
         assert cea.check_status() == 0
+
+
+@pytest.mark.parametrize("cu", BAD_CU, ids=str)
+@pytest.mark.parametrize("kv", BAD_KV, ids=str)
+def test_malformed_lengths_of_many_fp32_rows(cu, kv, monkeypatch):
+    c = Cache([(400, 464), (400, 64), (400, 500)], 4, 2, 36, 16, F32, seed=9, garbage=0.0)
+    kp, vp = c.device_pages(DEV)
+    cu = [min(max(20 * x, -2 ** 31), 2 ** 31 - 1) for x in cu]
+    dcu, dkv = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (cu, kv))
+    normal = cea.load_library()
+    for lib in (cea.load_debug_library(build_if_missing=True), normal):
+        monkeypatch.setattr(cea, "_lib", lib)
+        cea.paged_attn_fwd(c.q.to(DEV), kp, vp, c.table.to(DEV), dcu, dkv)
+        assert cea.check_status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_of_later_tokens_stay_out_of_fp32_rows(bad):
+    c = Cache([(400, 450)], 4, 1, 64, 16, F32, seed=11)
+    want, _ = attend(c)
+    c.v[c.table[0, 300 // 16], 300 % 16] = bad            # seen by new tokens 250 and on
+    got, _ = attend(c)
+    assert torch.equal(got[:250], want[:250])
+    assert not got[250:].isfinite().any()
 
 
 APPEND = {
@@ -392,6 +425,7 @@ def test_prefill_and_decode_against_dense_ring_attention(G):
 
 def test_debug_build_gives_the_same_bits(monkeypatch):
     cases = ["chunks and tokens", "odd group", "a long context", "fp32", "no new tokens between",
+             "fp32 prompts", "fp32 prompts wide", "fp32 group of nine",
              "more heads than a tile", "pages of 24", "twenty heads a group"]
     normal = {}
     for n in cases:
