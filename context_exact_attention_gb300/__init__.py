@@ -805,15 +805,17 @@ def _index_tensor(t, name, dim, sizes=None):
     if t.dtype is not torch.int32 or len(shape) != dim or (sizes is not None and shape != sizes):
         raise ValueError(f"{name} must be a {dim}-D int32 CUDA tensor"
                          + (f" of shape {list(sizes)}" if sizes else ""))
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    if not t.is_contiguous() and shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 def _token_stride(t, shape, name):
     """Elements between tokens of [..., H, D] rows whose heads lie side by side (a view of a
     fused projection output is one such); shape is t's."""
-    stride = t.stride()
     H, D = shape[-2], shape[-1]
+    if t.is_contiguous():
+        return H * D
+    stride = t.stride()
     if stride[-1] != 1 and D > 1 or stride[-2] != D and H > 1:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if len(shape) == 3:
