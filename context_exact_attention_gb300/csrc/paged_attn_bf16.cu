@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
     const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.q);
     const uint32_t ring = smem_addr(smem) + warp * 2 * S::kTile;
 
+    wait_for_earlier_work();
     Walk walk;
     walk.begin(p);
     Segment t{}, nt{};                          // the segment being multiplied, the next one
@@ -364,8 +365,7 @@ cudaError_t launch_d(PagedParams& p)
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
-    paged_bf16_kernel<D><<<p.grid, kThreads, Smem<D>::kBytes, a.stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(paged_bf16_kernel<D>, p.grid, kThreads, Smem<D>::kBytes, a.stream, p);
 }
 
 }  // namespace

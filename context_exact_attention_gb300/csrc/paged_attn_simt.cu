@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(kThreads, kVec4 == 1 ? 3 : 1) paged_simt_kerne
     const uint32_t ring_s = smem_addr(ring);
     constexpr int kHalf = kTurn * kVec4 * 512;     // bytes of a stage's keys
 
+    wait_for_earlier_work();
     Walk walk;
     walk.begin(p);
     Segment t{}, nt{};                          // the segment being worked on, the next one
@@ -313,10 +314,8 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
     if (a.D <= 128)
-        paged_simt_kernel<1><<<p.grid, kThreads, kWarps * kRing<1>, a.stream>>>(p);
-    else
-        paged_simt_kernel<2><<<p.grid, kThreads, kWarps * kRing<2>, a.stream>>>(p);
-    return cudaGetLastError();
+        return launch_early(paged_simt_kernel<1>, p.grid, kThreads, kWarps * kRing<1>, a.stream, p);
+    return launch_early(paged_simt_kernel<2>, p.grid, kThreads, kWarps * kRing<2>, a.stream, p);
 }
 
 }  // namespace ra

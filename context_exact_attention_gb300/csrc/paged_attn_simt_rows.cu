@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kThreads<kCols>, kCols <= 2 ? 2 : 1)
         }
     };
 
+    wait_for_earlier_work();
     Walk walk;
     walk.begin(p);
     Segment t;
@@ -248,8 +249,7 @@ cudaError_t launch_cols(PagedParams& p)
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
-    paged_rows_kernel<kCols><<<p.grid, kThreads<kCols>, kSmem<kCols>, p.a.stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(paged_rows_kernel<kCols>, p.grid, kThreads<kCols>, kSmem<kCols>, p.a.stream, p);
 }
 
 }  // namespace

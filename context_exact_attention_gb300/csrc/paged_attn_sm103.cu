@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     tc_fence_after();
+    wait_for_earlier_work();
     const uint32_t tmem = *tmem_slot;
     WaitCtx wc{abort_flag, a.status, a.timeout_ns};
 
@@ -812,8 +813,7 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
-    paged_tc_kernel<D><<<p.grid, kThreads, Layout<D>::kSmem, p.a.stream>>>(tq, tk, tv, p);
-    return cudaGetLastError();
+    return launch_early(paged_tc_kernel<D>, p.grid, kThreads, Layout<D>::kSmem, p.a.stream, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -322,6 +322,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c)
     return d;
 }
 
+// Returns once the work before this kernel in its stream has finished and its writes are
+// visible: the first thing that a kernel launched by launch_early does in every thread.
+__device__ __forceinline__ void wait_for_earlier_work()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Packed pairs of fp32 (low, high) for the f32x2 arithmetic.
 __device__ __forceinline__ uint64_t f2pack(float lo, float hi)
 {

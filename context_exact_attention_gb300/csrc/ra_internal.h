@@ -52,6 +52,27 @@ cudaError_t resident_ctas(std::atomic<int>* known, Kernel kernel, int threads, i
     return cudaSuccess;
 }
 
+// Launches a kernel that begins with wait_for_earlier_work() as a programmatic dependent: its
+// blocks are set up while the work before it in the stream drains.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, int threads, int bytes,
+                         cudaStream_t stream, const Args&... args)
+{
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(grid);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = bytes;
+    config.stream = stream;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, args...);
+    if (e != cudaSuccess) cudaGetLastError();       // reported here, not to the next caller who asks
+    return e;
+}
+
 // Everything one attention launch needs; validated by the ABI layer.
 struct AttnArgs {
     const void* q;

@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kMaxBlock) rope_kernel(const __grid_constant__
         if (two) *reinterpret_cast<Vec*>(out + apart) = r.x1;
     };
 
+    wait_for_earlier_work();
     if (!works || h >= heads) tok = n_tok;
     if (tok < n_tok) enter();
     // the first rows are on their way while the positions and angles are worked out
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(256) rope_shift_kernel(const __grid_constant__
     const int n_tok = static_cast<int>(min(static_cast<long long>(a.tokens), a.rows - t0));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
 
+    wait_for_earlier_work();
     for (int i = warp; i < n_tok; i += n_warps) {
         const TokenPos p = token_pos<kPaged>(a, t0 + i);
         if (lane == 0) tok_s[i] = p;
@@ -572,9 +574,8 @@ cudaError_t launch_shift(RopeArgs& a, int sms)
     const long long blocks = (a.rows + a.tokens - 1) / a.tokens;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (a.paged) rope_shift_kernel<T, true><<<grid, 32 * warps, 0, a.stream>>>(a);
-    else rope_shift_kernel<T, false><<<grid, 32 * warps, 0, a.stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(a.paged ? rope_shift_kernel<T, true> : rope_shift_kernel<T, false>, grid,
+                        32 * warps, 0, a.stream, a);
 }
 
 template <typename T, bool kHalfStyle, int N>
@@ -614,9 +615,8 @@ cudaError_t launch(RopeArgs& a, int sms)
     const long long blocks = (a.rows + a.tokens - 1) / a.tokens;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (a.paged) rope_kernel<T, kHalfStyle, N, true><<<grid, threads, 0, a.stream>>>(a);
-    else rope_kernel<T, kHalfStyle, N, false><<<grid, threads, 0, a.stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(a.paged ? rope_kernel<T, kHalfStyle, N, true> : rope_kernel<T, kHalfStyle, N, false>,
+                        grid, threads, 0, a.stream, a);
 }
 
 template <typename T>
