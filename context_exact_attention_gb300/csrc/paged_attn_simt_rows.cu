@@ -263,10 +263,13 @@ bool paged_rows_applies(const PagedArgs& a)
     // 209 against 132; 32 of 64 keys, 64 rows 22 against 20, 96 rows 28 against 33, 400 rows 108
     // against 73; 8 heads, one sequence of 4763 keys, 195 rows 242 against 170; 64 dims, 4000
     // rows over 1000 keys 187 against 56; 256 dims, 1200 rows over 3000 keys 557 against 248.
+    // Where the table holds a few steps of keys only, a tile cannot be split and many are needed
+    // to fill the GPU (three prompts of 180 tokens, 6 heads over 3, 36 tiles: 27 us against 41).
     const int G = a.H / a.H_kv;
     const long long rows = static_cast<long long>(a.T) * G;
+    const bool few_keys = static_cast<long long>(a.max_pages) * a.page_size <= 4 * kKeys;
     return a.elem == 4 && G <= kRows && rows >= 64ll * a.n_seqs &&
-           (rows * a.H_kv >= 24ll * kRows || rows >= 384ll * a.n_seqs);
+           (rows * a.H_kv >= (few_keys ? 128ll : 24ll) * kRows || (!few_keys && rows >= 384ll * a.n_seqs));
 }
 
 cudaError_t launch_paged_rows(const PagedArgs& a)

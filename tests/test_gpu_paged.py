@@ -64,6 +64,9 @@ ATTEND = {
     "fp32 prompts narrow": ([(500, 63), (400, 465)], 2, 1, 4, 1, F32, "slots", 2),
     "fp32 group of sixty-four": ([(9, 40), (20, 20)], 64, 1, 36, 16, F32, "by_head", 0),
     "fp32 group of nine": ([(90, 200), (64, 64)], 18, 2, 68, 3, F32, "slots", 0),
+    "fp32 group of sixty-four, more keys": ([(9, 400), (20, 20)], 64, 1, 36, 16, F32, "by_head", 0),
+    "fp32 group of nine, more keys": ([(90, 500), (64, 64)], 18, 2, 68, 3, F32, "slots", 1),
+    "fp32 prompts of few keys": ([(100, 100), (64, 70), (90, 3)], 40, 8, 20, 16, F32, "slots", 0),
 }
 
 
@@ -152,7 +155,8 @@ def test_shared_pages_and_a_wider_table():
     assert_attends(out, lse, c.reference())
 
 
-@pytest.mark.parametrize("dtype,D,n,H", [(BF, 128, 1, 4), (BF, 64, 70, 4), (F32, 32, 3, 4), (F32, 32, 700, 4)])
+@pytest.mark.parametrize("dtype,D,n,H", [(BF, 128, 1, 4), (BF, 64, 70, 4), (F32, 32, 3, 4), (F32, 32, 700, 4),
+                                           (F32, 32, 700, 32)])
 def test_page_indices_outside_the_cache_read_as_zeros(dtype, D, n, H, monkeypatch):
     c = Cache([(n, 200), (1, 90)], H, 2, D, 16, dtype, seed=8)
     for i, (g, j) in enumerate(((0, 0), (0, 5), (1, 2))):
