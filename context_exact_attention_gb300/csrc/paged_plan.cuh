@@ -294,22 +294,28 @@ struct PagedWalk {
             if (lane >= o) inc += y;
         }
         const long long total = __shfl_sync(0xffffffffu, inc, 31);
-        chunk = max(quotient(total + p.grid - 1, p.grid), static_cast<long long>(p.min_chunk));
         // A tile of cost t in parts of x takes x for the parts, which run side by side, and
         // join_cost t / x for joining them, one after the other: least at x = sqrt(join_cost t).
+        // A part need not be longer than a tile, though (26 sequences of 3 tokens and keys
+        // 9.2 us, 13 with parts of a fixed least length, which hold a tile and a half).
+        long long least;
         if constexpr (Tiles::kLongest) {
             // the longest tile's t, since the call ends with it (one token of 8 heads that share
             // a key head, 40000 keys: 26 us, and 63 in as many parts as there are CTAs)
             longest = __reduce_max_sync(0xffffffffu, longest);
             const float tile = static_cast<float>(longest) * static_cast<float>(p.join_cost << p.key_shift);
-            chunk = max(chunk, static_cast<long long>(sqrtf(tile)));
+            least = max(p.min_chunk, static_cast<int>(sqrtf(tile)));
+            least = min(least, p.tile_cost + (static_cast<long long>(longest) << p.key_shift));
         } else {
             // the mean tile's
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) n_tiles += __shfl_xor_sync(0xffffffffu, n_tiles, o);
             const float tile = static_cast<float>(total) / fmaxf(n_tiles, 1.f);
-            chunk = max(chunk, static_cast<long long>(sqrtf(tile * static_cast<float>(p.join_cost))));
+            const float part = fmaxf(sqrtf(tile * static_cast<float>(p.join_cost)),
+                                     static_cast<float>(p.min_chunk));
+            least = static_cast<long long>(fminf(part, tile + 1.f));
         }
+        chunk = max(quotient(total + p.grid - 1, p.grid), least);
         x = blockIdx.x * chunk;
         end = min(total, x + chunk);
         g = 0;
