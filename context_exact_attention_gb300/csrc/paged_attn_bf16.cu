@@ -359,6 +359,7 @@ cudaError_t launch_d(PagedParams& p)
     // head 39, 35, 36, 40 us, 8000 keys of 8 heads 18.8, 18.2, 17.6, 19.0, 2000 of 8 heads 10.1,
     // 10.1, 13.7, 14.0.
     p.join_cost = 12;
+    p.whole = 0;                    // (480: 100 to 450 keys 0.7 to 0.9 times as fast)
     p.min_chunk = 2 * kUnit;
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, D);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);

@@ -307,6 +307,7 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     // heads and sequences 33.7, 29.5, 34.5 us, 30000 keys of one head, G 4, 30.6, 26.7, 31.1, 3000
     // of one head 11.7, 12.9, 13.9.
     p.join_cost = 6;
+    p.whole = 140;                  // (4 single tokens over 50 to 100 keys: 9.0 us, 11.5 cut; 300: 0.6 to 1.0)
     p.min_chunk = 4 * kUnit;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, a.D);

@@ -281,6 +281,7 @@ cudaError_t launch_paged_rows(const PagedArgs& a)
     p.tile_cost = 128;
     p.snap = 2 * kKeys;
     p.min_chunk = 2 * kKeys;
+    p.whole = 0;
     p.join_cost = 8;                // (4, 16, 64: 83, 103, 144 us for 64 rows over 8000 keys of 2 heads)
     if (a.D <= 64) return launch_cols<1>(p);
     if (a.D <= 128) return launch_cols<2>(p);

@@ -807,7 +807,13 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     // with the rule that this feeds and without: 297 tokens over 11606 keys of 2 heads 52 us
     // against 59 (69 with parts of 2 blocks at least instead of 3), 8 tokens over 4000 keys of 8
     // heads 20 against 22.
-    p.join_cost = static_cast<long long>(p.a.T) * p.G > static_cast<long long>(kSub) * p.a.n_seqs ? 600 : 200;
+    const bool two = static_cast<long long>(p.a.T) * p.G > static_cast<long long>(kSub) * p.a.n_seqs;
+    p.join_cost = two ? 600 : 200;
+    // Tiles of two sub-tiles of up to eight blocks are faster whole: half the time of one that
+    // is longer pays for the partials and their joining (26 prompts of 30 to 60 tokens over 300
+    // to 600 keys, 4 key heads, 22 us and 31 cut; 5 prompts of 757, 21 and 28; at a third more
+    // the mixed batch above loses 3 %).
+    p.whole = two ? 2800 : 0;
     const PagedWorkspace w = paged_workspace_of(p.grid, 2 * kSub, D);
     uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
     p.counters = reinterpret_cast<unsigned int*>(ws);

@@ -35,6 +35,7 @@ struct PagedParams {
     int min_chunk;          // smallest part worth a CTA, in cost
     int join_cost;          // of joining one more partial of a tile
     int snap;               // shortest piece of a cut tile, in keys
+    int whole;              // tiles of up to this cost are never cut
     int tile_cost;          // a tile's fixed cost (its queries and output)
     int key_shift;          // log2 of a key's cost
     int key_shift_single;   // StepTiles: the same in a tile with one sub-tile of rows
@@ -240,8 +241,10 @@ struct PagedWalk {
             const int last = p.token_of(t.row0 + t.rows - 1);
             t.keys = p.a.causal ? min(max(s.kv - s.n + last + 1, 0), s.kv) : s.kv;
             const int shift = tiles.shift(p, j);
-            const int snap = static_cast<int>(
-                min(static_cast<long long>(p.snap), chunk >> (shift + 2)));
+            // (a tile that is never cut belongs to the CTA that holds its middle)
+            const int snap = b - a <= p.whole ? t.keys / 2 + 1
+                                              : static_cast<int>(min(static_cast<long long>(p.snap),
+                                                                     chunk >> (shift + 2)));
             // The CTAs that touch the tile, without those whose piece has no keys (only the
             // first and the last can have none); the first keeps a tile without keys.
             const int c = blockIdx.x;
@@ -304,8 +307,9 @@ struct PagedWalk {
             // a key head, 40000 keys: 26 us, and 63 in as many parts as there are CTAs)
             longest = __reduce_max_sync(0xffffffffu, longest);
             const float tile = static_cast<float>(longest) * static_cast<float>(p.join_cost << p.key_shift);
-            least = max(p.min_chunk, static_cast<int>(sqrtf(tile)));
-            least = min(least, p.tile_cost + (static_cast<long long>(longest) << p.key_shift));
+            least = p.tile_cost + (static_cast<long long>(longest) << p.key_shift);
+            if (least > p.whole)
+                least = min(least, static_cast<long long>(max(p.min_chunk, static_cast<int>(sqrtf(tile)))));
         } else {
             // the mean tile's
 #pragma unroll
@@ -313,7 +317,8 @@ struct PagedWalk {
             const float tile = static_cast<float>(total) / fmaxf(n_tiles, 1.f);
             const float part = fmaxf(sqrtf(tile * static_cast<float>(p.join_cost)),
                                      static_cast<float>(p.min_chunk));
-            least = static_cast<long long>(fminf(part, tile + 1.f));
+            least = static_cast<long long>(
+                tile <= static_cast<float>(p.whole) ? tile + 1.f : fminf(part, tile + 1.f));
         }
         chunk = max(quotient(total + p.grid - 1, p.grid), least);
         x = blockIdx.x * chunk;
