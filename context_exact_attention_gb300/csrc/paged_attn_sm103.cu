@@ -811,8 +811,8 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     p.join_cost = two ? 600 : 200;
     // Tiles of two sub-tiles of up to eight blocks are faster whole: half the time of one that
     // is longer pays for the partials and their joining (26 prompts of 30 to 60 tokens over 300
-    // to 600 keys, 4 key heads, 22 us and 31 cut; 5 prompts of 757, 21 and 28; at a third more
-    // the mixed batch above loses 3 %).
+    // to 600 keys, 4 key heads, 17 us and 31 cut; 5 prompts of 757, 19 and 28; at a third more
+    // a mixed batch loses 3 %).
     p.whole = two ? 2800 : 0;
     const PagedWorkspace w = paged_workspace_of(p.grid, 2 * kSub, D);
     uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);

@@ -241,13 +241,22 @@ struct PagedWalk {
             const int last = p.token_of(t.row0 + t.rows - 1);
             t.keys = p.a.causal ? min(max(s.kv - s.n + last + 1, 0), s.kv) : s.kv;
             const int shift = tiles.shift(p, j);
-            // (a tile that is never cut belongs to the CTA that holds its middle)
-            const int snap = b - a <= p.whole ? t.keys / 2 + 1
-                                              : static_cast<int>(min(static_cast<long long>(p.snap),
-                                                                     chunk >> (shift + 2)));
+            const int c = blockIdx.x;
+            if (!Tiles::kLongest && b - a <= p.whole) {
+                // never cut: the tile of the CTA whose part holds its middle
+                t.c_first = t.c_last = static_cast<int>(quotient(a + ((b - a) >> 1), chunk));
+                t.k0 = 0;
+                t.k1 = t.keys;
+                x = min(end, b);
+                if (c == t.c_first) return true;
+                continue;
+            }
+            const int snap = Tiles::kLongest && b - a <= p.whole
+                                 ? t.keys / 2 + 1               // not cut
+                                 : static_cast<int>(min(static_cast<long long>(p.snap),
+                                                        chunk >> (shift + 2)));
             // The CTAs that touch the tile, without those whose piece has no keys (only the
             // first and the last can have none); the first keeps a tile without keys.
-            const int c = blockIdx.x;
             t.c_first = a >= c * chunk ? c : static_cast<int>(quotient(a, chunk));
             t.c_last = b <= (c + 1) * chunk ? c : static_cast<int>(quotient(b - 1, chunk));
             auto before = [&](int cta) -> int {             // keys before that CTA's part
@@ -311,14 +320,15 @@ struct PagedWalk {
             if (least > p.whole)
                 least = min(least, static_cast<long long>(max(p.min_chunk, static_cast<int>(sqrtf(tile)))));
         } else {
-            // the mean tile's
+            // the mean tile's (of tiles that stay whole three quarters, so that two a little
+            // shorter than the mean do not fall to one CTA while another has none)
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) n_tiles += __shfl_xor_sync(0xffffffffu, n_tiles, o);
             const float tile = static_cast<float>(total) / fmaxf(n_tiles, 1.f);
             const float part = fmaxf(sqrtf(tile * static_cast<float>(p.join_cost)),
                                      static_cast<float>(p.min_chunk));
             least = static_cast<long long>(
-                tile <= static_cast<float>(p.whole) ? tile + 1.f : fminf(part, tile + 1.f));
+                tile <= static_cast<float>(p.whole) ? 0.75f * tile : fminf(part, tile + 1.f));
         }
         chunk = max(quotient(total + p.grid - 1, p.grid), least);
         x = blockIdx.x * chunk;
