@@ -873,11 +873,13 @@ def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out
         if not positions.is_contiguous():
             raise ValueError("positions must be contiguous")
     H = H_kv = qs = ks = qos = kos = 0
+    # the kernel writes every row but packed ones that no sequence holds
+    new = torch.zeros if packed else torch.empty
     if q is not None:
         H = shape[-2]
         qs = _token_stride(q, shape, "q")
         if q_out is None:
-            q_out = torch.empty(shape, dtype=dtype, device=device)
+            q_out = new(shape, dtype=dtype, device=device)
         elif q_out.shape != shape or q_out.dtype is not dtype:
             raise ValueError("outputs must be shaped and typed like their inputs")
         qos = _token_stride(q_out, shape, "q_out")
@@ -891,7 +893,7 @@ def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out
             raise ValueError("q and k must agree in every dimension but the heads, and in dtype")
         ks = _token_stride(k, k_shape, "k")
         if k_out is None:
-            k_out = torch.empty(k_shape, dtype=dtype, device=device)
+            k_out = new(k_shape, dtype=dtype, device=device)
         elif k_out.shape != k_shape or k_out.dtype is not dtype:
             raise ValueError("outputs must be shaped and typed like their inputs")
         kos = _token_stride(k_out, k_shape, "k_out")
@@ -910,7 +912,9 @@ def rope_fwd(q, k, rope: RopeTable, positions=None, offset: int = 0, layout: str
     their positions, in one launch: a row's position in its shard layout ("contiguous",
     "zigzag" over P shards, or "packed" with [L, H, D] tensors and cu_seqlens), or
     positions, an int32 [B, L]; offset is added.  Tokens may be strided views of a fused
-    projection output; q_out=q and k_out=k rotate in place.  Returns (q_out, k_out)."""
+    projection output; q_out=q and k_out=k rotate in place.  Packed rows that no sequence
+    holds are left as they are (zero in outputs allocated here, which costs a call of that
+    layout a fill that it saves by passing its outputs).  Returns (q_out, k_out)."""
     return _rope_call("rope_fwd", q, k, rope, positions, offset, layout, P, cu_seqlens, q_out,
                       k_out, stream)
 

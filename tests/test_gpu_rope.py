@@ -171,6 +171,29 @@ def test_rows_of_no_sequence_are_left():
     assert torch.equal(out[3], x[3]) and torch.equal(out[8], x[8])    # position 0 of each
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("back", [False, True], ids=["fwd", "bwd"])
+def test_rows_of_no_sequence_are_zero_in_outputs_allocated_here(back, dtype):
+    """The same rows where the call makes its outputs, in memory that held NaN before: a
+    gradient with anything else there would reach the projection's weights."""
+    g = torch.Generator().manual_seed(10)
+    q, k = (torch.randn(2000, h, 64, generator=g).to(dtype).to(DEV) for h in (4, 2))
+    cu = torch.tensor([3, 800, 800, 1500], dtype=torch.int32, device=DEV)
+    table = cea.rope_table(64, device=DEV)
+    f = cea.rope_bwd if back else cea.rope_fwd
+    want = [torch.zeros_like(x) for x in (q, k)]
+    f(q, k, table, layout="packed", cu_seqlens=cu, q_out=want[0], k_out=want[1])
+    for _ in range(3):
+        used = [torch.full((2000, h, 64), float("nan"), dtype=dtype, device=DEV)
+                for h in (4, 2) * 8]
+        del used
+        got = f(q, k, table, layout="packed", cu_seqlens=cu)
+        assert cea.check_status() == 0
+        for x, y in zip(got, want):
+            assert (x[:3] == 0).all() and (x[1500:] == 0).all()
+            assert torch.equal(x, y)
+
+
 def test_many_boundaries():
     """The 32-wide search over more sequences than one or two of its steps hold."""
     lens = [(i * 7) % 5 for i in range(2500)]
