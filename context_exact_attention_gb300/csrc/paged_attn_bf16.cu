@@ -78,6 +78,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The bits of the next fp32 number below a weight x >= +0, and 0 for 0.  (For a NaN a NaN,
+// infinity or 0: the rest x - that is NaN.)
+__device__ __forceinline__ uint32_t below(float x)
+{
+    return static_cast<uint32_t>(__viaddmax_s32(__float_as_int(x), -1, 0));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_constant__ PagedParams p)
 {
@@ -257,20 +264,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
                 l0 += s[i][0] + s[i][1];
                 l1 += s[i][2] + s[i][3];
             }
-            // The matrix product takes its weights in bf16.  Each goes in as two of them, itself
-            // rounded and the rest rounded, which keeps it to 2^-17: the products are not what
-            // bounds this kernel (17 % of the tensor pipe before), and without the second the
-            // weights' rounding would cost as much precision as the output's own.
+            // The matrix product takes its weights in bf16.  Each goes in as two of them, which
+            // keeps it to 2^-16: the products are not what bounds this kernel (17 % of the tensor
+            // pipe before), and without the second the weights' rounding would cost as much
+            // precision as the output's own.  Both parts of a weight above 0 are above 0 (the
+            // first is the weight less its last bit, cut off, the second the rest, rounded to
+            // nearest), so that an infinite value gives that infinity: with a part of 0 or of
+            // the other sign the two products would add up to NaN.
             uint32_t pf[4], pr[4];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float x0 = s[i][2 * h], x1 = s[i][2 * h + 1];
-                    const uint32_t hi = pack_bf16x2(x0, x1);
-                    pf[2 * i + h] = hi;
-                    pr[2 * i + h] = pack_bf16x2(x0 - __uint_as_float(hi << 16),
-                                                x1 - __uint_as_float(hi & 0xffff0000u));
+                    const uint32_t b0 = below(x0), b1 = below(x1);
+                    pf[2 * i + h] = __byte_perm(b0, b1, 0x7632);
+                    pr[2 * i + h] = pack_bf16x2(x0 - __uint_as_float(b0 & 0xffff0000u),
+                                                x1 - __uint_as_float(b1 & 0xffff0000u));
                 }
             {
                 const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;

@@ -680,9 +680,10 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  * keys are shared out evenly over the GPU whatever the lengths are.  (out, lse) is a partial
  * that attn_merge_partials can join with another over other keys.  A row that sees no key
  * gets 0 and -inf.  Slots behind a sequence's last key are never used, whatever they hold.
- * A key that a row does not see never reaches it.  A value that is not finite, of a new token
- * of a call with several new tokens per sequence, may in bf16 also reach earlier new rows of
- * its sequence (0 times infinity in the matrix product, as in ring_attn_fwd).
+ * A key that a row does not see never reaches it.  An infinite value gives the rows that see it
+ * (with a weight that fp32 holds) the same infinity.  A value that is not finite, of a new token
+ * of a call with several new tokens per sequence, may in bf16 also reach earlier new rows of its
+ * sequence (0 times infinity in the matrix product, as in ring_attn_fwd).
  *
  * q: [T, H, D], tokens q_stride elements apart (0: contiguous); out: [T, H, D] contiguous;
  * lse: fp32 [T, H] or NULL.  D 64 or 128 (RA_BF16), a multiple of 4 up to 256 (RA_F32).
@@ -691,7 +692,7 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  * share a workspace must not overlap on the GPU (two captured graphs that share one must be
  * replayed in order).  After a call that timed out (ra_check_status) zero it again.
  * Scores and softmax in fp32; for the value product, whose sums are fp32, bf16 calls round a
- * weight to two bf16 parts (2^-17) if sequences bring few rows and to one (2^-8 at most) if
+ * weight to two bf16 parts (2^-16) if sequences bring few rows and to one (2^-8 at most) if
  * they bring many; out is rounded once.  Repeated calls on the same inputs give
  * the same bits; the split over the GPU, and with it the last bits, depends on all lengths of
  * the call.  Limits: T * H <= 2^31 - 256.  Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED (dtype,
