@@ -14,8 +14,9 @@ attention: a score is a sum of D exact (bf16) or rounded (fp32) products, off by
   more than n / 16 of them in a row).  The quotient is off by twice that times the average
   of |v| under the weights, A_v; in fp32, where a thread may add the weighted values of all n
   keys one after the other (n - 1 roundings, each below u times a partial sum of at most the
-  weights' sum times A_v), by n u A_v more.  The tensor-core kernels also round the weights to
-  bf16: 2^-8 A_v.
+  weights' sum times A_v), by n u A_v more.  The kernel for bf16 calls with many rows also
+  rounds the weights to bf16, 2^-8 A_v, which is allowed in every bf16 call here; that few rows
+  keep them to 2^-16 is shown by values whose sum nearly cancels (test_gpu_paged_values).
 """
 import math
 

@@ -1,11 +1,12 @@
-"""paged_attn_fwd with infinite values that the rows see (bounds: paged_helpers)."""
+"""paged_attn_fwd with values that are not finite, and with values whose weighted sum nearly
+cancels, which shows what the weights were rounded to (bounds: paged_helpers)."""
 import math
 
 import pytest
 import torch
 
 import context_exact_attention_gb300 as cea
-from paged_helpers import Cache, assert_attends
+from paged_helpers import Cache, U, assert_attends, half_step
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -54,3 +55,62 @@ def test_infinite_values_that_every_row_sees(name):
         assert (out[..., 5] == -math.inf).all(), part
         rest = [x for x in range(D) if x not in (3, 5)]
         assert_attends(out[..., rest], lse, (ref[0][..., rest], ref[1], ref[2][..., rest], ref[3]), name)
+
+
+# (new tokens, keys) of every sequence, H, H_kv, D, page: calls of the kernel for few rows
+TWO_PARTS = {
+    "one token": ([(1, 2)], 32, 4, 128, 16),
+    "single tokens, D 64": ([(1, 70), (1, 500)] * 4, 16, 2, 64, 16),
+    "a long context": ([(1, 20000)], 16, 1, 128, 64),
+    "proposed tokens": ([(4, 300), (2, 30)] * 4, 16, 4, 64, 8),
+    "a chunk on odd pages": ([(70, 200)], 4, 2, 128, 3),
+}
+
+
+@pytest.mark.parametrize("name", TWO_PARTS)
+def test_weights_of_few_rows_go_in_as_two_parts(name):
+    """Half of the keys score 0 and have the values c, 1/2 to 1 over the columns; the others
+    score below 0, all the same in a row, and have the values -1.  Where c is near the weight w
+    of those, the output nearly cancels, and neither its own rounding nor the average hides how
+    w was rounded.  The bound: w is off by 2^-16 (two bf16 parts: the first cut off, the rest,
+    up to 2^-7 of a power of two, rounded to half a step, 2^-16 of that) and by e = (D + 8) u
+    |score| + 2^-21 (see paged_helpers), which the numerator feels as that times A = (sum of w
+    |v|) / sum of w.  The denominator's error is one of the quotient: e + (n / 16 + 64) u +
+    2^-20.  A matrix product of 16 keys is off by 17 2^-23 of the larger of its sum so far and
+    its terms; keys alternate, so sums grow as the result does: n / 32 products, 17 n / 32 2^-23
+    of |out| and (their terms, which are 1) 2^-21 A.  One part would be off by 2^-9 at weights
+    of 1/2 to 1."""
+    seqs, H, H_kv, D, page = TWO_PARTS[name]
+    c = Cache(seqs, H, H_kv, D, page, BF, seed=len(name), garbage=0.0)
+    columns = (0.5 + torch.arange(D) / (2 * D)).to(BF)
+    c.q.zero_()
+    # scores of 0 down to -0.7: weights of 1 down to 1/2
+    c.q[..., 0] = torch.rand(c.T, H, generator=torch.Generator().manual_seed(1)).mul(0.7).to(BF)
+    low = torch.tensor(-math.sqrt(D)).to(BF)
+    for i, (n, kv) in enumerate(seqs):
+        for j in range(kv):
+            at = int(c.table[i, j // page]), j % page
+            c.k[at], c.v[at] = 0, columns
+            if j % 2:
+                c.k[at][:, 0], c.v[at] = low, -1
+    out, _ = attend(c, causal=False)
+    got = out.double().cpu()
+
+    worst, one_part = 0.0, 0.0
+    for i, (n, kv) in enumerate(seqs):
+        rows = slice(int(c.cu[i]), int(c.cu[i]) + n)
+        score = c.q[rows, :, 0].double() * float(low) / math.sqrt(D)
+        w = torch.exp(score)[..., None]
+        a, b = (kv + 1) // 2, kv // 2              # keys that score 0, and below
+        total = a + b * w
+        ref, A = (a * columns.double() - b * w) / total, (a * columns.double() + b * w) / total
+        e = (D + 8) * U * score.abs()[..., None] + 2.0 ** -21
+        tol = ((2.0 ** -16 + e + 2.0 ** -21) * A
+               + (e + (kv / 16 + 64) * U + 2.0 ** -20 + 17 * kv / 32 * 2.0 ** -23) * ref.abs())
+        tol = tol + half_step(BF) * (ref.abs() + tol)
+        worst = max(worst, float(((got[rows] - ref).abs() / tol).max()))
+        # the same with weights of one part: the bound has to tell them apart
+        planted = (a * columns.double() - b * w.to(BF).double()) / total
+        one_part = max(one_part, float(((planted - ref).abs() / tol).max()))
+    assert one_part > 4, one_part
+    assert worst <= 1, f"{worst:.2f} bounds off"
