@@ -255,12 +255,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
                 }
             }
             const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
+            // (the product rounded, as the maximum's was, so that the maximum's own exponent is 0: a
+            // fused multiply-add leaves it the rounding, which for huge scores overflows)
+            auto weight = [&](float x, float n) { return ex2(__fadd_rn(__fmul_rn(x, p.scale_log2), n)); };
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                s[i][0] = ex2(fmaf(s[i][0], p.scale_log2, n0));
-                s[i][1] = ex2(fmaf(s[i][1], p.scale_log2, n0));
-                s[i][2] = ex2(fmaf(s[i][2], p.scale_log2, n1));
-                s[i][3] = ex2(fmaf(s[i][3], p.scale_log2, n1));
+                s[i][0] = weight(s[i][0], n0);
+                s[i][1] = weight(s[i][1], n0);
+                s[i][2] = weight(s[i][2], n1);
+                s[i][3] = weight(s[i][3], n1);
                 l0 += s[i][0] + s[i][1];
                 l1 += s[i][2] + s[i][3];
             }

@@ -49,6 +49,12 @@ constexpr int kKeys = 128;        // keys per block
 constexpr int kThreads = 384;
 constexpr int kReaders = 2 + 8;   // warps that read a published segment
 constexpr float kRescaleThreshold = 8.0f;
+// A scaled maximum is rounded by up to 2^-24 of it, and that is what the fused multiply-add
+// leaves of its exponent, which for huge scores would overflow.  From 2^29 on (rounded by 32)
+// two scores that differ at all differ by 2^-23 2^29, and a weight is 1 or nothing whatever the
+// scale is: they are taken times a power of two, which rounds nothing.
+constexpr float kFar = 536870912.f;
+constexpr float kFarScale = 0.25f;
 
 template <int D>
 struct Layout {
@@ -565,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n_blocks = single ? (s.n_blocks + 1 - tq) / 2 : s.n_blocks;
 
             float m = -INFINITY, l = 0.f;
+            float top = -INFINITY;                             // the score that m is the scaled one of
             for (int n = 0; n < n_blocks; ++n) {
                 ok = mbar_wait(bar(kBarSFull + tq), sn & 1, wc);
                 ok = __all_sync(0xffffffffu, ok);
@@ -591,15 +598,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mx2 = fmax3(mx2, sv[c + 4], sv[c + 5]);
                     mx3 = fmax3(mx3, sv[c + 6], sv[c + 7]);
                 }
-                const float m_blk = fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2;
-                const float m_new = fmaxf(m, m_blk);
+                const float top_blk = fmax3(mx0, mx1, fmaxf(mx2, mx3));
+                const float m_new = fmaxf(m, top_blk * sl2);
                 const bool raise = m_new > m + kRescaleThreshold;
                 const float m_ref = raise ? m_new : m;
+                top = raise ? top_blk : top;
                 const float alpha = raise ? ex2(m - m_ref) : 1.f;
-                const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+                const bool far = !(fabsf(m_ref) < kFar);       // (minus infinity, too)
+                const float far_neg = top == -INFINITY ? 0.f : -top * kFarScale;
+                const float scale = far ? kFarScale : sl2, neg_m = far ? far_neg : -m_ref;
                 // weights 2^(s - m_ref), rounded to bf16 (the product's operand type) over S
                 // in two halves; the denominator is summed in fp32 before the rounding
-                const uint64_t scale2 = f2pack(sl2, sl2), negm2 = f2pack(neg_m, neg_m);
+                const uint64_t scale2 = f2pack(scale, scale), negm2 = f2pack(neg_m, neg_m);
                 uint64_t sum_a = 0, sum_b = 0;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {

@@ -1,5 +1,6 @@
-"""paged_attn_fwd with values that are not finite, and with values whose weighted sum nearly
-cancels, which shows what the weights were rounded to (bounds: paged_helpers)."""
+"""paged_attn_fwd with values that are not finite, with values whose weighted sum nearly
+cancels, which shows what the weights were rounded to, and with huge scores (bounds:
+paged_helpers)."""
 import math
 
 import pytest
@@ -114,3 +115,45 @@ def test_weights_of_few_rows_go_in_as_two_parts(name):
         one_part = max(one_part, float(((planted - ref).abs() / tol).max()))
     assert one_part > 4, one_part
     assert worst <= 1, f"{worst:.2f} bounds off"
+
+
+# sequences (new tokens, keys), H, H_kv, D, page, dtype
+HUGE = {
+    "single tokens": ([(1, 5), (1, 64), (1, 70), (1, 1000)], 8, 2, 128, 16, BF),
+    "single tokens, D 64": ([(1, 9), (1, 129), (1, 500)], 4, 4, 64, 8, BF),
+    "a long context": ([(1, 20000)], 4, 1, 128, 64, BF),
+    "chunks": ([(300, 1000), (40, 44)], 4, 2, 128, 64, BF),
+    "chunks, D 64": ([(140, 900), (33, 53)], 4, 1, 64, 16, BF),
+    "a chunk, a long context": ([(40, 12000)], 4, 2, 128, 128, BF),
+    "fp32": ([(1, 90), (7, 40), (1, 3000)], 6, 2, 128, 16, F32),
+    "fp32 prompts": ([(170, 333), (200, 400)], 4, 2, 64, 16, F32),
+}
+
+
+@pytest.mark.parametrize("top", [26, 31, 32, 33, 38, 60, 120])
+@pytest.mark.parametrize("name", HUGE)
+def test_huge_scores_pick_their_keys(name, top):
+    """Scores up to 2^top / sqrt(D) of either sign, so far apart that a row's result is the value
+    of its largest key, which every row sees: that key's weight is 1, however the maximum was
+    rounded.  (Products of one column, exact in fp32; the value's rounding as a weight of one
+    bf16 part and to the output, half a step each; lse a few roundings of fp32.)"""
+    seqs, H, H_kv, D, page, dtype = HUGE[name]
+    c = Cache(seqs, H, H_kv, D, page, dtype, seed=len(name))
+    g = torch.Generator().manual_seed(2)
+    a, b = 2.0 ** (top // 2), 2.0 ** (top - top // 2)
+    c.q.zero_()
+    c.q[..., 0] = (torch.randint(65, 128, c.q.shape[:2], generator=g) * (a / 128)).to(dtype)
+    c.q[:, ::2] *= -1
+    for i, (n, kv) in enumerate(seqs):
+        for j in range(kv):
+            at = int(c.table[i, j // page]), j % page
+            # the first for the positive queries, the second for the negative ones
+            x = {int(0.4 * (kv - n)): 1.0, int(0.8 * (kv - n)): 0.25}.get(j, 0.5)
+            c.k[at] = 0
+            c.k[at][:, 0] = x * b
+    r_out, r_lse, _, _ = c.reference()
+    out, lse = attend(c)
+    err = (out.double().cpu() - r_out).abs() / r_out.abs()
+    assert err.max() <= 2.02 * half_step(dtype), f"{err.max()} of the value"
+    err = (lse.double().cpu() / r_lse - 1).abs()
+    assert err.max() <= 4 * U, err.max()
