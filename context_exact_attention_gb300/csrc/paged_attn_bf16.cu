@@ -22,11 +22,11 @@
 // are rarely rescaled.
 //
 // Measured: 64 sequences of 1000 to 16384 keys, 32 heads over 8, head dim 128 (2.26 GB) in
-// 343 to 350 us, 6.5 TB/s (97 % of the measured copy rate; the tensor pipe is 25 % busy); one
-// token over 131072 keys of 8 heads (0.54 GB) in 93 us, of which the plan, the first reads
-// and the joining of 38 partials per head take about 8; one token over 1000 keys in 9 us, a
-// chain of code that runs once (plan 2, first reads 1.5, sums and partial 2, joining 1.5,
-// launch 2).  It was 16 us while the walk and the copies were compiled into several places:
+// 344 to 357 us, 6.3 to 6.6 TB/s (95 to 98 % of the measured copy rate; the tensor pipe is 28 %
+// busy); one token over 131072 keys of 8 heads (0.54 GB) in 89 to 90 us, of which the plan, the
+// first reads and the joining of 19 partials per head take about 6; one token over 1000 keys in
+// 9 us, a chain of code that runs once (plan 2, first reads 1.5, sums and partial 2, joining
+// 1.5, launch 2).  It was 16 us while the walk and the copies were compiled into several places:
 // a call this short is bound by fetching instructions.
 #include <algorithm>
 
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
             }
             // The matrix product takes its weights in bf16.  Each goes in as two of them, which
             // keeps it to 2^-16: the products are not what bounds this kernel (17 % of the tensor
-            // pipe before), and without the second the weights' rounding would cost as much
+            // pipe with one part, 28 % with two), and without the second the weights' rounding would cost as much
             // precision as the output's own.  Both parts of a weight above 0 are above 0 (the
             // first is the weight less its last bit, cut off, the second the rest, rounded to
             // nearest), so that an infinite value gives that infinity: with a part of 0 or of

@@ -14,9 +14,12 @@
 // other's gaps.
 //
 // What bounds it: fp32 arithmetic (64 keys of 64 rows take 2 64 64 D FMA, 8192 cycles of an SM
-// at 128 dims) and the reads from shared memory that feed it, which take as long.
-// Measured: a prompt of 1000 tokens, 8 heads of 128, 106 us (216 four rows at a time); 8 heads
-// over 2 of 64, 56 us (187).  4 rows a thread instead of 8: 113 and 62.
+// at 128 dims), the reads from shared memory that feed it, and eight warps an SM that wait for
+// both in turn.
+// Measured: a prompt of 1000 tokens, 8 heads of 128, 106 us (216 four rows at a time), 19 TFLOP/s
+// of pairs that are seen: the SMs have work 63 % of the time (128 tiles of unequal length for 304
+// CTAs), in which the FMA pipe is busy 52 %, the shared memory 42 % and the issue slots 44 %.  8
+// heads over 2 of 64, 56 us (187).  4 rows a thread instead of 8: 113 and 62.
 #include <type_traits>
 
 #include "paged_plan.cuh"

@@ -6,10 +6,11 @@
 // token-major ("packed row" r is token r / G, head r % G of the group).  The tiles of a
 // call are laid end to end, sequence by sequence, head by head, on one axis of cost, each
 // tile as long as its fixed cost and its keys times a weight, and CTA c takes the part
-// [c chunk, (c + 1) chunk) of that axis: whatever the lengths are, every CTA does the same
-// work, and one token over a long cache fills the whole GPU.  Everything is computed from the
-// lengths on the device, by each warp that needs it (a scan over the sequences), so a
-// captured call follows the lengths that it finds when it is replayed.
+// [c chunk, (c + 1) chunk) of that axis: whatever the lengths are, the CTAs' parts are equal up
+// to one tile of at most PagedParams::whole, which is never cut, and one token over a long cache
+// fills the whole GPU.  Everything is computed from the lengths on the device, by each warp that
+// needs it (a scan over the sequences), so a captured call follows the lengths that it finds when
+// it is replayed.
 //
 // A tile that lies in one CTA's part is written by that CTA.  Of a tile cut by a part's
 // end each CTA writes its unnormalised sum, maximum and denominator to its own place in
@@ -114,7 +115,9 @@ __device__ __forceinline__ long long quotient(long long a, long long b)
 }
 
 // Tiles of one (sequence, head).  kRows packed rows a tile; every tile of a sequence
-// counts all the keys (sequences with few new tokens see nearly all in every tile).
+// counts all the keys: sequences with few new tokens see nearly all in every tile.  (Of a causal
+// prompt that goes this way the first tiles see few of the keys that they are priced at, and
+// the split is that uneven.)
 template <int kRows>
 struct FlatTiles {
     static constexpr bool kLongest = true;
@@ -255,8 +258,10 @@ struct PagedWalk {
                                  ? t.keys / 2 + 1               // not cut
                                  : static_cast<int>(min(static_cast<long long>(p.snap),
                                                         chunk >> (shift + 2)));
-            // The CTAs that touch the tile, without those whose piece has no keys (only the
-            // first and the last can have none); the first keeps a tile without keys.
+            // The CTAs that touch the tile, without the first and the last of them where their
+            // piece has no keys; the first keeps a tile without keys.  Others can have none
+            // too (a part inside the fixed cost, and with FlatTiles the parts behind the last
+            // key that a causal tile sees): they contribute a partial of weight 0.
             t.c_first = a >= c * chunk ? c : static_cast<int>(quotient(a, chunk));
             t.c_last = b <= (c + 1) * chunk ? c : static_cast<int>(quotient(b - 1, chunk));
             auto before = [&](int cta) -> int {             // keys before that CTA's part

@@ -678,8 +678,8 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  *   out = sum_j softmax_j(q . k_j / sqrt(D)) v_j,   lse = ln sum_j exp(q . k_j / sqrt(D))
  * over the keys j the row sees.  One token per sequence or thousands, in any mixture: the
  * keys are shared out evenly over the GPU whatever the lengths are.  (out, lse) is a partial
- * that attn_merge_partials can join with another over other keys.  A row that sees no key
- * gets 0 and -inf.  Slots behind a sequence's last key are never used, whatever they hold.
+ * that attn_merge_partials can join with another over other keys.  A row that sees no key, or
+ * only keys of score -inf, gets 0 and -inf.  Slots behind a sequence's last key are never used, whatever they hold.
  * A key that a row does not see never reaches it.  An infinite value gives the rows that see it
  * (with a weight that fp32 holds) the same infinity.  A value that is not finite, of a new token
  * of a call with several new tokens per sequence, may in bf16 also reach earlier new rows of its
@@ -691,11 +691,17 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  * by the caller before its first use; every call leaves it ready for the next.  Calls that
  * share a workspace must not overlap on the GPU (two captured graphs that share one must be
  * replayed in order).  After a call that timed out (ra_check_status) zero it again.
- * Scores and softmax in fp32; for the value product, whose sums are fp32, bf16 calls round a
- * weight to two bf16 parts (2^-16) if sequences bring few rows and to one (2^-8 at most) if
- * they bring many; out is rounded once.  Repeated calls on the same inputs give
- * the same bits; the split over the GPU, and with it the last bits, depends on all lengths of
- * the call.  Limits: T * H <= 2^31 - 256.  Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED (dtype,
+ * Scores and softmax in fp32; for the value product, whose sums are fp32, bf16 calls keep a
+ * weight as two bf16 parts (2^-16) or round it to one (2^-8 at most); out is rounded once.
+ * Which of the two is decided for the whole call, from its sizes: one part where T * H / H_kv >
+ * 16 * n_seqs (more than 16 rows per sequence and key head on average), pages hold a multiple
+ * of 8 slots, H / H_kv <= 128 and all strides are below 2^39, two parts otherwise.  So a single
+ * token's result may be 2^-8 of the average |v| less precise beside sequences that bring many
+ * tokens than alone; calls of their own keep it.  Repeated calls on the same inputs give the same
+ * bits; the split over the GPU, and with it the last bits, depends on all lengths of the call.
+ * Speed: a call of the second kind reads a sequence's keys once for every 16 rows, so chunks of
+ * prompts want pages of a multiple of 8 slots, and a call of their own beside very many single
+ * tokens.  Limits: T * H <= 2^31 - 256.  Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED (dtype,
  * D), RA_ERR_NOT_DIVISIBLE (H % H_kv), RA_ERR_MISALIGNED, RA_ERR_CUDA.
  */
 ra_status paged_attn_fwd(const ra_paged_desc* desc, const void* q, long long q_stride,

@@ -58,6 +58,24 @@ def test_infinite_values_that_every_row_sees(name):
         assert_attends(out[..., rest], lse, (ref[0][..., rest], ref[1], ref[2][..., rest], ref[3]), name)
 
 
+@pytest.mark.parametrize("name", SEEN)
+def test_rows_whose_scores_are_all_minus_infinity(name):
+    """Such a row is as one that sees no key; the other heads and sequences are as ever."""
+    seqs, H, H_kv, D, page, dtype = SEEN[name]
+    c = Cache(seqs, H, H_kv, D, page, dtype, seed=len(name))
+    c.q[:, 0, 0] = 1.0
+    ref = c.reference()
+    for pg in c.table[0, :-(-seqs[0][1] // page)]:
+        c.k[pg, :, 0, 0] = -math.inf               # the first sequence's keys for the first head
+    out, lse = attend(c)
+    n, G = seqs[0][0], H // H_kv
+    assert (out[:n, 0] == 0).all() and (lse[:n, 0] == -math.inf).all()
+    if G < H:
+        assert_attends(out[:, G:], lse[:, G:], tuple(x[:, G:] for x in ref), name)
+    if len(seqs) > 1:
+        assert_attends(out[n:], lse[n:], tuple(x[n:] for x in ref), name)
+
+
 # (new tokens, keys) of every sequence, H, H_kv, D, page: calls of the kernel for few rows
 TWO_PARTS = {
     "one token": ([(1, 2)], 32, 4, 128, 16),
