@@ -681,7 +681,7 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  * that attn_merge_partials can join with another over other keys.  A row that sees no key, or
  * only keys of score -inf, gets 0 and -inf.  Slots behind a sequence's last key are never used, whatever they hold.
  * A key that a row does not see never reaches it.  An infinite value gives the rows that see it
- * (with a weight that fp32 holds) the same infinity.  A value that is not finite, of a new token
+ * (with a weight of 2^-100 of the largest or more) the same infinity.  A value that is not finite, of a new token
  * of a call with several new tokens per sequence, may in bf16 also reach earlier new rows of its
  * sequence (0 times infinity in the matrix product, as in ring_attn_fwd).
  *
