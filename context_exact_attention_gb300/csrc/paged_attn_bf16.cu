@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
             }
             // The matrix product takes its weights in bf16.  Each goes in as two of them, which
             // keeps it to 2^-16: the products are not what bounds this kernel (17 % of the tensor
-            // pipe with one part, 28 % with two), and without the second the weights' rounding would cost as much
-            // precision as the output's own.  Both parts of a weight above 0 are above 0 (the
+            // pipe with one part, 28 % with two), and without the second the weights' rounding
+            // would cost as much precision as the output's own.  Both parts of a weight above 0 are above 0 (the
             // first is the weight less its last bit, cut off, the second the rest, rounded to
             // nearest), so that an infinite value gives that infinity: with a part of 0 or of
             // the other sign the two products would add up to NaN.

@@ -679,7 +679,8 @@ unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype);
  * over the keys j the row sees.  One token per sequence or thousands, in any mixture: the
  * keys are shared out evenly over the GPU whatever the lengths are.  (out, lse) is a partial
  * that attn_merge_partials can join with another over other keys.  A row that sees no key, or
- * only keys of score -inf, gets 0 and -inf.  Slots behind a sequence's last key are never used, whatever they hold.
+ * only keys of score -inf, gets 0 and -inf.  Slots behind a sequence's last key are never used,
+ * whatever they hold.
  * A key that a row does not see never reaches it.  An infinite value gives the rows that see
  * it, with a weight of 2^-100 of the largest or more, the same infinity.  A value that is not
  * finite, of a new token of a call with several new tokens per sequence, may in bf16 also reach
