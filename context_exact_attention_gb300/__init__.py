@@ -15,6 +15,7 @@ import ctypes
 import os
 import struct
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -29,6 +30,8 @@ __all__ = [
     "ring_attn_bwd_zigzag", "ring_attn_bwd_varlen", "ring_attn_fwd_ex", "ring_attn_bwd_ex",
     "ulysses_attention_fused", "varlen_schedule", "EXPORTED_SYMBOLS", "RopeTable", "rope_table",
     "rope_fwd", "rope_bwd", "paged_kv_append", "paged_attn_fwd", "paged_attn_workspace",
+    "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_workspace", "PagePool", "page_pool",
+    "PagedStep", "paged_step", "paged_reserve", "paged_release", "paged_kv_keep", "KEEP_ALL",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -53,7 +56,9 @@ EXPORTED_SYMBOLS = (
     "ring_attn_bwd_ex", "ulysses_attention_fused", "ring_attn_varlen_schedule",
     "ring_attn_varlen_schedule_bytes", "ra_padded_length", "ra_probe_bounds_check",
     "ra_rope_phases", "ra_rope_phases_of", "rope_fwd", "rope_bwd", "paged_kv_append",
-    "paged_attn_fwd", "paged_attn_workspace_bytes",
+    "paged_attn_fwd", "paged_attn_workspace_bytes", "qk_norm_workspace_bytes", "qk_norm_rope_fwd",
+    "qk_norm_rope_bwd", "paged_kv_append_ex", "paged_attn_tree_fwd", "paged_reserve",
+    "paged_release", "paged_kv_keep",
 )
 
 
@@ -106,6 +111,20 @@ class PagedDesc(ctypes.Structure):
                 ("head_stride", ctypes.c_longlong), ("table_stride", ctypes.c_longlong),
                 ("page_table", ctypes.c_void_p), ("cu_new", ctypes.c_void_p),
                 ("kv_lens", ctypes.c_void_p), ("dtype", ctypes.c_int), ("causal", ctypes.c_int)]
+
+
+class HeadNorm(ctypes.Structure):
+    """Mirror of ra_head_norm (include/ring_attn.h)."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
+class PagePoolDesc(ctypes.Structure):
+    """Mirror of ra_page_pool (include/ring_attn.h)."""
+    _fields_ = [("num_pages", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("free_pages", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("state", ctypes.c_void_p)]
 
 
 class RingAttnError(RuntimeError):
@@ -184,6 +203,14 @@ def _open(path, build_if_missing, debug_bounds):
         "rope_bwd": [vp, vp, vp, vp, vp, vp, vp],
         "paged_kv_append": [vp, vp, vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, vp],
         "paged_attn_fwd": [vp, vp, ll, vp, vp, vp, vp, vp, ctypes.c_ulonglong, vp],
+        "qk_norm_rope_fwd": [vp, vp, vp, vp, vp, vp, vp, vp],
+        "qk_norm_rope_bwd": [vp, vp, vp, vp, vp, vp, ll, vp, ll, vp, vp, vp, vp, vp,
+                             ctypes.c_ulonglong, vp],
+        "paged_kv_append_ex": [vp, vp, vp, vp, vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, vp],
+        "paged_attn_tree_fwd": [vp, vp, i, ll, vp, ll, vp, vp, vp, vp, vp, ctypes.c_ulonglong, vp],
+        "paged_reserve": [vp, vp, vp, vp, i, ll, i, i, vp, vp, vp, vp, vp, vp, i, vp],
+        "paged_release": [vp, vp, vp, i, ll, i, vp],
+        "paged_kv_keep": [vp, vp, i, ll, i, ll, vp, vp, vp, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -197,6 +224,8 @@ def _open(path, build_if_missing, debug_bounds):
     lib.ring_attn_varlen_schedule_bytes.restype = ctypes.c_ulonglong
     lib.paged_attn_workspace_bytes.argtypes = [i, i]
     lib.paged_attn_workspace_bytes.restype = ctypes.c_ulonglong
+    lib.qk_norm_workspace_bytes.argtypes = []
+    lib.qk_norm_workspace_bytes.restype = ctypes.c_ulonglong
     lib.ra_status_string.argtypes = [ctypes.c_int]
     lib.ra_status_string.restype = ctypes.c_char_p
     lib.ra_padded_length.argtypes = [ctypes.c_longlong, i, i]
@@ -759,6 +788,7 @@ def rope_table(rot_dim: int, base: float = 10000.0, style: str = "half", scaling
 # (the formats are RopeDesc's and PagedDesc's layouts).
 _ROPE_DESC = struct.Struct("=7i4xQi4xQ2i4q")
 _PAGED_DESC = struct.Struct("=8i4q3Q2i")
+_HEAD_NORM = struct.Struct("=2Qi2f4x")
 
 
 def _same_device(first, *others):
@@ -841,18 +871,36 @@ def _float_code(dtype, name):
     raise ValueError(f"{name} must be bf16 or fp32")
 
 
-def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out, k_out, stream):
+def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out, k_out, stream,
+               norm=None):
+    """norm: None, or (q_weight, k_weight, eps, weight_offset), and rope may then be None."""
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    device = _same_device(ref, k, rope.phases, positions, cu_seqlens, q_out, k_out)
+    device = _same_device(ref, k, rope.phases if rope is not None else None, positions, cu_seqlens,
+                          q_out, k_out, *(norm[:2] if norm is not None else ()))
     s = _stream_here(device, stream)
     if s is None:
         with _entered(device, stream):
             return _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out,
-                              k_out, None)
+                              k_out, None, norm)
+    d, B, L, D, q_out, k_out = _rope_args(q, k, ref, device, positions, offset, layout, P,
+                                          cu_seqlens, q_out, k_out)
+    if B > 0 and L > 0:
+        r = rope._c if rope is not None else None
+        if norm is None:
+            _call_fast(name, d, r, _addr(q), _addr(k), _addr(q_out), _addr(k_out), s)
+        else:
+            _call_fast(name, d, r, _head_norm(D, *norm), _addr(q), _addr(k), _addr(q_out),
+                       _addr(k_out), s)
+    return q_out, k_out
+
+
+def _rope_args(q, k, ref, device, positions, offset, layout, P, cu_seqlens, q_out, k_out):
+    """The checks of a call that rotates q into q_out and k into k_out (ref: one that is given):
+    (packed ra_rope_desc, B, L, D, q_out, k_out), the outputs allocated if they were None."""
     dtype = ref.dtype
     code = _float_code(dtype, "q and k")
     packed = layout == "packed"
@@ -899,11 +947,9 @@ def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out
         kos = _token_stride(k_out, k_shape, "k_out")
     elif k_out is not None:
         raise ValueError("an output without its input")
-    if B > 0 and L > 0:
-        d = _ROPE_DESC.pack(B, L, H, H_kv, D, P, LAYOUTS[layout], _addr(cu_seqlens), n_seqs,
-                            _addr(positions), offset, code, qs, ks, qos, kos)
-        _call_fast(name, d, rope._c, _addr(q), _addr(k), _addr(q_out), _addr(k_out), s)
-    return q_out, k_out
+    d = _ROPE_DESC.pack(B, L, H, H_kv, D, P, LAYOUTS[layout], _addr(cu_seqlens), n_seqs,
+                        _addr(positions), offset, code, qs, ks, qos, kos)
+    return d, B, L, D, q_out, k_out
 
 
 def rope_fwd(q, k, rope: RopeTable, positions=None, offset: int = 0, layout: str = "contiguous",
@@ -926,6 +972,94 @@ def rope_bwd(dq_out, dk_out, rope: RopeTable, positions=None, offset: int = 0,
     arguments as rope_fwd, q_out and k_out receiving dq and dk.  Returns (dq, dk)."""
     return _rope_call("rope_bwd", dq_out, dk_out, rope, positions, offset, layout, P, cu_seqlens,
                       q_out, k_out, stream)
+
+
+def _head_norm(D, q_weight, k_weight, eps, weight_offset):
+    """Packed ra_head_norm of weights [D] (or None) for heads of D dims."""
+    code = RA_F32
+    for name, w, other in (("q_weight", q_weight, k_weight), ("k_weight", k_weight, q_weight)):
+        if w is None:
+            continue
+        if w.shape != (D,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [D] tensor")
+        code = _float_code(w.dtype, name)
+        if other is not None and other.dtype is not w.dtype:
+            raise ValueError("the weights must have one dtype")
+    return _HEAD_NORM.pack(_addr(q_weight), _addr(k_weight), code, eps, weight_offset)
+
+
+def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, rope: RopeTable | None = None,
+                     eps: float = 1e-6, weight_offset: float = 0.0, positions=None,
+                     offset: int = 0, layout: str = "contiguous", P: int = 1, cu_seqlens=None,
+                     q_out=None, k_out=None, stream=None):
+    """rope_fwd of heads that are normalised first: x (weight + weight_offset) /
+    sqrt(mean(x^2) + eps) over each head's D dims, then the rotation (rope None: none), in one
+    launch with one rounding.  q_weight, k_weight: [D] in bf16 or fp32, or None for ones.  The
+    other arguments as rope_fwd.  Returns (q_out, k_out)."""
+    return _rope_call("qk_norm_rope_fwd", q, k, rope, positions, offset, layout, P, cu_seqlens,
+                      q_out, k_out, stream, (q_weight, k_weight, eps, weight_offset))
+
+
+def qk_norm_workspace(device=None):
+    """A zeroed workspace for qk_norm_rope_bwd: keep one per stream (calls that share one must
+    not overlap on the GPU)."""
+    dev = torch.device(device) if device is not None else torch.device(
+        "cuda", torch.cuda.current_device())
+    return torch.zeros(int(load_library().qk_norm_workspace_bytes()), dtype=torch.uint8, device=dev)
+
+
+def qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, rope: RopeTable | None = None,
+                     eps: float = 1e-6, weight_offset: float = 0.0, positions=None,
+                     offset: int = 0, layout: str = "contiguous", P: int = 1, cu_seqlens=None,
+                     dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None,
+                     stream=None):
+    """Gradients of qk_norm_rope_fwd: q, k are its inputs, dq_out, dk_out the gradients of its
+    outputs.  Returns (dq, dk, dq_weight, dk_weight), the weights' in fp32 [D] (None for a
+    tensor that was not given).  workspace: qk_norm_workspace(), kept by the caller (None
+    allocates and zeroes one for this call)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
+    device = _same_device(ref, k, dq_out, dk_out, q_weight, k_weight, positions, cu_seqlens, dq,
+                          dk, dq_weight, dk_weight, workspace,
+                          rope.phases if rope is not None else None)
+    s = _stream_here(device, stream)
+    if s is None:
+        with _entered(device, stream):
+            return qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, rope, eps,
+                                    weight_offset, positions, offset, layout, P, cu_seqlens, dq,
+                                    dk, dq_weight, dk_weight, workspace)
+    d, B, L, D, dq, dk = _rope_args(q, k, ref, device, positions, offset, layout, P, cu_seqlens,
+                                    dq, dk)
+    steps, weights = [], []
+    for x, dy, w in ((q, dq_out, dq_weight), (k, dk_out, dk_weight)):
+        if x is None:
+            if dy is not None or w is not None:
+                raise ValueError("a gradient without its input")
+        elif dy is None or dy.shape != x.shape or dy.dtype is not x.dtype:
+            raise ValueError("the outputs' gradients must be shaped and typed like q and k")
+        elif w is None:
+            w = torch.empty(D, dtype=torch.float32, device=device)
+        elif w.shape != (D,) or w.dtype is not torch.float32 or not w.is_contiguous():
+            raise ValueError("the weights' gradients must be contiguous fp32 [D] tensors")
+        steps.append(_token_stride(dy, dy.shape, "the outputs' gradients") if x is not None else 0)
+        weights.append(w)
+    norm = _head_norm(D, q_weight, k_weight, eps, weight_offset)
+    if B > 0 and L > 0:
+        if workspace is None:
+            workspace = qk_norm_workspace(device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        _call_fast("qk_norm_rope_bwd", d, rope._c if rope is not None else None, norm, _addr(q),
+                   _addr(k), _addr(dq_out), steps[0], _addr(dk_out), steps[1], _addr(dq), _addr(dk),
+                   _addr(weights[0]), _addr(weights[1]), workspace.data_ptr(), workspace.nbytes, s)
+    else:
+        for w in weights:
+            if w is not None:
+                w.zero_()
+    return dq, dk, weights[0], weights[1]
 
 
 def _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal):
@@ -951,19 +1085,26 @@ def _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal):
 
 
 def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
-                    rope: RopeTable | None = None, q=None, q_out=None, stream=None):
+                    rope: RopeTable | None = None, q=None, q_out=None, stream=None,
+                    positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    weight_offset: float = 0.0, normalise: bool | None = None):
     """Writes a step's new keys and values (k, v: [T, H_kv, D]; sequence g's are rows
     [cu_new[g], cu_new[g + 1]), the last of its kv_lens[g]) into the pages [num_pages,
     page_size, H_kv, D] that page_table names, k rotated by rope on the way.  q [T, H, D],
     if given, is rotated into q_out (allocated like q, zeroed, if None; q_out=q in place)
-    and returned.  Pages and tokens may be strided views (see ra_paged_desc)."""
+    and returned.  Pages and tokens may be strided views (see ra_paged_desc).
+    positions: int32 [T], the positions to rotate by where they are not the tokens' places in
+    their sequences (paged_reserve's, for drafted trees).  q_weight, k_weight ([D], either may
+    be None for ones) normalise q and k first, as qk_norm_rope_fwd does; normalise=True does so
+    without any weights."""
     device = _same_device(k, v, k_pages, v_pages, page_table, cu_new, kv_lens, q, q_out,
-                          rope.phases if rope is not None else None)
+                          rope.phases if rope is not None else None, positions, q_weight, k_weight)
     s = _stream_here(device, stream)
     if s is None:
         with _entered(device, stream):
             return paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens, rope, q,
-                                   q_out)
+                                   q_out, None, positions, q_weight, k_weight, eps, weight_offset,
+                                   normalise)
     shape, dtype = k.shape, k.dtype
     pages = k_pages.shape
     if len(shape) != 3 or v.shape != shape or len(pages) != 4 or shape[1] != pages[2] \
@@ -985,11 +1126,24 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
     elif q_out is not None:
         raise ValueError("q_out must be shaped and typed like q")
     d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, 0)
+    norm = None
+    if q_weight is not None or k_weight is not None or normalise:
+        if normalise is False:
+            raise ValueError("weights without a norm")
+        norm = _head_norm(shape[2], q_weight, k_weight, eps, weight_offset)
+    if positions is not None:
+        _index_tensor(positions, "positions", 1, (T,))
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
     if T > 0:
-        _call_fast("paged_kv_append", d, rope._c if rope is not None else None, _addr(q), qs,
-                   k.data_ptr(), _token_stride(k, shape, "k"), v.data_ptr(),
-                   _token_stride(v, shape, "v"), _addr(q_out), qos, k_pages.data_ptr(),
-                   v_pages.data_ptr(), s)
+        args = (_addr(q), qs, k.data_ptr(), _token_stride(k, shape, "k"), v.data_ptr(),
+                _token_stride(v, shape, "v"), _addr(q_out), qos, k_pages.data_ptr(),
+                v_pages.data_ptr(), s)
+        r = rope._c if rope is not None else None
+        if norm is None and positions is None:
+            _call_fast("paged_kv_append", d, r, *args)
+        else:
+            _call_fast("paged_kv_append_ex", d, r, norm, _addr(positions), *args)
     return q_out
 
 
@@ -1005,18 +1159,22 @@ def paged_attn_workspace(D: int, dtype=torch.bfloat16, device=None):
 
 
 def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: bool = True, out=None,
-                   lse=None, want_lse: bool = True, workspace=None, stream=None):
+                   lse=None, want_lse: bool = True, workspace=None, stream=None, masks=None):
     """Attention of the step's queries q [T, H, D] over the paged cache (their own keys
     appended before): row i of a sequence's n new ones sees keys [0, kv_lens - n + i], or all
     with causal=False.  workspace: paged_attn_workspace(D, dtype), kept by the caller (None
-    allocates and zeroes one for this call).  Returns (out [T, H, D], lse fp32 [T, H]); rows
-    behind the last sequence are left as they are (zero in an out allocated here)."""
-    device = _same_device(q, k_pages, v_pages, page_table, cu_new, kv_lens, out, lse, workspace)
+    allocates and zeroes one for this call).  masks: int32 [T, words], drafted trees
+    (paged_reserve's): row i then sees the keys from before the step and the new tokens of its
+    sequence whose bits its mask has, whatever causal says.  Returns (out [T, H, D], lse fp32
+    [T, H]); rows behind the last sequence are left as they are (zero in an out allocated
+    here)."""
+    device = _same_device(q, k_pages, v_pages, page_table, cu_new, kv_lens, out, lse, workspace,
+                          masks)
     s = _stream_here(device, stream)
     if s is None:
         with _entered(device, stream):
             return paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal, out,
-                                  lse, want_lse, workspace)
+                                  lse, want_lse, workspace, None, masks)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3 or dtype is not k_pages.dtype or shape[2] != k_pages.shape[-1]:
         raise ValueError("q must be [T, H, D] with the head dim and dtype of the pages")
@@ -1031,15 +1189,179 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
             raise ValueError("lse must be a contiguous fp32 [T, H] tensor")
     elif want_lse:
         lse = torch.zeros((T, H), dtype=torch.float32, device=device)
+    if masks is not None:
+        words = masks.shape[-1] if masks.dim() == 2 else 0
+        _index_tensor(masks, "masks", 2, (T, words))
     if T > 0:
         if workspace is None:
             workspace = paged_attn_workspace(D, dtype, device)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        _call_fast("paged_attn_fwd", d, q.data_ptr(), _token_stride(q, shape, "q"),
-                   k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _addr(lse),
-                   workspace.data_ptr(), workspace.nbytes, s)
+        args = (q.data_ptr(), _token_stride(q, shape, "q"), k_pages.data_ptr(), v_pages.data_ptr(),
+                out.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.nbytes, s)
+        if masks is None:
+            _call_fast("paged_attn_fwd", d, *args)
+        else:
+            _call_fast("paged_attn_tree_fwd", d, masks.data_ptr(), words,
+                       masks.stride(0) if T > 1 else words, *args)
     return out, lse
+
+
+KEEP_ALL = -2
+
+
+class PagePool:
+    """Handle of a pool of pages (ra_page_pool), made by page_pool: free, the stack of free pages
+    of which the first count are free, held, the pages of every sequence, and status, how the
+    last paged_reserve ended (0, or 1 too few pages, 2 too many rows, 3 a sequence too long);
+    int32 tensors on the device.  Calls that share a pool must not overlap on the GPU."""
+
+    def __init__(self, num_pages: int, n_seqs: int, device):
+        self.num_pages, self.n_seqs = num_pages, n_seqs
+        self.free = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.held = torch.zeros(n_seqs, dtype=torch.int32, device=device)
+        self.state = torch.zeros(3, dtype=torch.int32, device=device)
+        self.count, self.status = self.state[:1], self.state[2:]
+        self.count.fill_(num_pages)
+        self._desc = PagePoolDesc(num_pages, n_seqs, self.free.data_ptr(), self.held.data_ptr(),
+                                  self.state.data_ptr())
+        self._c = ctypes.byref(self._desc)
+
+
+def page_pool(num_pages: int, n_seqs: int, device=None) -> PagePool:
+    """A PagePool of num_pages pages, all free (page 0 taken first), for n_seqs sequences."""
+    if num_pages < 1 or n_seqs < 1:
+        raise ValueError("num_pages and n_seqs must be positive")
+    dev = torch.device(device) if device is not None else torch.device(
+        "cuda", torch.cuda.current_device())
+    return PagePool(num_pages, n_seqs, dev)
+
+
+class PagedStep(NamedTuple):
+    """What a step knows of its rows (paged_reserve): cu_new, kv_lens as the paged calls take
+    them, positions to rotate by, slots of the keys, masks of a drafted tree (or None)."""
+    cu_new: torch.Tensor
+    kv_lens: torch.Tensor
+    positions: torch.Tensor | None
+    slots: torch.Tensor | None
+    masks: torch.Tensor | None
+
+
+def paged_step(n_seqs: int, rows: int, mask_words: int = 0, device=None) -> PagedStep:
+    """Buffers for steps of up to `rows` new tokens, with masks of 32 * mask_words of them per
+    sequence, to be filled by paged_reserve step after step (and replayed in a graph)."""
+    dev = torch.device(device) if device is not None else torch.device(
+        "cuda", torch.cuda.current_device())
+
+    def ints(*shape, dtype=torch.int32):
+        return torch.zeros(shape, dtype=dtype, device=dev)
+    return PagedStep(ints(n_seqs + 1), ints(n_seqs), ints(rows), ints(rows, dtype=torch.int64),
+                     ints(rows, mask_words) if mask_words else None)
+
+
+def _pool_args(pool, lens, page_table):
+    _index_tensor(lens, "lens", 1, (pool.n_seqs,))
+    _index_tensor(page_table, "page_table", 2)
+    rows, cols = page_table.shape
+    if rows != pool.n_seqs:
+        raise ValueError("page_table must have a row for every sequence of the pool")
+    if not lens.is_contiguous():
+        raise ValueError("lens must be contiguous")
+    return page_table.data_ptr(), cols, page_table.stride(0) if rows > 1 else cols
+
+
+def paged_reserve(pool: PagePool, new_lens, lens, page_table, page_size: int, step: PagedStep,
+                  parents=None, stream=None) -> PagedStep:
+    """Makes room for a step in which sequence g, of lens[g] keys, brings new_lens[g] tokens: its
+    pages from the pool into page_table (int32 [n_seqs, max_pages]), and step's tensors filled
+    with the rows, lengths, positions and slots (see paged_reserve in ring_attn.h).  parents:
+    int32 [rows], for drafted trees: entry i of a sequence's tokens names the one that its
+    token i extends (-1: a root); positions then follow the depth, and step.masks, if there,
+    get every row's ancestors.  step.kv_lens may be lens itself.  A step that does not fit
+    becomes one without rows, and pool.status says why.  Returns step."""
+    cu_new, kv_lens, positions, slots, masks = step
+    device = _same_device(new_lens, lens, page_table, pool.state, cu_new, kv_lens, positions, slots,
+                          masks, parents)
+    s = _stream_here(device, stream)
+    if s is None:
+        with _entered(device, stream):
+            return paged_reserve(pool, new_lens, lens, page_table, page_size, step, parents)
+    n = pool.n_seqs
+    table = _pool_args(pool, lens, page_table)
+    _index_tensor(new_lens, "new_lens", 1, (n,))
+    _index_tensor(cu_new, "step.cu_new", 1, (n + 1,))
+    _index_tensor(kv_lens, "step.kv_lens", 1, (n,))
+    rows = next((t.shape[0] for t in (positions, slots, masks, parents) if t is not None), None)
+    if rows is None:
+        raise ValueError("step must have positions, slots or masks, whose size is its rows'")
+    if positions is not None:
+        _index_tensor(positions, "step.positions", 1, (rows,))
+    if parents is not None:
+        _index_tensor(parents, "parents", 1, (rows,))
+    if slots is not None and (slots.dtype is not torch.int64 or slots.shape != (rows,)):
+        raise ValueError(f"step.slots must be an int64 tensor of shape [{rows}]")
+    words = 0
+    if parents is not None and masks is not None:
+        words = masks.shape[-1]
+        _index_tensor(masks, "step.masks", 2, (rows, words))
+    for t in (new_lens, cu_new, kv_lens, positions, slots, parents, masks):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("all tensors but page_table must be contiguous")
+    _call_fast("paged_reserve", pool._c, new_lens.data_ptr(), lens.data_ptr(), *table, page_size,
+               rows, cu_new.data_ptr(), kv_lens.data_ptr(), _addr(positions), _addr(slots),
+               _addr(parents), masks.data_ptr() if words else 0, words, s)
+    return step
+
+
+def paged_release(pool: PagePool, lens, page_table, page_size: int, stream=None):
+    """Gives the pages behind the first lens[g] keys of every sequence back to the pool (all of
+    an ended sequence's with lens[g] = 0) and sets their entries of page_table to -1.  Undoes
+    paged_reserve."""
+    device = _same_device(lens, page_table, pool.state)
+    s = _stream_here(device, stream)
+    if s is None:
+        with _entered(device, stream):
+            return paged_release(pool, lens, page_table, page_size)
+    _call_fast("paged_release", pool._c, lens.data_ptr(), *_pool_args(pool, lens, page_table),
+               page_size, s)
+
+
+def paged_kv_keep(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens=None, stream=None):
+    """After a step's drafted tokens have been checked: kept (int32 [n_seqs, width]) names the
+    accepted ones of every sequence in ascending order (-1 behind them, or KEEP_ALL in front:
+    every new token stays), whose keys and values move to the front of the step's slots.
+    k_pages, v_pages: the pages of one layer, or of all layers at once, [layers, num_pages,
+    page_size, H_kv, D].  Returns lens (int32 [n_seqs], allocated if None, not kv_lens): the
+    lengths with what was kept."""
+    device = _same_device(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens)
+    s = _stream_here(device, stream)
+    if s is None:
+        with _entered(device, stream):
+            return paged_kv_keep(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens)
+    layers, step = 1, 0
+    if k_pages.dim() == 5:
+        if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+            raise ValueError("k_pages and v_pages must be alike")
+        layers, step = k_pages.shape[0], k_pages.stride(0)
+        if layers < 1:
+            raise ValueError("k_pages and v_pages must have a layer")
+        k_pages, v_pages = k_pages[0], v_pages[0]
+    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, 0, 1, 0)
+    n = kv_lens.shape[0]
+    _index_tensor(kept, "kept", 2)
+    width = kept.shape[1]
+    if kept.shape[0] != n:
+        raise ValueError("kept must have a row for every sequence")
+    if lens is None:
+        lens = torch.empty(n, dtype=torch.int32, device=device)
+    else:
+        _index_tensor(lens, "lens", 1, (n,))
+        if not lens.is_contiguous():
+            raise ValueError("lens must be contiguous")
+    _call_fast("paged_kv_keep", d, kept.data_ptr(), width, kept.stride(0) if n > 1 else width,
+               layers, step if layers > 1 else 0, k_pages.data_ptr(), v_pages.data_ptr(),
+               lens.data_ptr(), s)
+    return lens
 
 
 def check_status(stream=None) -> int:

@@ -60,8 +60,10 @@ ra_status check_rope(const ra_rope* rope, int D)
     return aligned(rope->phases, 8) ? RA_OK : RA_ERR_MISALIGNED;
 }
 
-ra_status rope_impl(const ra_rope_desc* d, const ra_rope* rope, const void* q, const void* k,
-                    void* q_out, void* k_out, float sign, ra_stream_t stream)
+// The checks of a call that rotates q into q_out and k into k_out, and its arguments for the
+// kernels.  rope may be NULL where a norm goes before it (norm: whether one does).
+ra_status rope_args(const ra_rope_desc* d, const ra_rope* rope, bool norm, const void* q, const void* k,
+                    void* q_out, void* k_out, float sign, ra_stream_t stream, ra::RopeArgs* args)
 {
     if (!d) return RA_ERR_INVALID_ARG;
     if (d->B < 1 || d->L < 1 || d->D < 1 || d->P < 1 || d->H < 0 || d->H_kv < 0 ||
@@ -70,7 +72,7 @@ ra_status rope_impl(const ra_rope_desc* d, const ra_rope* rope, const void* q, c
     if (d->dtype != RA_BF16 && d->dtype != RA_F32) return RA_ERR_UNSUPPORTED;
     const int elem = d->dtype == RA_BF16 ? 2 : 4;
     if ((d->D * elem) % 16 != 0 || d->D > 256) return RA_ERR_UNSUPPORTED;
-    ra_status st = check_rope(rope, d->D);
+    ra_status st = norm && !rope ? RA_OK : check_rope(rope, d->D);
     if (st != RA_OK) return st;
     if ((d->H > 0) != (q != nullptr) || (d->H > 0) != (q_out != nullptr) ||
         (d->H_kv > 0) != (k != nullptr) || (d->H_kv > 0) != (k_out != nullptr))
@@ -96,7 +98,8 @@ ra_status rope_impl(const ra_rope_desc* d, const ra_rope* rope, const void* q, c
     if (d->positions && d->layout != RA_LAYOUT_CONTIGUOUS) return RA_ERR_INVALID_ARG;
     if (d->positions && !aligned(d->positions, 4)) return RA_ERR_MISALIGNED;
 
-    ra::RopeArgs a{};
+    ra::RopeArgs& a = *args;
+    a = {};
     a.rows = static_cast<long long>(d->B) * d->L;
     const long long nq = static_cast<long long>(d->H) * d->D, nk = static_cast<long long>(d->H_kv) * d->D;
     if (nq + nk > 0x7fffffffll || static_cast<ull>(a.rows) * (nq + nk) >= kMaxElems)
@@ -118,14 +121,16 @@ ra_status rope_impl(const ra_rope_desc* d, const ra_rope* rope, const void* q, c
     const Rows rk{k, n, static_cast<ull>(nk) * elem, static_cast<ull>(a.k_stride) * elem};
     const Rows rqo{q_out, n, static_cast<ull>(nq) * elem, static_cast<ull>(a.q_out_stride) * elem};
     const Rows rko{k_out, n, static_cast<ull>(nk) * elem, static_cast<ull>(a.k_out_stride) * elem};
+    const void* phases = rope ? rope->phases : nullptr;
+    const ull phase_bytes = rope ? 4ull * rope->rot_dim : 0;
     // in place (the same rows) is allowed, any other overlap is not
     const bool q_in_place = q == q_out && a.q_stride == a.q_out_stride;
     const bool k_in_place = k == k_out && a.k_stride == a.k_out_stride;
     if (nq > 0 && ((!q_in_place && overlap(rqo, rq)) || (nk > 0 && overlap(rqo, rk)) ||
-                   overlap(q_out, rqo.span(), rope->phases, 4ull * rope->rot_dim)))
+                   overlap(q_out, rqo.span(), phases, phase_bytes)))
         return RA_ERR_INVALID_ARG;
     if (nk > 0 && ((!k_in_place && overlap(rko, rk)) || (nq > 0 && overlap(rko, rq)) ||
-                   overlap(k_out, rko.span(), rope->phases, 4ull * rope->rot_dim)))
+                   overlap(k_out, rko.span(), phases, phase_bytes)))
         return RA_ERR_INVALID_ARG;
     if (nq > 0 && nk > 0 && overlap(rqo, rko)) return RA_ERR_INVALID_ARG;
     if (d->positions && (overlap(q_out, rqo.span(), d->positions, 4 * n) ||
@@ -148,38 +153,71 @@ ra_status rope_impl(const ra_rope_desc* d, const ra_rope* rope, const void* q, c
     a.H_kv = d->H_kv;
     a.D = d->D;
     a.elem = elem;
-    a.rot = rope->rot_dim;
-    a.half_style = rope->style == RA_ROPE_HALF;
-    a.amplitude = rope->amplitude;
+    a.rot = rope ? rope->rot_dim : 0;
+    a.half_style = !rope || rope->style == RA_ROPE_HALF;
+    a.amplitude = rope ? rope->amplitude : 1.f;
     a.sign = sign;
-    a.phases = rope->phases;
+    a.phases = rope ? rope->phases : nullptr;
     a.layout = d->layout;
     a.positions = d->positions;
     a.position_offset = d->position_offset;
     a.cu_seqlens = d->cu_seqlens;
     a.n_seqs = d->n_seqs;
     a.stream = reinterpret_cast<cudaStream_t>(stream);
-    st = ra::current_status_word(&a.status);
-    if (st != RA_OK) return st;
-    return from_cuda(ra::launch_rope(a));
+    return RA_OK;
 }
 
-// The cache's extent in elements; RA_OK only if distinct (page, slot, head) triples are
+ra_status rope_impl(const ra_rope_desc* d, const ra_rope* rope, const void* q, const void* k,
+                    void* q_out, void* k_out, float sign, ra_stream_t stream)
+{
+    ra::RopeArgs a;
+    ra_status st = rope_args(d, rope, false, q, k, q_out, k_out, sign, stream, &a);
+    if (st == RA_OK) st = ra::current_status_word(&a.status);
+    return st != RA_OK ? st : from_cuda(ra::launch_rope(a));
+}
+
+// The norm's part of the arguments of a call with heads of D dims; the outputs outs[i] of
+// bytes[i] must not share memory with the weights.
+ra_status norm_args(const ra_head_norm* norm, int D, void* const* outs, const ull* bytes, int n_outs,
+                    ra::NormArgs* n)
+{
+    if (!norm) return RA_ERR_INVALID_ARG;
+    if (norm->weight_dtype != RA_BF16 && norm->weight_dtype != RA_F32) return RA_ERR_UNSUPPORTED;
+    if (!(norm->eps >= 0) || !std::isfinite(norm->eps) || !std::isfinite(norm->weight_offset))
+        return RA_ERR_INVALID_ARG;
+    n->weight_elem = norm->weight_dtype == RA_BF16 ? 2 : 4;
+    n->q_weight = norm->q_weight;
+    n->k_weight = norm->k_weight;
+    n->eps = norm->eps;
+    n->weight_offset = norm->weight_offset;
+    for (const void* w : {norm->q_weight, norm->k_weight}) {
+        if (!aligned(w, n->weight_elem)) return RA_ERR_MISALIGNED;
+        for (int i = 0; w && i < n_outs; ++i)
+            if (overlap(outs[i], bytes[i], w, static_cast<ull>(D) * n->weight_elem))
+                return RA_ERR_INVALID_ARG;
+    }
+    return RA_OK;
+}
+
+
+// The cache's extent in elements; RA_OK only if distinct (layer, page, slot, head) quadruples are
 // distinct memory and every head vector starts on a 16-byte boundary.
 struct Dim {
     ull size, stride;
 };
-ra_status page_extent(const ra_paged_desc* d, int elem, ull* elems, Dim (&dims)[3])
+ra_status page_extent(const ra_paged_desc* d, int layers, long long layer_stride, int elem, ull* elems,
+                      Dim (&dims)[4])
 {
     dims[0] = {static_cast<ull>(d->num_pages), static_cast<ull>(d->page_stride)};
     dims[1] = {static_cast<ull>(d->page_size), static_cast<ull>(d->token_stride)};
     dims[2] = {static_cast<ull>(d->H_kv), static_cast<ull>(d->head_stride)};
-    if (d->page_stride < 0 || d->token_stride < 0 || d->head_stride < 0) return RA_ERR_INVALID_ARG;
+    dims[3] = {static_cast<ull>(layers), static_cast<ull>(layer_stride)};
+    if (layer_stride < 0 || d->page_stride < 0 || d->token_stride < 0 || d->head_stride < 0) return RA_ERR_INVALID_ARG;
     for (const Dim& x : dims) {
         if (x.stride >= kMaxElems) return RA_ERR_INVALID_ARG;
         if (x.size > 1 && (x.stride * elem) % 16 != 0) return RA_ERR_MISALIGNED;
     }
-    std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) {
+    std::sort(dims, dims + 4, [](const Dim& a, const Dim& b) {
         return a.stride != b.stride ? a.stride < b.stride : a.size < b.size;
     });
     ull span = static_cast<ull>(d->D);
@@ -195,7 +233,7 @@ ra_status page_extent(const ra_paged_desc* d, int elem, ull* elems, Dim (&dims)[
 
 // Whether two caches of one geometry share memory.  Interleaved views of one buffer (keys
 // and values of a page, of a token or of a head side by side) do not.
-bool pages_overlap(const void* k, const void* v, const Dim (&dims)[3], ull D, ull span, int elem)
+bool pages_overlap(const void* k, const void* v, const Dim (&dims)[4], ull D, ull span, int elem)
 {
     if (!overlap(k, span * elem, v, span * elem)) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(k), y = reinterpret_cast<uintptr_t>(v);
@@ -203,12 +241,12 @@ bool pages_overlap(const void* k, const void* v, const Dim (&dims)[3], ull D, ul
     if (bytes % elem != 0) return true;
     ull delta = bytes / elem;
     // spans of the dims inside each level, outermost first
-    ull inner[3], s = D;
-    for (int i = 0; i < 3; ++i) {
+    ull inner[4], s = D;
+    for (int i = 0; i < 4; ++i) {
         inner[i] = s;
         if (dims[i].size > 1) s += (dims[i].size - 1) * dims[i].stride;
     }
-    for (int i = 2; i >= 0; --i) {
+    for (int i = 3; i >= 0; --i) {
         if (dims[i].size == 1) continue;
         delta %= dims[i].stride;
         if (delta >= inner[i] && dims[i].stride - delta >= inner[i]) return false;
@@ -221,7 +259,8 @@ bool pages_overlap(const void* k, const void* v, const Dim (&dims)[3], ull D, ul
     return true;
 }
 
-ra_status check_paged(const ra_paged_desc* d, int* elem, ull* page_elems, Dim (&dims)[3])
+ra_status check_paged(const ra_paged_desc* d, int* elem, ull* page_elems, Dim (&dims)[4], int layers = 1,
+                      long long layer_stride = 0)
 {
     if (!d) return RA_ERR_INVALID_ARG;
     if (d->T < 0 || d->n_seqs < 1 || d->H_kv < 1 || d->D < 1 || d->num_pages < 1 ||
@@ -233,7 +272,123 @@ ra_status check_paged(const ra_paged_desc* d, int* elem, ull* page_elems, Dim (&
         return RA_ERR_MISALIGNED;
     if (d->table_stride < d->max_pages) return RA_ERR_INVALID_ARG;
     *elem = d->dtype == RA_BF16 ? 2 : 4;
-    return page_extent(d, *elem, page_elems, dims);
+    return page_extent(d, layers, layer_stride, *elem, page_elems, dims);
+}
+
+struct Span {
+    const void* base;
+    ull bytes;
+};
+
+// The checks of a pool and a page table with it, and their part of the kernels' arguments.
+ra_status pool_args(const ra_page_pool* pool, const int* lens, int* page_table, int max_pages,
+                    long long table_stride, int page_size, ra::ReserveArgs* r)
+{
+    if (!pool || !pool->free_pages || !pool->held || !pool->state || !lens || !page_table)
+        return RA_ERR_INVALID_ARG;
+    if (pool->num_pages < 1 || pool->n_seqs < 1 || max_pages < 1 || page_size < 1) return RA_ERR_INVALID_ARG;
+    if (pool->n_seqs > ra::kPoolSeqs || pool->num_pages > 0x7fffffff - 1024) return RA_ERR_UNSUPPORTED;
+    if (table_stride < max_pages || table_stride >= static_cast<long long>(kMaxElems)) return RA_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(pool->free_pages), static_cast<const void*>(pool->held),
+                          static_cast<const void*>(pool->state), static_cast<const void*>(lens),
+                          static_cast<const void*>(page_table)})
+        if (!aligned(p, 4)) return RA_ERR_MISALIGNED;
+    ra::PoolArgs& a = r->pool;
+    a.free_pages = pool->free_pages;
+    a.held = pool->held;
+    a.state = pool->state;
+    a.page_table = page_table;
+    a.table_stride = table_stride;
+    a.table_elems = (pool->n_seqs - 1ll) * table_stride + max_pages;
+    a.num_pages = pool->num_pages;
+    a.n_seqs = pool->n_seqs;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    return RA_OK;
+}
+
+// paged_attn_fwd, and paged_attn_tree_fwd with the new tokens' masks.
+ra_status attn_impl(const ra_paged_desc* d, const int* masks, int mask_words, long long mask_stride,
+                    const void* q, long long q_stride, const void* k_pages, const void* v_pages,
+                    void* out, float* lse, void* workspace, unsigned long long workspace_bytes,
+                    ra_stream_t stream)
+{
+    int elem = 0;
+    ull page_elems = 0;
+    Dim dims[4];
+    ra_status st = check_paged(d, &elem, &page_elems, dims);
+    if (st != RA_OK) return st;
+    const ull need = paged_attn_workspace_bytes(d->D, d->dtype);
+    if (need == 0) return RA_ERR_UNSUPPORTED;
+    if (!q || !k_pages || !v_pages || !out || !workspace) return RA_ERR_INVALID_ARG;
+    if (d->H < 1) return RA_ERR_INVALID_ARG;
+    if (d->H % d->H_kv != 0) return RA_ERR_NOT_DIVISIBLE;
+    const long long nq = static_cast<long long>(d->H) * d->D;
+    if (nq > 0x7fffffffll || static_cast<ull>(d->T) * nq >= kMaxElems ||
+        static_cast<ull>(d->T) * d->H > 0x7fffff00ull)
+        return RA_ERR_INVALID_ARG;
+    if ((st = row_stride(&q_stride, nq, elem)) != RA_OK) return st;
+    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
+        !aligned(lse, 4) || !aligned(workspace, 256))
+        return RA_ERR_MISALIGNED;
+    if (workspace_bytes < need) return RA_ERR_INVALID_ARG;
+    const ull n = static_cast<ull>(d->T), pb = page_elems * elem;
+    const ull ob = n * nq * elem, lb = lse ? n * d->H * 4 : 0;
+    const ull table_elems = (d->n_seqs - 1ull) * d->table_stride + d->max_pages;
+    const Rows rq{q, n, static_cast<ull>(nq) * elem, static_cast<ull>(q_stride) * elem};
+    const long long mask_elems = masks && n > 0 ? (static_cast<long long>(n) - 1) * mask_stride + mask_words : 0;
+    if (mask_elems >= static_cast<long long>(kMaxElems)) return RA_ERR_INVALID_ARG;
+    const void* ins[7] = {q, k_pages, v_pages, d->page_table, d->cu_new, d->kv_lens, masks};
+    const ull in_bytes[7] = {rq.span(), pb, pb, 4 * table_elems, 4ull * d->n_seqs + 4, 4ull * d->n_seqs,
+                             4ull * mask_elems};
+    for (int i = 0; i < 7; ++i)
+        if (overlap(out, ob, ins[i], in_bytes[i]) || overlap(lse, lb, ins[i], in_bytes[i]) ||
+            overlap(workspace, need, ins[i], in_bytes[i]))
+            return RA_ERR_INVALID_ARG;
+    if (overlap(out, ob, lse, lb) || overlap(out, ob, workspace, need) ||
+        overlap(lse, lb, workspace, need))
+        return RA_ERR_INVALID_ARG;
+    if (d->T == 0) return RA_OK;
+    ra::PagedArgs a{};
+    a.q = q;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.q_stride = q_stride;
+    a.q_elems = (static_cast<long long>(d->T) - 1) * q_stride + nq;
+    a.page_elems = static_cast<long long>(page_elems);
+    a.out_elems = static_cast<long long>(n) * nq;
+    a.lse_elems = static_cast<long long>(n) * d->H;
+    a.table_elems = static_cast<long long>(table_elems);
+    a.page_stride = d->page_stride;
+    a.token_stride = d->token_stride;
+    a.head_stride = d->head_stride;
+    a.table_stride = d->table_stride;
+    a.T = d->T;
+    a.n_seqs = d->n_seqs;
+    a.H = d->H;
+    a.H_kv = d->H_kv;
+    a.D = d->D;
+    a.elem = elem;
+    // a tree's rows may see any of the new tokens: their tiles run to the last key
+    a.causal = d->causal && !masks ? 1 : 0;
+    a.masks = masks;
+    a.mask_words = mask_words;
+    a.mask_stride = mask_stride;
+    a.mask_elems = mask_elems;
+    a.num_pages = d->num_pages;
+    a.page_size = d->page_size;
+    a.max_pages = d->max_pages;
+    a.cu_new = d->cu_new;
+    a.kv_lens = d->kv_lens;
+    a.page_table = d->page_table;
+    a.timeout_ns = kWaitLimitNs;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    st = ra::current_status_word(&a.status);
+    if (st != RA_OK) return st;
+    return from_cuda(ra::launch_paged(a));
 }
 
 }  // namespace
@@ -319,9 +474,18 @@ ra_status paged_kv_append(const ra_paged_desc* d, const ra_rope* rope, const voi
                           long long v_stride, void* q_out, long long q_out_stride, void* k_pages,
                           void* v_pages, ra_stream_t stream)
 {
+    return paged_kv_append_ex(d, rope, nullptr, nullptr, q, q_stride, k, k_stride, v, v_stride, q_out,
+                              q_out_stride, k_pages, v_pages, stream);
+}
+
+ra_status paged_kv_append_ex(const ra_paged_desc* d, const ra_rope* rope, const ra_head_norm* norm,
+                             const int* positions, const void* q, long long q_stride, const void* k,
+                             long long k_stride, const void* v, long long v_stride, void* q_out,
+                             long long q_out_stride, void* k_pages, void* v_pages, ra_stream_t stream)
+{
     int elem = 0;
     ull page_elems = 0;
-    Dim dims[3];
+    Dim dims[4];
     ra_status st = check_paged(d, &elem, &page_elems, dims);
     if (st != RA_OK) return st;
     if ((d->D * elem) % 16 != 0 || d->D > 256) return RA_ERR_UNSUPPORTED;
@@ -355,15 +519,20 @@ ra_status paged_kv_append(const ra_paged_desc* d, const ra_rope* rope, const voi
         for (const Rows& r : {rq, rqo, rk, rv})
             if (overlap(pages, pb, r.base, r.span())) return RA_ERR_INVALID_ARG;
     if (pages_overlap(k_pages, v_pages, dims, d->D, page_elems, elem)) return RA_ERR_INVALID_ARG;
-    const void* ins[4] = {d->page_table, d->cu_new, d->kv_lens, rope ? rope->phases : nullptr};
-    const ull in_bytes[4] = {4 * table_elems, 4ull * d->n_seqs + 4, 4ull * d->n_seqs,
-                             rope ? 4ull * rope->rot_dim : 0};
-    for (int i = 0; i < 4; ++i)
+    if (!aligned(positions, 4)) return RA_ERR_MISALIGNED;
+    const void* ins[5] = {d->page_table, d->cu_new, d->kv_lens, rope ? rope->phases : nullptr, positions};
+    const ull in_bytes[5] = {4 * table_elems, 4ull * d->n_seqs + 4, 4ull * d->n_seqs,
+                             rope ? 4ull * rope->rot_dim : 0, 4 * n};
+    for (int i = 0; i < 5; ++i)
         if (overlap(k_pages, pb, ins[i], in_bytes[i]) || overlap(v_pages, pb, ins[i], in_bytes[i]) ||
             overlap(q_out, rqo.span(), ins[i], in_bytes[i]))
             return RA_ERR_INVALID_ARG;
+    ra::NormArgs args{};
+    void* const outs[3] = {q_out, k_pages, v_pages};
+    const ull out_bytes[3] = {rqo.span(), pb, pb};
+    if (norm && (st = norm_args(norm, d->D, outs, out_bytes, 3, &args)) != RA_OK) return st;
     if (d->T == 0) return RA_OK;
-    ra::RopeArgs a{};
+    ra::RopeArgs& a = args.rope;
     a.paged = 1;
     a.rows = d->T;
     a.L = d->T;
@@ -393,6 +562,7 @@ ra_status paged_kv_append(const ra_paged_desc* d, const ra_rope* rope, const voi
     a.sign = 1.f;
     a.phases = rope ? rope->phases : nullptr;
     a.layout = RA_LAYOUT_PACKED;
+    a.positions = positions;
     a.cu_seqlens = d->cu_new;
     a.n_seqs = d->n_seqs;
     a.kv_lens = d->kv_lens;
@@ -408,7 +578,7 @@ ra_status paged_kv_append(const ra_paged_desc* d, const ra_rope* rope, const voi
     a.stream = reinterpret_cast<cudaStream_t>(stream);
     st = ra::current_status_word(&a.status);
     if (st != RA_OK) return st;
-    return from_cuda(ra::launch_rope(a));
+    return from_cuda(norm ? ra::launch_norm(args, false) : ra::launch_rope(a));
 }
 
 unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype)
@@ -423,74 +593,215 @@ ra_status paged_attn_fwd(const ra_paged_desc* d, const void* q, long long q_stri
                          const void* k_pages, const void* v_pages, void* out, float* lse,
                          void* workspace, unsigned long long workspace_bytes, ra_stream_t stream)
 {
+    return attn_impl(d, nullptr, 0, 0, q, q_stride, k_pages, v_pages, out, lse, workspace,
+                     workspace_bytes, stream);
+}
+
+ra_status paged_attn_tree_fwd(const ra_paged_desc* d, const int* masks, int mask_words,
+                              long long mask_stride, const void* q, long long q_stride,
+                              const void* k_pages, const void* v_pages, void* out, float* lse,
+                              void* workspace, unsigned long long workspace_bytes, ra_stream_t stream)
+{
+    if (!masks || mask_words < 1) return RA_ERR_INVALID_ARG;
+    if (!aligned(masks, 4)) return RA_ERR_MISALIGNED;
+    if (mask_stride == 0) mask_stride = mask_words;
+    if (mask_stride < mask_words || mask_stride >= static_cast<long long>(kMaxElems)) return RA_ERR_INVALID_ARG;
+    return attn_impl(d, masks, mask_words, mask_stride, q, q_stride, k_pages, v_pages, out, lse, workspace,
+                     workspace_bytes, stream);
+}
+
+unsigned long long qk_norm_workspace_bytes(void) { return 256 + 2048ull * ra::kNormCtas; }
+
+ra_status qk_norm_rope_fwd(const ra_rope_desc* desc, const ra_rope* rope, const ra_head_norm* norm,
+                           const void* q, const void* k, void* q_out, void* k_out, ra_stream_t stream)
+{
+    ra::NormArgs n{};
+    ra_status st = rope_args(desc, rope, true, q, k, q_out, k_out, 1.f, stream, &n.rope);
+    if (st != RA_OK) return st;
+    void* const outs[2] = {q_out, k_out};
+    const ull bytes[2] = {static_cast<ull>(n.rope.q_out_elems) * n.rope.elem,
+                          static_cast<ull>(n.rope.k_out_elems) * n.rope.elem};
+    st = norm_args(norm, n.rope.D, outs, bytes, 2, &n);
+    if (st == RA_OK) st = ra::current_status_word(&n.rope.status);
+    return st != RA_OK ? st : from_cuda(ra::launch_norm(n, false));
+}
+
+ra_status qk_norm_rope_bwd(const ra_rope_desc* desc, const ra_rope* rope, const ra_head_norm* norm,
+                           const void* q, const void* k, const void* dq_out, long long dq_out_stride,
+                           const void* dk_out, long long dk_out_stride, void* dq, void* dk,
+                           float* dq_weight, float* dk_weight, void* workspace,
+                           unsigned long long workspace_bytes, ra_stream_t stream)
+{
+    ra::NormArgs n{};
+    ra_status st = rope_args(desc, rope, true, q, k, dq, dk, 1.f, stream, &n.rope);
+    if (st != RA_OK) return st;
+    ra::RopeArgs& a = n.rope;
+    const long long nq = static_cast<long long>(a.H) * a.D, nk = static_cast<long long>(a.H_kv) * a.D;
+    if ((nq > 0) != (dq_out != nullptr) || (nk > 0) != (dk_out != nullptr) || (!nq && dq_weight) ||
+        (!nk && dk_weight) || !workspace || workspace_bytes < qk_norm_workspace_bytes())
+        return RA_ERR_INVALID_ARG;
+    if (nq > 0 && (st = row_stride(&dq_out_stride, nq, a.elem)) != RA_OK) return st;
+    if (nk > 0 && (st = row_stride(&dk_out_stride, nk, a.elem)) != RA_OK) return st;
+    if (!aligned(dq_out, 16) || !aligned(dk_out, 16) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4) ||
+        !aligned(workspace, 256))
+        return RA_ERR_MISALIGNED;
+    const ull r = static_cast<ull>(a.rows), e = static_cast<ull>(a.elem);
+    const Rows rx[2] = {{q, nq ? r : 0, nq * e, a.q_stride * e}, {k, nk ? r : 0, nk * e, a.k_stride * e}};
+    const Rows ry[2] = {{dq_out, nq ? r : 0, nq * e, dq_out_stride * e},
+                        {dk_out, nk ? r : 0, nk * e, dk_out_stride * e}};
+    const Rows rd[2] = {{dq, nq ? r : 0, nq * e, a.q_out_stride * e}, {dk, nk ? r : 0, nk * e, a.k_out_stride * e}};
+    // over its own upstream gradient a gradient may be written, over nothing else of them
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (!(i == j && rd[i].base == ry[j].base && rd[i].stride == ry[j].stride) && overlap(rd[i], ry[j]))
+                return RA_ERR_INVALID_ARG;
+    void* const outs[5] = {dq_weight, dk_weight, workspace, dq, dk};
+    const ull bytes[5] = {dq_weight ? 4ull * a.D : 0, dk_weight ? 4ull * a.D : 0, qk_norm_workspace_bytes(),
+                          rd[0].span(), rd[1].span()};
+    for (int i = 0; i < 3; ++i) {
+        for (const Rows* x : {rx, rx + 1, ry, ry + 1})
+            if (overlap(outs[i], bytes[i], x->base, x->span())) return RA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 5; ++j)
+            if (overlap(outs[i], bytes[i], outs[j], bytes[j])) return RA_ERR_INVALID_ARG;
+        if (overlap(outs[i], bytes[i], a.phases, 4ull * a.rot) || overlap(outs[i], bytes[i], a.positions, 4 * r) ||
+            overlap(outs[i], bytes[i], a.cu_seqlens, a.cu_seqlens ? 4ull * a.n_seqs + 4 : 0))
+            return RA_ERR_INVALID_ARG;
+    }
+    if ((st = norm_args(norm, a.D, outs, bytes, 5, &n)) != RA_OK) return st;
+    n.dq_out = dq_out;
+    n.dk_out = dk_out;
+    n.dq_out_stride = dq_out_stride;
+    n.dk_out_stride = dk_out_stride;
+    n.dq_out_elems = nq ? (a.rows - 1) * dq_out_stride + nq : 0;
+    n.dk_out_elems = nk ? (a.rows - 1) * dk_out_stride + nk : 0;
+    n.dq_weight = dq_weight;
+    n.dk_weight = dk_weight;
+    n.ticket = static_cast<unsigned int*>(workspace);
+    n.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
+    st = ra::current_status_word(&a.status);
+    return st != RA_OK ? st : from_cuda(ra::launch_norm(n, true));
+}
+
+ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int* lens, int* page_table,
+                        int max_pages, long long table_stride, int page_size, int T, int* cu_new,
+                        int* kv_lens, int* positions, long long* slots, const int* parents, int* masks,
+                        int mask_words, ra_stream_t stream)
+{
+    ra::ReserveArgs r{};
+    ra_status st = pool_args(pool, lens, page_table, max_pages, table_stride, page_size, &r);
+    if (st != RA_OK) return st;
+    const ull n = static_cast<ull>(pool->n_seqs), t = static_cast<ull>(std::max(T, 0));
+    if (!new_lens || !cu_new || !kv_lens || T < 0 || mask_words < 0 || (mask_words > 0) != (masks != nullptr) ||
+        (masks && !parents) || t * static_cast<ull>(mask_words) >= kMaxElems)
+        return RA_ERR_INVALID_ARG;
+    if (T > 0x7fffffff - 1024) return RA_ERR_UNSUPPORTED;
+    for (const void* p : {static_cast<const void*>(new_lens), static_cast<const void*>(cu_new),
+                          static_cast<const void*>(kv_lens), static_cast<const void*>(positions),
+                          static_cast<const void*>(parents), static_cast<const void*>(masks)})
+        if (!aligned(p, 4)) return RA_ERR_MISALIGNED;
+    if (!aligned(slots, 8)) return RA_ERR_MISALIGNED;
+    // what is written, and what is only read; kv_lens may be lens
+    const Span outs[9] = {{cu_new, 4 * n + 4}, {kv_lens, 4 * n}, {positions, positions ? 4 * t : 0},
+                          {slots, slots ? 8 * t : 0}, {masks, masks ? 4 * t * mask_words : 0},
+                          {page_table, 4ull * r.pool.table_elems}, {pool->held, 4 * n}, {pool->state, 12},
+                          {pool->free_pages, 4ull * pool->num_pages}};
+    const Span ins[3] = {{new_lens, 4 * n}, {parents, parents ? 4 * t : 0}, {lens, 4 * n}};
+    for (int i = 0; i < 9; ++i) {
+        for (int j = i + 1; j < 9; ++j)
+            if (overlap(outs[i].base, outs[i].bytes, outs[j].base, outs[j].bytes)) return RA_ERR_INVALID_ARG;
+        for (int j = 0; j < 3; ++j)
+            if (!(i == 1 && j == 2 && kv_lens == lens) &&
+                overlap(outs[i].base, outs[i].bytes, ins[j].base, ins[j].bytes))
+                return RA_ERR_INVALID_ARG;
+    }
+    r.new_lens = new_lens;
+    r.lens = lens;
+    r.cu_new = cu_new;
+    r.kv_lens = kv_lens;
+    r.positions = positions;
+    r.slots = slots;
+    r.parents = parents;
+    r.masks = masks;
+    r.T = T;
+    r.mask_words = mask_words;
+    r.stream = reinterpret_cast<cudaStream_t>(stream);
+    st = ra::current_status_word(&r.pool.status);
+    return st != RA_OK ? st : from_cuda(ra::launch_reserve(r));
+}
+
+ra_status paged_release(const ra_page_pool* pool, const int* lens, int* page_table, int max_pages,
+                        long long table_stride, int page_size, ra_stream_t stream)
+{
+    ra::ReserveArgs r{};
+    ra_status st = pool_args(pool, lens, page_table, max_pages, table_stride, page_size, &r);
+    if (st != RA_OK) return st;
+    const ull n = static_cast<ull>(pool->n_seqs);
+    const Span all[5] = {{page_table, 4ull * r.pool.table_elems}, {pool->held, 4 * n}, {pool->state, 12},
+                         {pool->free_pages, 4ull * pool->num_pages}, {lens, 4 * n}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < 5; ++j)
+            if (overlap(all[i].base, all[i].bytes, all[j].base, all[j].bytes)) return RA_ERR_INVALID_ARG;
+    r.lens = lens;
+    r.stream = reinterpret_cast<cudaStream_t>(stream);
+    st = ra::current_status_word(&r.pool.status);
+    return st != RA_OK ? st : from_cuda(ra::launch_release(r));
+}
+
+ra_status paged_kv_keep(const ra_paged_desc* d, const int* kept, int width, long long kept_stride, int layers,
+                        long long layer_stride, void* k_pages, void* v_pages, int* lens, ra_stream_t stream)
+{
     int elem = 0;
     ull page_elems = 0;
-    Dim dims[3];
-    ra_status st = check_paged(d, &elem, &page_elems, dims);
+    Dim dims[4];
+    if (layers < 1) return RA_ERR_INVALID_ARG;
+    const ra_status st = check_paged(d, &elem, &page_elems, dims, layers, layers > 1 ? layer_stride : 0);
     if (st != RA_OK) return st;
-    const ull need = paged_attn_workspace_bytes(d->D, d->dtype);
-    if (need == 0) return RA_ERR_UNSUPPORTED;
-    if (!q || !k_pages || !v_pages || !out || !workspace) return RA_ERR_INVALID_ARG;
-    if (d->H < 1) return RA_ERR_INVALID_ARG;
-    if (d->H % d->H_kv != 0) return RA_ERR_NOT_DIVISIBLE;
-    const long long nq = static_cast<long long>(d->H) * d->D;
-    if (nq > 0x7fffffffll || static_cast<ull>(d->T) * nq >= kMaxElems ||
-        static_cast<ull>(d->T) * d->H > 0x7fffff00ull)
-        return RA_ERR_INVALID_ARG;
-    if ((st = row_stride(&q_stride, nq, elem)) != RA_OK) return st;
-    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
-        !aligned(lse, 4) || !aligned(workspace, 256))
+    if ((d->D * elem) % 16 != 0) return RA_ERR_UNSUPPORTED;
+    if (!kept || !k_pages || !v_pages || !lens || width < 1) return RA_ERR_INVALID_ARG;
+    if (kept_stride == 0) kept_stride = width;
+    if (kept_stride < width || kept_stride >= static_cast<long long>(kMaxElems)) return RA_ERR_INVALID_ARG;
+    if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(kept, 4) || !aligned(lens, 4))
         return RA_ERR_MISALIGNED;
-    if (workspace_bytes < need) return RA_ERR_INVALID_ARG;
-    const ull n = static_cast<ull>(d->T), pb = page_elems * elem;
-    const ull ob = n * nq * elem, lb = lse ? n * d->H * 4 : 0;
-    const ull table_elems = (d->n_seqs - 1ull) * d->table_stride + d->max_pages;
-    const Rows rq{q, n, static_cast<ull>(nq) * elem, static_cast<ull>(q_stride) * elem};
-    const void* ins[6] = {q, k_pages, v_pages, d->page_table, d->cu_new, d->kv_lens};
-    const ull in_bytes[6] = {rq.span(), pb, pb, 4 * table_elems, 4ull * d->n_seqs + 4, 4ull * d->n_seqs};
-    for (int i = 0; i < 6; ++i)
-        if (overlap(out, ob, ins[i], in_bytes[i]) || overlap(lse, lb, ins[i], in_bytes[i]) ||
-            overlap(workspace, need, ins[i], in_bytes[i]))
+    const ull n = static_cast<ull>(d->n_seqs), pb = page_elems * elem;
+    const ull table_elems = (n - 1) * d->table_stride + d->max_pages;
+    const ull kept_elems = (n - 1) * kept_stride + width;
+    if (pages_overlap(k_pages, v_pages, dims, d->D, page_elems, elem)) return RA_ERR_INVALID_ARG;
+    const Span ins[4] = {{kept, 4 * kept_elems}, {d->page_table, 4 * table_elems}, {d->cu_new, 4 * n + 4},
+                         {d->kv_lens, 4 * n}};
+    for (const Span& x : ins)
+        if (overlap(k_pages, pb, x.base, x.bytes) || overlap(v_pages, pb, x.base, x.bytes) ||
+            overlap(lens, 4 * n, x.base, x.bytes))
             return RA_ERR_INVALID_ARG;
-    if (overlap(out, ob, lse, lb) || overlap(out, ob, workspace, need) ||
-        overlap(lse, lb, workspace, need))
-        return RA_ERR_INVALID_ARG;
-    if (d->T == 0) return RA_OK;
-    ra::PagedArgs a{};
-    a.q = q;
+    if (overlap(lens, 4 * n, k_pages, pb) || overlap(lens, 4 * n, v_pages, pb)) return RA_ERR_INVALID_ARG;
+    ra::KeepArgs a{};
     a.k_pages = k_pages;
     a.v_pages = v_pages;
-    a.out = out;
-    a.lse = lse;
-    a.workspace = workspace;
-    a.q_stride = q_stride;
-    a.q_elems = (static_cast<long long>(d->T) - 1) * q_stride + nq;
-    a.page_elems = static_cast<long long>(page_elems);
-    a.out_elems = static_cast<long long>(n) * nq;
-    a.lse_elems = static_cast<long long>(n) * d->H;
-    a.table_elems = static_cast<long long>(table_elems);
     a.page_stride = d->page_stride;
     a.token_stride = d->token_stride;
     a.head_stride = d->head_stride;
+    a.layer_stride = layers > 1 ? layer_stride : 0;
     a.table_stride = d->table_stride;
-    a.T = d->T;
+    a.page_elems = static_cast<long long>(page_elems);
+    a.table_elems = static_cast<long long>(table_elems);
+    a.kept_elems = static_cast<long long>(kept_elems);
+    a.kept_stride = kept_stride;
+    a.layers = layers;
     a.n_seqs = d->n_seqs;
-    a.H = d->H;
     a.H_kv = d->H_kv;
     a.D = d->D;
     a.elem = elem;
-    a.causal = d->causal ? 1 : 0;
     a.num_pages = d->num_pages;
     a.page_size = d->page_size;
     a.max_pages = d->max_pages;
+    a.width = width;
+    a.kept = kept;
+    a.page_table = d->page_table;
     a.cu_new = d->cu_new;
     a.kv_lens = d->kv_lens;
-    a.page_table = d->page_table;
-    a.timeout_ns = kWaitLimitNs;
+    a.lens = lens;
     a.stream = reinterpret_cast<cudaStream_t>(stream);
-    st = ra::current_status_word(&a.status);
-    if (st != RA_OK) return st;
-    return from_cuda(ra::launch_paged(a));
+    const ra_status word = ra::current_status_word(&a.status);
+    return word != RA_OK ? word : from_cuda(ra::launch_keep(a));
 }
 
 }  // extern "C"

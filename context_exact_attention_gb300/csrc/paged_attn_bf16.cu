@@ -85,7 +85,8 @@ __device__ __forceinline__ uint32_t below(float x)
     return static_cast<uint32_t>(__viaddmax_s32(__float_as_int(x), -1, 0));
 }
 
-template <int D>
+// kTree: rows see the new tokens that their masks name.
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_constant__ PagedParams p)
 {
     using S = Smem<D>;
@@ -193,7 +194,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         // keys that this thread's two rows see, and that every row of the tile sees
+        // (of a tree: the keys from before the step)
         auto seen_by = [&](int r) {
+            if (kTree) return t.s.kv - t.s.n;
             const int tok = p.token_of(t.row0 + r);
             return a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
         };
@@ -223,7 +226,22 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
                 }
             }
             const int k0w = k + kKeysW * warp;
-            if (k0w + kKeysW > see_all) {
+            if (kTree && k0w + kKeysW > see_all) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = (lane >> 2) + 8 * h;
+                    unsigned seen = 0;
+                    if (r < t.rows)
+                        seen = seen_from(p, t.s.first + p.token_of(t.row0 + r), k0w - (t.s.kv - t.s.n));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int in = 8 * i + 2 * (lane & 3) + j;
+                            if (!(seen >> in & 1) || k0w + in >= t.k1) s[i][2 * h + j] = -INFINITY;
+                        }
+                }
+            } else if (k0w + kKeysW > see_all) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -347,14 +365,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_bf16_kernel(const __grid_co
     cp_async_wait<0>();
 }
 
-template <int D>
+template <int D, bool kTree>
 cudaError_t launch_d(PagedParams& p)
 {
     const PagedArgs& a = p.a;
     static std::atomic<int> known[kMaxDevices];
     int grid = 0;
     const cudaError_t e =
-        resident_ctas(known, paged_bf16_kernel<D>, kThreads, Smem<D>::kBytes, &grid);
+        resident_ctas(known, paged_bf16_kernel<D, kTree>, kThreads, Smem<D>::kBytes, &grid);
     if (e != cudaSuccess) return e;
     // With so few tiles that each would fall into 24 parts or more, one block an SM: it copies
     // nearly as fast as two and halves the joining (one token over 131072 keys of 8 heads 89 us
@@ -379,7 +397,7 @@ cudaError_t launch_d(PagedParams& p)
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
-    return launch_early(paged_bf16_kernel<D>, p.grid, kThreads, Smem<D>::kBytes, a.stream, p);
+    return launch_early(paged_bf16_kernel<D, kTree>, p.grid, kThreads, Smem<D>::kBytes, a.stream, p);
 }
 
 }  // namespace
@@ -388,8 +406,8 @@ cudaError_t launch_paged_bf16(const PagedArgs& a)
 {
     PagedParams p;
     fill_params(&p, a);
-    if (a.D == 64) return launch_d<64>(p);
-    if (a.D == 128) return launch_d<128>(p);
+    if (a.D == 64) return a.masks ? launch_d<64, true>(p) : launch_d<64, false>(p);
+    if (a.D == 128) return a.masks ? launch_d<128, true>(p) : launch_d<128, false>(p);
     return cudaErrorInvalidValue;
 }
 

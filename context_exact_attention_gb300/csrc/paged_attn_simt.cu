@@ -41,7 +41,8 @@ constexpr int kRing = kStages * 2 * kTurn * kVec4 * 32 * 16;
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
-template <int kVec4>
+// kTree: rows see the new tokens that their masks name.
+template <int kVec4, bool kTree>
 __global__ void __launch_bounds__(kThreads, kVec4 == 1 ? 3 : 1) paged_simt_kernel(const __grid_constant__ PagedParams p)
 {
     using Walk = PagedWalk<FlatTiles<kRows>, kUnit>;
@@ -150,10 +151,12 @@ __global__ void __launch_bounds__(kThreads, kVec4 == 1 ? 3 : 1) paged_simt_kerne
         const unsigned rows_in = 0x11111111u * ((1u << t.rows) - 1);
         // this lane's score is of row lane & 3: the keys it sees are [0, seen)
         const int my_row = lane & 3, my_key = lane >> 2;
-        int seen = 0;
+        int seen = 0;                      // (of a tree: those from before the step)
+        int my_token = -1;
         if (my_row < t.rows) {
             const int tok = p.token_of(t.row0 + my_row);
-            seen = a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
+            my_token = t.s.first + tok;
+            seen = kTree ? t.s.kv - t.s.n : a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
         }
         float m = -INFINITY, l = 0.f;      // of row my_row; l over this lane's keys only
         for (int k = t.k0 + kTurn * warp; k - kTurn * warp < t.k1; k += kUnit) {
@@ -200,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, kVec4 == 1 ? 3 : 1) paged_simt_kerne
                 }
             }
             const int key = k + my_key;
-            const bool sees = key < seen && key < t.k1;
+            bool sees = key < seen && key < t.k1;
+            if (kTree && key >= seen && key < t.k1 && my_token >= 0)
+                sees = seen_from(p, my_token, key - seen) & 1;
             const unsigned vis = __ballot_sync(0xffffffffu, sees);
             const float x = sees ? s[0] * p.scale_log2 : -INFINITY;
             float mx = x;
@@ -294,10 +299,14 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
 {
     PagedParams p;
     fill_params(&p, a);
-    static std::atomic<int> known1[kMaxDevices], known2[kMaxDevices];
+    static std::atomic<int> known[4][kMaxDevices];
+    const int which = (a.D <= 128 ? 0 : 2) + (a.masks ? 1 : 0);
+    constexpr auto kOne = paged_simt_kernel<1, false>, kOneTree = paged_simt_kernel<1, true>;
+    constexpr auto kTwo = paged_simt_kernel<2, false>, kTwoTree = paged_simt_kernel<2, true>;
+    const auto kernel = a.D <= 128 ? (a.masks ? kOneTree : kOne) : (a.masks ? kTwoTree : kTwo);
+    const int ring = kWarps * (a.D <= 128 ? kRing<1> : kRing<2>);
     int grid = 0;
-    const cudaError_t e = a.D <= 128 ? resident_ctas(known1, paged_simt_kernel<1>, kThreads, kWarps * kRing<1>, &grid)
-                                     : resident_ctas(known2, paged_simt_kernel<2>, kThreads, kWarps * kRing<2>, &grid);
+    const cudaError_t e = resident_ctas(known[which], kernel, kThreads, ring, &grid);
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedMaxCtas ? grid : kPagedMaxCtas;
     p.tile_cost = 64;
@@ -314,9 +323,7 @@ cudaError_t launch_paged_simt(const PagedArgs& a)
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
-    if (a.D <= 128)
-        return launch_early(paged_simt_kernel<1>, p.grid, kThreads, kWarps * kRing<1>, a.stream, p);
-    return launch_early(paged_simt_kernel<2>, p.grid, kThreads, kWarps * kRing<2>, a.stream, p);
+    return launch_early(kernel, p.grid, kThreads, ring, a.stream, p);
 }
 
 }  // namespace ra

@@ -40,7 +40,8 @@ template <int kCols>
 constexpr int kSmem = (3 * kRows * 64 * kCols + kRows * kKeys) * 4;
 
 // kCols: column groups of 64 (D <= 64 kCols; the columns behind D are zeros).
-template <int kCols>
+// kTree: rows see the new tokens that their masks name.
+template <int kCols, bool kTree>
 __global__ void __launch_bounds__(kThreads<kCols>, kCols <= 2 ? 2 : 1)
     paged_rows_kernel(const __grid_constant__ PagedParams p)
 {
@@ -104,7 +105,9 @@ __global__ void __launch_bounds__(kThreads<kCols>, kCols <= 2 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < kR; ++i) {
             const int r = ty + kStep * i, tok = p.token_of(t.row0 + r);
-            end[i] = r >= t.rows ? 0 : min(a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv, t.k1);
+            // (of a tree: those from before the step)
+            const int seen = kTree ? t.s.kv - t.s.n : a.causal ? t.s.kv - t.s.n + tok + 1 : t.s.kv;
+            end[i] = r >= t.rows ? 0 : min(seen, t.k1);
             if (r < t.rows) least = min(least, end[i]);
         }
         uint64_t o[kR][kCols][2];
@@ -153,7 +156,11 @@ __global__ void __launch_bounds__(kThreads<kCols>, kCols <= 2 ? 2 : 1)
                 for (int j = 0; j < 4; ++j) {
                     float lo, hi;
                     f2unpack(acc[i][j], lo, hi);
-                    s[j] = kb + tx + 16 * j < end[i] ? (lo + hi) * p.scale_log2 : -INFINITY;
+                    const int key = kb + tx + 16 * j, r = ty + kStep * i;
+                    bool sees = key < end[i];
+                    if (kTree && key >= end[i] && key < t.k1 && r < t.rows)
+                        sees = seen_from(p, t.s.first + p.token_of(t.row0 + r), key - (t.s.kv - t.s.n)) & 1;
+                    s[j] = sees ? (lo + hi) * p.scale_log2 : -INFINITY;
                     mx = fmaxf(mx, s[j]);
                 }
 #pragma unroll
@@ -239,12 +246,13 @@ __global__ void __launch_bounds__(kThreads<kCols>, kCols <= 2 ? 2 : 1)
     }
 }
 
-template <int kCols>
+template <int kCols, bool kTree>
 cudaError_t launch_cols(PagedParams& p)
 {
+    constexpr auto kernel = paged_rows_kernel<kCols, kTree>;
     static std::atomic<int> known[kMaxDevices];
     int grid = 0;
-    const cudaError_t e = resident_ctas(known, paged_rows_kernel<kCols>, kThreads<kCols>, kSmem<kCols>, &grid);
+    const cudaError_t e = resident_ctas(known, kernel, kThreads<kCols>, kSmem<kCols>, &grid);
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedRowsCtas ? grid : kPagedRowsCtas;
     const PagedWorkspace w = paged_workspace_of(p.grid, kRows, p.a.D);
@@ -252,7 +260,7 @@ cudaError_t launch_cols(PagedParams& p)
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
-    return launch_early(paged_rows_kernel<kCols>, p.grid, kThreads<kCols>, kSmem<kCols>, p.a.stream, p);
+    return launch_early(kernel, p.grid, kThreads<kCols>, kSmem<kCols>, p.a.stream, p);
 }
 
 }  // namespace
@@ -286,10 +294,10 @@ cudaError_t launch_paged_rows(const PagedArgs& a)
     p.min_chunk = 2 * kKeys;
     p.whole = 0;
     p.join_cost = 8;                // (4, 16, 64: 83, 103, 144 us for 64 rows over 8000 keys of 2 heads)
-    if (a.D <= 64) return launch_cols<1>(p);
-    if (a.D <= 128) return launch_cols<2>(p);
-    if (a.D <= 192) return launch_cols<3>(p);
-    return launch_cols<4>(p);
+    if (a.D <= 64) return a.masks ? launch_cols<1, true>(p) : launch_cols<1, false>(p);
+    if (a.D <= 128) return a.masks ? launch_cols<2, true>(p) : launch_cols<2, false>(p);
+    if (a.D <= 192) return a.masks ? launch_cols<3, true>(p) : launch_cols<3, false>(p);
+    return a.masks ? launch_cols<4, true>(p) : launch_cols<4, false>(p);
 }
 
 }  // namespace ra

@@ -153,7 +153,8 @@ __device__ __forceinline__ bool consume(volatile int* e, Seg& s)
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
 
-template <int D>
+// kTree: rows see the new tokens that their masks name.
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     const __grid_constant__ CUtensorMap tmap_k,
@@ -569,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = row < sub_rows && in_tile < s.rows;
             const int tok = p.token_of(s.row0 + in_tile);            // within the sequence
             // keys that this row sees: [0, seen)
-            const int seen = !valid ? 0 : a.causal ? s.kv - s.n + tok + 1 : s.kv;
+            // (of a tree: those from before the step)
+            const int seen = !valid ? 0 : kTree ? s.kv - s.n : a.causal ? s.kv - s.n + tok + 1 : s.kv;
             const int n_blocks = single ? (s.n_blocks + 1 - tq) / 2 : s.n_blocks;
 
             float m = -INFINITY, l = 0.f;
@@ -586,8 +588,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float sv[128];
 #pragma unroll
                 for (int c = 0; c < 128; ++c) sv[c] = u2f(sraw[c]);
-                const int lim = seen - (first_key + n * stride);   // columns [0, lim) are seen
-                if (lim < kKeys) {
+                const int kb = first_key + n * stride;
+                const int lim = seen - kb;                     // columns [0, lim) are seen
+                if (kTree && lim < kKeys) {
+                    // of the new tokens, from column lim on, what the row's mask names
+                    unsigned bits[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int left = s.kv - (kb + 32 * w);       // keys that there are
+                        bits[w] = 0;
+                        if (valid && left > 0)
+                            bits[w] = seen_from(p, s.first + tok, 32 * w - lim) &
+                                      (left < 32 ? (1u << left) - 1 : 0xffffffffu);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) sv[c] = bits[c >> 5] >> (c & 31) & 1 ? sv[c] : -INFINITY;
+                } else if (lim < kKeys) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c) sv[c] = c >= lim ? -INFINITY : sv[c];
                 }
@@ -799,13 +815,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool kTree>
 cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv)
 {
     static std::atomic<int> known[kMaxDevices];
     int grid = 0;
-    const cudaError_t e = resident_ctas(known, paged_tc_kernel<D>, kThreads, Layout<D>::kSmem, &grid);
+    const cudaError_t e = resident_ctas(known, paged_tc_kernel<D, kTree>, kThreads, Layout<D>::kSmem, &grid);
     if (e != cudaSuccess) return e;
     p.grid = grid < kPagedTcCtas ? grid : kPagedTcCtas;
     // a block of a single sub-tile takes half the time of a double one at head dim 64 (1500
@@ -831,7 +847,7 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part_stat = reinterpret_cast<float*>(ws + w.stat);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
-    return launch_early(paged_tc_kernel<D>, p.grid, kThreads, Layout<D>::kSmem, p.a.stream, tq, tk, tv, p);
+    return launch_early(paged_tc_kernel<D, kTree>, p.grid, kThreads, Layout<D>::kSmem, p.a.stream, tq, tk, tv, p);
 }
 
 }  // namespace
@@ -882,8 +898,8 @@ cudaError_t launch_paged_tc(const PagedArgs& a)
     if (!encode_bf16_map(&tq, a.q, 3, qd, qs, qb) || !encode_bf16_map(&tk, a.k_pages, 4, kd, ks, kb) ||
         !encode_bf16_map(&tv, a.v_pages, 4, kd, ks, kb))
         return cudaErrorInvalidValue;
-    if (a.D == 64) return launch_d<64>(p, tq, tk, tv);
-    if (a.D == 128) return launch_d<128>(p, tq, tk, tv);
+    if (a.D == 64) return a.masks ? launch_d<64, true>(p, tq, tk, tv) : launch_d<64, false>(p, tq, tk, tv);
+    if (a.D == 128) return a.masks ? launch_d<128, true>(p, tq, tk, tv) : launch_d<128, false>(p, tq, tk, tv);
     return cudaErrorInvalidValue;
 }
 

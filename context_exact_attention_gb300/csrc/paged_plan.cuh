@@ -587,6 +587,21 @@ __device__ void finish_segment(const PagedParams& p, const Segment& seg, const f
     __syncthreads();
 }
 
+// Trees of drafted tokens (a.masks): which of the new tokens node .. node + 31 of its sequence a
+// row sees, a bit each; what lies before node 0 are keys from before the step, which all rows see.
+// row: its index in the call.
+__device__ __forceinline__ unsigned seen_from(const PagedParams& p, int row, int node)
+{
+    const PagedArgs& a = p.a;
+    auto word = [&](int w) -> unsigned {
+        if (w >= a.mask_words) return 0u;
+        return static_cast<unsigned>(checked_ldg(a.masks, row * a.mask_stride + w, a.mask_elems, a.status));
+    };
+    if (node <= -32) return 0xffffffffu;
+    if (node < 0) return word(0) << -node | ((1u << -node) - 1);
+    return __funnelshift_r(word(node >> 5), word((node >> 5) + 1), node & 31);
+}
+
 // Asynchronous 16-byte copies into shared memory.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real)
 {

@@ -218,6 +218,74 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a);
 
+// The same with a norm of every head before the rotation (qk_norm_rope_fwd, _bwd, and the
+// paged append with weights).
+struct NormArgs {
+    RopeArgs rope;                 // backward: q, k the inputs, q_out, k_out their gradients
+    const void* q_weight;          // [D] each, or null: ones
+    const void* k_weight;
+    int weight_elem;               // bytes
+    float eps, weight_offset;
+    // backward: gradients of the outputs, and of the weights (or null)
+    const void* dq_out;
+    const void* dk_out;
+    long long dq_out_stride, dk_out_stride, dq_out_elems, dk_out_elems;
+    float* dq_weight;
+    float* dk_weight;
+    float* partials;               // [kNormCtas][2][256]
+    unsigned int* ticket;          // zero between calls
+    int lanes;                     // of a head vector, a power of two (set by the launch)
+    int items;                     // of them, those that hold some of it (set by the launch)
+};
+constexpr int kNormCtas = 640;     // of the backward
+cudaError_t launch_norm(const NormArgs& a, bool backward);
+
+// The pool of pages (paged_reserve, paged_release).
+struct PoolArgs {
+    int* free_pages;               // [num_pages], a stack
+    int* held;                     // [n_seqs]
+    int* state;                    // free pages, block counter, status of the last reserve
+    int* page_table;
+    long long table_stride, table_elems;
+    int num_pages, n_seqs, max_pages, page_size;
+    unsigned int* status;
+};
+constexpr int kPoolSeqs = 8192;    // sequences (their sums lie in shared memory)
+struct ReserveArgs {
+    PoolArgs pool;
+    const int* new_lens;
+    const int* lens;
+    int* cu_new;
+    int* kv_lens;
+    int* positions;                // these four may be null
+    long long* slots;
+    const int* parents;
+    int* masks;
+    int T, mask_words;
+    cudaStream_t stream;
+};
+cudaError_t launch_reserve(const ReserveArgs& r);
+cudaError_t launch_release(const ReserveArgs& r);
+
+// Accepted tokens to the front of a step's slots (paged_kv_keep).
+struct KeepArgs {
+    void* k_pages;
+    void* v_pages;
+    long long page_stride, token_stride, head_stride, layer_stride, table_stride;
+    long long page_elems, table_elems, kept_elems, kept_stride;
+    int layers, n_seqs, H_kv, D, elem, num_pages, page_size, max_pages, width;
+    const int* kept;
+    const int* page_table;
+    const int* cu_new;
+    const int* kv_lens;
+    int* lens;
+    long long columns;             // 16-byte columns of a token over all layers (by the launch)
+    int pieces;                    // blocks of a sequence (by the launch)
+    unsigned int* status;
+    cudaStream_t stream;
+};
+cudaError_t launch_keep(const KeepArgs& a);
+
 // Attention over a paged cache (paged_attn_fwd).
 struct PagedArgs {
     const void* q;
@@ -229,6 +297,9 @@ struct PagedArgs {
     long long q_stride;            // elements per token
     long long q_elems, page_elems, out_elems, lse_elems, table_elems;     // extents, for checks
     long long page_stride, token_stride, head_stride, table_stride;
+    const int* masks;              // a drafted tree: bits of the new tokens that a row sees, or null
+    long long mask_stride, mask_elems;
+    int mask_words;
     int T, n_seqs, H, H_kv, D, elem, causal;
     int num_pages, page_size, max_pages;
     const int* cu_new;

@@ -603,6 +603,51 @@ ra_status rope_bwd(const ra_rope_desc* desc, const ra_rope* rope, const void* dq
                    const void* dk_out, void* dq, void* dk, ra_stream_t stream);
 
 /*
+ * Norms of heads.
+ *
+ * Many models normalise every query and key head before its rotation:
+ *   y = R(p) (w x / sqrt(mean(x^2) + eps)),
+ * the mean over the head's D dims, w a weight per dim shared by all heads of q, or of k, R(p)
+ * the rotation of rope_fwd.  One pass does both.
+ *   q_weight, k_weight  DEVICE [D] of weight_dtype, or NULL for ones;
+ *   eps                 finite, >= 0;
+ *   weight_offset       added to the weights given (1 where a model stores them less one).
+ */
+typedef struct {
+    const void* q_weight;
+    const void* k_weight;
+    ra_dtype weight_dtype;
+    float eps, weight_offset;
+} ra_head_norm;
+
+/*
+ * qk_norm_rope_fwd -- q and k normalised by *norm, rotated (rope NULL: normalised only) and
+ * written to q_out and k_out in one launch; layouts, positions, strides, in-place outputs and
+ * errors as rope_fwd.  Everything between the input and the one rounding of the result is fp32.
+ *
+ * qk_norm_rope_bwd -- its gradients.  q, k: the forward's inputs (strides q_stride, k_stride);
+ * dq_out, dk_out: the gradients of its outputs, tokens dq_out_stride, dk_out_stride elements
+ * apart (0: contiguous); dq, dk: those of its inputs (strides q_out_stride, k_out_stride), which
+ * may be written over q, k or dq_out, dk_out (the same rows); dq_weight, dk_weight: fp32 [D],
+ * the sums over all rows and heads, or NULL.  With R^T the rotation back, g = w R^T dy,
+ * u = x / sqrt(mean(x^2) + eps):  dx = (g - u mean(g u)) / sqrt(mean(x^2) + eps),
+ * dw = sum R^T dy u.  Packed rows that no sequence holds are left as they are and add nothing.
+ * No atomics on results: repeated calls give the same bits.  workspace: at least
+ * qk_norm_workspace_bytes() bytes, 256-byte aligned, ZEROED before its first use; every call
+ * leaves it ready for the next, and calls that share one must not overlap on the GPU.
+ * Errors: rope_fwd's, and RA_ERR_INVALID_ARG for an eps or offset that is not finite or a
+ * workspace that is too small, RA_ERR_UNSUPPORTED for the weights' dtype.
+ */
+unsigned long long qk_norm_workspace_bytes(void);
+ra_status qk_norm_rope_fwd(const ra_rope_desc* desc, const ra_rope* rope, const ra_head_norm* norm,
+                           const void* q, const void* k, void* q_out, void* k_out, ra_stream_t stream);
+ra_status qk_norm_rope_bwd(const ra_rope_desc* desc, const ra_rope* rope, const ra_head_norm* norm,
+                           const void* q, const void* k, const void* dq_out, long long dq_out_stride,
+                           const void* dk_out, long long dk_out_stride, void* dq, void* dk,
+                           float* dq_weight, float* dk_weight, void* workspace,
+                           unsigned long long workspace_bytes, ra_stream_t stream);
+
+/*
  * The paged key/value cache (no counterpart on the pages: the serving side of the same
  * attention).
  *
@@ -666,6 +711,17 @@ ra_status paged_kv_append(const ra_paged_desc* desc, const ra_rope* rope, const 
                           void* v_pages, ra_stream_t stream);
 
 /*
+ * paged_kv_append_ex -- the same with a norm of q's and k's heads before the rotation (norm, or
+ * NULL) and given positions (DEVICE int32 [T], or NULL): a row then turns by its entry there,
+ * and is stored where it was before.  A drafted tree's tokens stand behind one another in the
+ * cache but turn by their depth.  Without either it is paged_kv_append.
+ */
+ra_status paged_kv_append_ex(const ra_paged_desc* desc, const ra_rope* rope, const ra_head_norm* norm,
+                             const int* positions, const void* q, long long q_stride, const void* k,
+                             long long k_stride, const void* v, long long v_stride, void* q_out,
+                             long long q_out_stride, void* k_pages, void* v_pages, ra_stream_t stream);
+
+/*
  * paged_attn_workspace_bytes -- device bytes paged_attn_fwd needs for a head dim and type,
  * whatever the lengths (0 for a head dim the type does not have).
  */
@@ -710,6 +766,98 @@ ra_status paged_attn_fwd(const ra_paged_desc* desc, const void* q, long long q_s
                          const void* k_pages, const void* v_pages, void* out, float* lse,
                          void* workspace, unsigned long long workspace_bytes,
                          ra_stream_t stream);
+
+/*
+ * paged_attn_tree_fwd -- paged_attn_fwd for trees of drafted tokens (or any other mask among a
+ * step's new tokens): row i of sequence g sees the kv_lens[g] - n keys before the step, and new
+ * token j of its sequence where bit j % 32 of word j / 32 of its mask is set, itself included
+ * only if its own bit is.  New tokens beyond 32 * mask_words are seen by no row; causal is not
+ * looked at.
+ *
+ * masks: DEVICE int32 [T, mask_words], rows mask_stride entries apart (0: mask_words); rows that
+ * no sequence holds are not read.  paged_reserve writes them from the tokens' parents.
+ * Everything else as paged_attn_fwd, the workspace too.  A value that is not finite, of a new
+ * token of a call with several new tokens per sequence, may in bf16 reach rows of its sequence
+ * that do not see it.  A row that sees nothing gets 0 and -inf.
+ */
+ra_status paged_attn_tree_fwd(const ra_paged_desc* desc, const int* masks, int mask_words,
+                              long long mask_stride, const void* q, long long q_stride,
+                              const void* k_pages, const void* v_pages, void* out, float* lse,
+                              void* workspace, unsigned long long workspace_bytes, ra_stream_t stream);
+
+/*
+ * The pool of pages: which pages of a cache are free, on the device, so that a step's bookkeeping
+ * needs no host and can be captured with the step.
+ *   free_pages  DEVICE int32 [num_pages], a stack: the first state[0] entries are the free pages,
+ *               the last of them is taken first;
+ *   held        DEVICE int32 [n_seqs], pages that every sequence holds: the first held[g] entries
+ *               of its row of the page table;
+ *   state       DEVICE int32 [3]: the number of free pages, a counter of the kernels (zero between
+ *               calls), and how the last paged_reserve ended: 0, or 1 too few free pages, 2 more
+ *               than T new rows, 3 a sequence longer than its row of the table.
+ * Filled by the caller once (every page on the stack, the rest zero) and afterwards changed by
+ * the calls below, which must not overlap on the GPU.  At most 8192 sequences.
+ */
+typedef struct {
+    int num_pages, n_seqs;
+    int* free_pages;
+    int* held;
+    int* state;
+} ra_page_pool;
+
+/*
+ * paged_reserve -- what a step needs to know of its sequences, from their lengths, in one launch:
+ * sequence g has lens[g] keys and brings new_lens[g] more (negative ones count as 0).
+ *   page_table  DEVICE int32 [n_seqs, max_pages], rows table_stride apart: entries are added for
+ *               the pages that the new tokens need beyond held, from the top of the stack, sequence
+ *               by sequence and page by page; held and the free pages follow;
+ *   cu_new      int32 [n_seqs + 1]: the rows of every sequence, as ra_paged_desc takes them;
+ *   kv_lens     int32 [n_seqs]: lens + new_lens; may be lens itself;
+ *   positions   NULL or int32 [T]: lens[g] + i of row i of sequence g, or with parents
+ *               lens[g] + depth;
+ *   slots       NULL or int64 [T]: page * page_size + place of every row's key in the cache;
+ *   parents     NULL or int32 [T]: the new tokens of a sequence form a tree (or several), entry i
+ *               naming the token of the same sequence that its token i extends, parents before
+ *               children; anything else (-1) is a root, whose depth is 0;
+ *   masks       NULL (mask_words 0) or int32 [T, mask_words]: bits of a row's ancestors and its
+ *               own, as paged_attn_tree_fwd takes them; needs parents.
+ * Rows behind the last sequence's get position 0, slot -1 and no bits.  A step that does not fit
+ * (too few free pages, more than T rows, a sequence longer than max_pages * page_size or 2^31 - 1)
+ * becomes one without rows: cu_new all 0, kv_lens = lens, nothing taken, and state[2] says why.
+ *
+ * paged_release -- gives back the pages behind the first ceil(lens[g] / page_size) of every
+ * sequence (lens[g] = 0: all it holds) and sets their table entries to -1.  It undoes a
+ * paged_reserve: released down to the lengths before it, the stack is what it was.
+ * Whatever the arrays hold, no access leaves them.  Errors: RA_ERR_INVALID_ARG (NULL pointers,
+ * sizes, arrays that share memory), RA_ERR_UNSUPPORTED (more than 8192 sequences, T above
+ * 2^31 - 1025), RA_ERR_MISALIGNED, RA_ERR_CUDA.
+ */
+ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int* lens, int* page_table,
+                        int max_pages, long long table_stride, int page_size, int T, int* cu_new,
+                        int* kv_lens, int* positions, long long* slots, const int* parents, int* masks,
+                        int mask_words, ra_stream_t stream);
+ra_status paged_release(const ra_page_pool* pool, const int* lens, int* page_table, int max_pages,
+                        long long table_stride, int page_size, ra_stream_t stream);
+
+/*
+ * paged_kv_keep -- after drafted tokens have been checked: of the n new tokens of sequence g
+ * (desc: cu_new, kv_lens, the cache) the accepted ones, kept[g][0 .. m), ascending indices, move
+ * to the front of the step's slots, in all layers at once, and lens[g] = kv_lens[g] - n + m.  A
+ * row of kept ends at the first entry that is not above the one before it and below n (-1, say).
+ * RA_KEEP_ALL in its first entry keeps every new token where it is (a prompt beside the trees).
+ * Their keys have the right positions already if they turned by depth (paged_kv_append_ex).
+ *
+ * kept: DEVICE int32 [n_seqs, width], rows kept_stride apart (0: width).  The cache is desc's,
+ * layers times, layer_stride elements apart (a multiple of 16 bytes; layers may lie between one
+ * another's pages as long as no two entries share memory); k_pages and v_pages may alternate in
+ * one buffer.  lens: DEVICE int32 [n_seqs], not kv_lens.  H, T and causal are not looked at.
+ * Entries whose page the table does not name properly are not moved.  D * element size a
+ * multiple of 16 bytes.  Errors as paged_kv_append.
+ */
+#define RA_KEEP_ALL (-2)
+ra_status paged_kv_keep(const ra_paged_desc* desc, const int* kept, int width, long long kept_stride,
+                        int layers, long long layer_stride, void* k_pages, void* v_pages, int* lens,
+                        ra_stream_t stream);
 
 /*
  * ra_check_status -- synchronise `stream`, then read and clear the status word
