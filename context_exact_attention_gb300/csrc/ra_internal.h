@@ -233,11 +233,15 @@ struct NormArgs {
     float* dq_weight;
     float* dk_weight;
     float* partials;               // [kNormCtas][2][256]
-    unsigned int* ticket;          // zero between calls
+    unsigned int* ticket;          // [1 + groups of blocks], zero between calls
     int lanes;                     // of a head vector, a power of two (set by the launch)
     int items;                     // of them, those that hold some of it (set by the launch)
+    int per_token, parts;          // rounds of a warp for a token's heads, and the parts that they
+                                   // are shared out in (set by the launch)
 };
 constexpr int kNormCtas = 640;     // of the backward
+constexpr int kNormGroup = 16;     // of its blocks, whose sums are added at once
+static_assert(4 * (1 + (kNormCtas + kNormGroup - 1) / kNormGroup) <= 256, "counters before the partial sums");
 cudaError_t launch_norm(const NormArgs& a, bool backward);
 
 // The pool of pages (paged_reserve, paged_release).

@@ -15,23 +15,28 @@ struct TokenPos {
     int live;           // 0: the row belongs to no sequence and is left as it is
 };
 
+// One step of warp_upper: the answer lies in [lo, lo + len), before and afterwards.
+__device__ __forceinline__ void warp_narrow(const int* v, int& lo, int& len, long long x, long long extent,
+                                            unsigned int* status)
+{
+    const int lane = threadIdx.x & 31;
+    const int step = (len + 31) / 32;
+    const int j = lo + lane * step;
+    const bool le = lane * step < len && checked_ldg(v, j, extent, status) <= x;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+    const int k = cnt > 0 ? cnt - 1 : 0;
+    lo += k * step;
+    len = min(step, len - k * step);
+}
+
 // The largest j in [0, n) with v[j] <= x (0 if there is none) for a non-decreasing v, by
 // one warp: every step loads 32 evenly spaced entries at once, so 1024 entries take two
 // dependent loads where a binary search takes ten.
 __device__ __forceinline__ int warp_upper(const int* v, int n, long long x, long long extent,
                                           unsigned int* status)
 {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, len = n;                       // the answer lies in [lo, lo + len)
-    while (len > 1) {
-        const int step = (len + 31) / 32;
-        const int j = lo + lane * step;
-        const bool le = lane * step < len && checked_ldg(v, j, extent, status) <= x;
-        const int cnt = __popc(__ballot_sync(0xffffffffu, le));
-        const int k = cnt > 0 ? cnt - 1 : 0;
-        lo += k * step;
-        len = min(step, len - k * step);
-    }
+    int lo = 0, len = n;
+    while (len > 1) warp_narrow(v, lo, len, x, extent, status);
     return lo;
 }
 
@@ -42,17 +47,29 @@ __device__ __forceinline__ TokenPos token_pos(const RopeArgs& a, long long t)
     TokenPos r{0, -1, 0};
     if (t >= a.rows) return r;
     if constexpr (kPaged) {
-        const int g = warp_upper(a.cu_seqlens, a.n_seqs, t, a.n_seqs + 1, a.status);
-        const int first = checked_ldg(a.cu_seqlens, g, a.n_seqs + 1, a.status);
-        const int end = checked_ldg(a.cu_seqlens, g + 1, a.n_seqs + 1, a.status);
+        // The last 32 sequences that the search leaves are looked at with their ends and
+        // lengths, so that a step of up to 32 sequences waits for one read before the table's.
+        const int lane = threadIdx.x & 31;
+        int lo = 0, len = a.n_seqs;
+        while (len > 32) warp_narrow(a.cu_seqlens, lo, len, t, a.n_seqs + 1, a.status);
+        int first = 0x7fffffff, end = 0, keys = 0;
+        if (lane < len) {
+            first = checked_ldg(a.cu_seqlens, lo + lane, a.n_seqs + 1, a.status);
+            end = checked_ldg(a.cu_seqlens, lo + lane + 1, a.n_seqs + 1, a.status);
+            keys = checked_ldg(a.kv_lens, lo + lane, a.n_seqs, a.status);
+        }
+        const int before = __popc(__ballot_sync(0xffffffffu, lane < len && first <= t));
+        const int k = before > 0 ? before - 1 : 0, g = lo + k;
+        first = __shfl_sync(0xffffffffu, first, k);
+        end = __shfl_sync(0xffffffffu, end, k);
+        keys = __shfl_sync(0xffffffffu, keys, k);
         if (t < first || t >= end) return r;
         r.live = 1;
-        r.pos = static_cast<long long>(checked_ldg(a.kv_lens, g, a.n_seqs, a.status)) -
-                (static_cast<long long>(end) - t);
+        r.pos = static_cast<long long>(keys) - (static_cast<long long>(end) - t);
         const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
-        if (r.pos >= 0 && r.pos < cap) {
-            const int col = static_cast<int>(r.pos / a.page_size);
-            const int in_page = static_cast<int>(r.pos - static_cast<long long>(col) * a.page_size);
+        if (r.pos >= 0 && r.pos < cap) {                // (below 2^31, as the lengths are)
+            const int col = static_cast<int>(static_cast<unsigned>(r.pos) / static_cast<unsigned>(a.page_size));
+            const int in_page = static_cast<int>(r.pos) - col * a.page_size;
             const int page = checked_ldg(a.page_table, g * a.table_stride + col, a.table_elems,
                                          a.status);
             if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages))
@@ -63,7 +80,8 @@ __device__ __forceinline__ TokenPos token_pos(const RopeArgs& a, long long t)
         return r;
     } else {
         r.live = 1;
-        const int l = static_cast<int>(t % a.L);
+        const int l = t >> 31 ? static_cast<int>(t % a.L)
+                              : static_cast<int>(static_cast<unsigned>(t) % static_cast<unsigned>(a.L));
         if (a.positions != nullptr) {
             r.pos = checked_ldg(a.positions, t, a.rows, a.status);
         } else if (a.layout == RA_LAYOUT_ZIGZAG) {
