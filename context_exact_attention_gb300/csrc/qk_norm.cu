@@ -28,16 +28,14 @@
 namespace ra {
 namespace {
 
-#ifndef FB
-#define FB 4
-#define BB 4
-#define AH 2
-#define BT 128
-#define MW 4ll
-#define FP 3
-#endif
-constexpr int kFwdThreads = 256, kBwdThreads = BT;
-constexpr int kAhead = AH;           // rounds in flight
+// Threads of a block, blocks that an SM should hold (of 128 threads with 64 registers each and 94,
+// and of 256 with 128) and rounds in flight.  Measured: 32768 tokens of 40 heads of 128 in bf16
+// 100 us (three rounds in flight, six blocks: 102); 8192 tokens of 32 and 8 heads appended 38 us
+// (two rounds, six blocks: 40; blocks of 256: 42); gradients of 16381 tokens of 40 heads 89 us
+// (two rounds: 90; one, three blocks: 105; blocks of 128: 91 to 93).
+constexpr int kFwdThreads = 128, kBwdThreads = 256;
+constexpr int kFwdBlocks = 8, kPagedBlocks = 5, kBwdBlocks = 2;
+constexpr int kFwdAhead = 2, kPagedAhead = 3, kBwdAhead = 3;
 
 enum Mode { kHalf, kInterleaved, kExchange };
 
@@ -357,9 +355,10 @@ constexpr int kLanesOf = kD / (2 * (16 / static_cast<int>(sizeof(T))));
 
 // kD: the head dim, or 0 for any.
 template <typename T, Mode kMode, int kD, bool kPaged>
-__global__ void __launch_bounds__(kFwdThreads, kPaged ? FP : FB) norm_fwd_kernel(const __grid_constant__ NormArgs n)
+__global__ void __launch_bounds__(kFwdThreads, kPaged ? kPagedBlocks : kFwdBlocks) norm_fwd_kernel(const __grid_constant__ NormArgs n)
 {
     constexpr int N = 16 / sizeof(T);
+    constexpr int kAhead = kPaged ? kPagedAhead : kFwdAhead;
     __shared__ Smem<T, kMode, kFwdThreads / 32, false> s;
     const RopeArgs& a = n.rope;
     constexpr int kLanes = kLanesOf<T, kD>;
@@ -446,9 +445,10 @@ __global__ void __launch_bounds__(kFwdThreads, kPaged ? FP : FB) norm_fwd_kernel
 }
 
 template <typename T, Mode kMode, int kD>
-__global__ void __launch_bounds__(kBwdThreads, BB) norm_bwd_kernel(const __grid_constant__ NormArgs n)
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) norm_bwd_kernel(const __grid_constant__ NormArgs n)
 {
     constexpr int N = 16 / sizeof(T);
+    constexpr int kAhead = kBwdAhead;
     constexpr int kWarps = kBwdThreads / 32;
     __shared__ Smem<T, kMode, kWarps, true> s;
     const RopeArgs& a = n.rope;
@@ -677,11 +677,21 @@ cudaError_t launch(NormArgs& n, bool backward)
         const unsigned grid = static_cast<unsigned>(std::min<long long>((rounds + warps - 1) / warps, slots));
         return launch_early(kernel, grid, threads, 0, a.stream, n);
     }
-    // A warp takes a token, or a part of one where there would not be four for every warp that
-    // the GPU holds (its positions and angles are then worked out once a part).
-    n.parts = 1;
-    while (a.rows * n.parts < MW * slots * warps && n.per_token >= 2 * (n.parts + 1)) ++n.parts;
-    if (a.rows * n.parts < slots * warps) n.parts = n.per_token;
+    // The parts of a token's rounds, a warp each, with which the call is done first, taking that
+    // the warps go in waves of as many as the GPU holds and that one takes as long as kFixed
+    // rounds (first reads, position, angles) besides its own.
+    constexpr int kFixed = 4;
+    const long long held = static_cast<long long>(slots) * warps;
+    long long least = 0;
+    for (int p = 1; p <= std::min(n.per_token, 64); ++p) {
+        const long long waves = (a.rows * p + held - 1) / held;
+        const long long cost = waves * (kFixed + (n.per_token + p - 1) / p);
+        if (p == 1 || cost < least) {
+            least = cost;
+            n.parts = p;
+        }
+        if (waves > 64) break;                      // (more parts only cost more)
+    }
     const long long blocks = (a.rows * n.parts + warps - 1) / warps;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(blocks);
