@@ -432,6 +432,20 @@ TREE = {
     "more new than keys": ([(40, 25), (30, 0), (8, 3)], 8, 2, 64, 16, BF, "slots", 2, 2),
     "pages of 3": ([(12, 100), (40, 44)], 8, 2, 64, 3, BF, "slots", 0, 2),
     "long context": ([(60, 9000)], 8, 2, 128, 128, BF, "slots", 0, 2),
+    # many tiles
+    "many, few rows": ([((i * 3) % 5, 30 * i + 6) for i in range(20)], 8, 4, 128, 16, BF, "slots", 2, 1),
+    "many, few rows, D 64": ([(4, 50 + 90 * i) for i in range(12)], 16, 4, 64, 8, BF, "heads", 0, 1),
+    "many, long": ([(4, 3000), (3, 100)] + [(1, 500)] * 9, 16, 4, 128, 64, BF, "slots", 0, 1),
+    "many, many rows": ([((i * 13) % 62, 40 * i + 62) for i in range(11)], 16, 4, 128, 16, BF, "by_slot", 3, 2),
+    "many, single sub-tiles": ([(20 + i % 7, 100 * i + 30) for i in range(10)], 16, 4, 128, 64, BF, "slots", 0, 1),
+    "many, D 64": ([((i * 29) % 100, 30 * i + 100) for i in range(10)], 16, 4, 64, 32, BF, "by_page", 1, 4),
+    "many, words too few": ([(50, 55 + i) for i in range(10)], 8, 4, 128, 16, BF, "slots", 0, 1),
+    "many, more new than keys": ([(30 + i, 20 + 2 * i) for i in range(12)], 8, 4, 64, 16, BF, "slots", 2, 2),
+    "a wide group, many": ([(5, 200 + i) for i in range(12)], 128, 4, 64, 16, BF, "slots", 0, 1),
+    "pages of 3, many": ([(12, 100 + i) for i in range(12)], 8, 4, 64, 3, BF, "slots", 0, 1),
+    "one long context": ([(64, 30000)], 8, 2, 128, 64, BF, "slots", 0, 2),
+    "two rows of a tile": ([(3, 700)], 16, 2, 128, 16, BF, "by_head", 0, 1),
+    "no keys": ([(5, 0), (0, 0), (3, 1)], 8, 2, 128, 16, BF, "slots", 1, 1),
     "fp32": ([(5, 90), (7, 40), (1, 1), (0, 3)], 6, 2, 128, 16, F32, "slots", 1, 1),
     "fp32 wide": ([(9, 130), (3, 3)], 5, 1, 256, 8, F32, "heads", 0, 1),
     "fp32 rows": ([(64, 300), (90, 777)], 8, 4, 64, 16, F32, "slots", 2, 3),
@@ -491,7 +505,8 @@ def test_tree_attention(name, kind):
 
 
 def test_a_chain_is_the_causal_rule():
-    for seqs, dtype in (([(60, 500), (33, 64)], BF), ([(3, 400), (4, 30)], BF), ([(9, 100)], F32)):
+    for seqs, dtype in (([(60, 500), (33, 64)], BF), ([(3, 400), (4, 30)], BF), ([(9, 100)], F32),
+                        ([(60, 300 + i) for i in range(8)], BF), ([(3, 100)] * 20, BF)):
         c = Cache(seqs, 8, 2, 128, 16, dtype, seed=8)
         masks = torch.cat([mask_words(torch.ones(n, n).tril().bool(), 2) for n, _ in seqs])
         out, lse = tree_attend(c, masks)
@@ -502,6 +517,7 @@ def test_unseen_keys_that_are_not_finite():
     """A drafted token's key that is infinite or NaN reaches the rows that see it, and no others; in
     fp32 its value too."""
     for seqs, H, dtype in (([(4, 100), (3, 50)], 4, BF), ([(40, 300), (20, 90)], 8, BF),
+                           ([(4, 100)] + [(3, 50)] * 20, 4, BF), ([(40, 300)] + [(20, 90)] * 12, 8, BF),
                            ([(5, 60), (4, 33)], 4, F32), ([(100, 300)], 8, F32)):
         c = Cache(seqs, H, 2, 64, 16, dtype, seed=9)
         seen, masks = tree_masks(c, 4, "trees", 5)
@@ -767,7 +783,8 @@ def test_index_checked_build(monkeypatch):
             res += cea.qk_norm_rope_fwd(*c.dev("q", "k", "wq", "wk"), **c.kw)
             c.kw["dq"], c.kw["dk"] = torch.zeros_like(c.q, device=DEV), torch.zeros_like(c.k, device=DEV)
             res += cea.qk_norm_rope_bwd(*c.dev("q", "k", "wq", "wk", "dq", "dk"), **c.kw)
-        for name in ("few rows", "many rows", "more new than keys", "fp32", "fp32 rows"):
+        for name in ("few rows", "many rows", "more new than keys", "many, few rows", "many, many rows",
+                     "fp32", "fp32 rows"):
             seqs, H, K, D, page, dtype, layout, pad, words = TREE[name]
             c = Cache(seqs, H, K, D, page, dtype, layout, pad, seed=1)
             res += tree_attend(c, tree_masks(c, words, "trees")[1])
