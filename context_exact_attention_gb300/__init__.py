@@ -974,18 +974,24 @@ def rope_bwd(dq_out, dk_out, rope: RopeTable, positions=None, offset: int = 0,
                       q_out, k_out, stream)
 
 
+def _weight(w, D, dtype, name):
+    """The address of a norm's weight [D], checked (0 for None)."""
+    if w is None:
+        return 0
+    if w.dtype is not dtype or w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [D] tensor, of the other weight's dtype")
+    return w.data_ptr()
+
+
 def _head_norm(D, q_weight, k_weight, eps, weight_offset):
     """Packed ra_head_norm of weights [D] (or None) for heads of D dims."""
-    code = RA_F32
-    for name, w, other in (("q_weight", q_weight, k_weight), ("k_weight", k_weight, q_weight)):
-        if w is None:
-            continue
-        if w.shape != (D,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [D] tensor")
-        code = _float_code(w.dtype, name)
-        if other is not None and other.dtype is not w.dtype:
-            raise ValueError("the weights must have one dtype")
-    return _HEAD_NORM.pack(_addr(q_weight), _addr(k_weight), code, eps, weight_offset)
+    ref = q_weight if q_weight is not None else k_weight
+    if ref is None:
+        return _HEAD_NORM.pack(0, 0, RA_F32, eps, weight_offset)
+    dtype = ref.dtype
+    return _HEAD_NORM.pack(_weight(q_weight, D, dtype, "q_weight"),
+                           _weight(k_weight, D, dtype, "k_weight"),
+                           _float_code(dtype, "the weights"), eps, weight_offset)
 
 
 def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, rope: RopeTable | None = None,
@@ -1062,10 +1068,14 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, rope: RopeTable |
     return dq, dk, weights[0], weights[1]
 
 
-def _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal):
+def _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal, layers=False):
+    """Packed ra_paged_desc; of the first layer, if the pages may be [layers, ...]."""
     shape, stride = k_pages.shape, k_pages.stride()
-    if len(shape) != 4 or shape != v_pages.shape or k_pages.dtype != v_pages.dtype \
-            or stride != v_pages.stride():
+    if layers and len(shape) == 5 and shape == v_pages.shape and stride == v_pages.stride():
+        shape, stride = shape[1:], stride[1:]
+    elif len(shape) != 4 or shape != v_pages.shape or stride != v_pages.stride():
+        shape = ()
+    if len(shape) != 4 or k_pages.dtype is not v_pages.dtype:
         raise ValueError("k_pages and v_pages must be alike: [num_pages, page_size, H_kv, D] "
                          "of one dtype with the same strides")
     if stride[3] != 1 and shape[3] > 1:
@@ -1259,14 +1269,19 @@ def paged_step(n_seqs: int, rows: int, mask_words: int = 0, device=None) -> Page
                      ints(rows, mask_words) if mask_words else None)
 
 
+def _index_array(t, name, n, dtype=torch.int32):
+    """The address of a contiguous integer tensor of n entries, checked."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape [{n}]")
+    return t.data_ptr()
+
+
 def _pool_args(pool, lens, page_table):
-    _index_tensor(lens, "lens", 1, (pool.n_seqs,))
+    _index_array(lens, "lens", pool.n_seqs)
     _index_tensor(page_table, "page_table", 2)
     rows, cols = page_table.shape
     if rows != pool.n_seqs:
         raise ValueError("page_table must have a row for every sequence of the pool")
-    if not lens.is_contiguous():
-        raise ValueError("lens must be contiguous")
     return page_table.data_ptr(), cols, page_table.stride(0) if rows > 1 else cols
 
 
@@ -1287,29 +1302,30 @@ def paged_reserve(pool: PagePool, new_lens, lens, page_table, page_size: int, st
         with _entered(device, stream):
             return paged_reserve(pool, new_lens, lens, page_table, page_size, step, parents)
     n = pool.n_seqs
-    table = _pool_args(pool, lens, page_table)
-    _index_tensor(new_lens, "new_lens", 1, (n,))
-    _index_tensor(cu_new, "step.cu_new", 1, (n + 1,))
-    _index_tensor(kv_lens, "step.kv_lens", 1, (n,))
-    rows = next((t.shape[0] for t in (positions, slots, masks, parents) if t is not None), None)
-    if rows is None:
+    table, cols, table_step = _pool_args(pool, lens, page_table)
+    row_wise = positions if positions is not None else slots if slots is not None else masks
+    if row_wise is None:
         raise ValueError("step must have positions, slots or masks, whose size is its rows'")
+    rows = row_wise.shape[0]
+    _index_array(new_lens, "new_lens", n)
+    _index_array(cu_new, "step.cu_new", n + 1)
+    _index_array(kv_lens, "step.kv_lens", n)
+    at_positions = at_slots = at_parents = at_masks = words = 0
     if positions is not None:
-        _index_tensor(positions, "step.positions", 1, (rows,))
+        at_positions = _index_array(positions, "step.positions", rows)
+    if slots is not None:
+        at_slots = _index_array(slots, "step.slots", rows, torch.int64)
     if parents is not None:
-        _index_tensor(parents, "parents", 1, (rows,))
-    if slots is not None and (slots.dtype is not torch.int64 or slots.shape != (rows,)):
-        raise ValueError(f"step.slots must be an int64 tensor of shape [{rows}]")
-    words = 0
-    if parents is not None and masks is not None:
-        words = masks.shape[-1]
-        _index_tensor(masks, "step.masks", 2, (rows, words))
-    for t in (new_lens, cu_new, kv_lens, positions, slots, parents, masks):
-        if t is not None and not t.is_contiguous():
-            raise ValueError("all tensors but page_table must be contiguous")
-    _call_fast("paged_reserve", pool._c, new_lens.data_ptr(), lens.data_ptr(), *table, page_size,
-               rows, cu_new.data_ptr(), kv_lens.data_ptr(), _addr(positions), _addr(slots),
-               _addr(parents), masks.data_ptr() if words else 0, words, s)
+        at_parents = _index_array(parents, "parents", rows)
+        if masks is not None:
+            words = masks.shape[-1]
+            _index_tensor(masks, "step.masks", 2, (rows, words))
+            if not masks.is_contiguous():
+                raise ValueError("step.masks must be contiguous")
+            at_masks = masks.data_ptr()
+    _call_fast("paged_reserve", pool._c, new_lens.data_ptr(), lens.data_ptr(), table, cols,
+               table_step, page_size, rows, cu_new.data_ptr(), kv_lens.data_ptr(), at_positions,
+               at_slots, at_parents, at_masks, words, s)
     return step
 
 
@@ -1338,15 +1354,12 @@ def paged_kv_keep(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens=None
     if s is None:
         with _entered(device, stream):
             return paged_kv_keep(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens)
+    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, 0, 1, 0, True)
     layers, step = 1, 0
     if k_pages.dim() == 5:
-        if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
-            raise ValueError("k_pages and v_pages must be alike")
         layers, step = k_pages.shape[0], k_pages.stride(0)
         if layers < 1:
             raise ValueError("k_pages and v_pages must have a layer")
-        k_pages, v_pages = k_pages[0], v_pages[0]
-    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, 0, 1, 0)
     n = kv_lens.shape[0]
     _index_tensor(kept, "kept", 2)
     width = kept.shape[1]
@@ -1355,9 +1368,7 @@ def paged_kv_keep(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens=None
     if lens is None:
         lens = torch.empty(n, dtype=torch.int32, device=device)
     else:
-        _index_tensor(lens, "lens", 1, (n,))
-        if not lens.is_contiguous():
-            raise ValueError("lens must be contiguous")
+        _index_array(lens, "lens", n)
     _call_fast("paged_kv_keep", d, kept.data_ptr(), width, kept.stride(0) if n > 1 else width,
                layers, step if layers > 1 else 0, k_pages.data_ptr(), v_pages.data_ptr(),
                lens.data_ptr(), s)

@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kDeep = 8;                    // reads (of keep_kernel: moves) in flight of a thread
 
 // Exclusive sum of two values over the block's threads; totals in *all_a, *all_b.
 __device__ __forceinline__ void block_sums(long long& a, long long& b, long long* all_a, long long* all_b)
@@ -120,18 +121,33 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
     const int g0 = min(static_cast<int>(threadIdx.x) * per, n), g1 = min(g0 + per, n);
     const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
     auto need_of = [&](int g, int add) -> long long {
-        const long long pages = (static_cast<long long>(len[g]) + add + a.page_size - 1) / a.page_size;
+        // (below 2^33: a sum of three numbers below 2^31)
+        const unsigned long long keys = static_cast<unsigned long long>(len[g]) + add + a.page_size - 1;
+        const long long pages = keys >> 32 ? static_cast<long long>(keys / a.page_size)
+                                           : static_cast<unsigned>(keys) / static_cast<unsigned>(a.page_size);
         return max(pages - held[g], 0ll);
     };
     long long rows = 0, pages = 0;
-    for (int g = g0; g < g1; ++g) {
-        const int add = length_of(a, r.new_lens, g);
-        len[g] = length_of(a, r.lens, g);
-        held[g] = held_of(a, g);
-        cu[g] = add;
-        rows += add;
-        pages += need_of(g, add);
-        if (static_cast<long long>(len[g]) + add > min(cap, 0x7fffffffll)) too_long = 1;
+    for (int first = g0; first < g1; first += kDeep) {
+        int add[kDeep], before[kDeep], has[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {               // (all reads first)
+            const int g = min(first + k, g1 - 1);
+            add[k] = length_of(a, r.new_lens, g);
+            before[k] = length_of(a, r.lens, g);
+            has[k] = held_of(a, g);
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int g = first + k;
+            if (g >= g1) break;
+            len[g] = before[k];
+            held[g] = has[k];
+            cu[g] = add[k];
+            rows += add[k];
+            pages += need_of(g, add[k]);
+            if (static_cast<long long>(before[k]) + add[k] > min(cap, 0x7fffffffll)) too_long = 1;
+        }
     }
     long long all_rows, all_pages;
     long long at_row = rows, at_page = pages;
@@ -172,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
             c = cu[g];
             i = t - c;
             pos = len[g] + i;
-            const int col = pos / a.page_size;
+            const int col = static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(a.page_size));
             int page;
             if (col < held[g]) {
                 const long long at = g * a.table_stride + col;
@@ -247,12 +263,24 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
     const int per = (n + kThreads - 1) / kThreads;
     const int g0 = min(static_cast<int>(threadIdx.x) * per, n), g1 = min(g0 + per, n);
     long long pages = 0, none = 0, all_none, all;
-    for (int g = g0; g < g1; ++g) {
-        const int held = held_of(a, g);
-        const long long want = (static_cast<long long>(length_of(a, r.lens, g)) + a.page_size - 1) / a.page_size;
-        left[g] = static_cast<int>(min(want, static_cast<long long>(held)));
-        gone[g] = held - left[g];
-        pages += gone[g];
+    for (int first = g0; first < g1; first += kDeep) {
+        int has[kDeep], keys[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {               // (all reads first)
+            const int g = min(first + k, g1 - 1);
+            has[k] = held_of(a, g);
+            keys[k] = length_of(a, r.lens, g);
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int g = first + k;
+            if (g >= g1) break;
+            const int want = static_cast<int>((keys[k] + static_cast<unsigned>(a.page_size) - 1) /
+                                              static_cast<unsigned>(a.page_size));
+            left[g] = min(want, has[k]);
+            gone[g] = has[k] - left[g];
+            pages += gone[g];
+        }
     }
     long long at = pages;
     block_sums(at, none, &all, &all_none);
@@ -289,7 +317,6 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
 // A block takes a piece of one sequence: 256 threads' 16-byte columns of (layer, keys or values,
 // head); its first warp looks the path's slots up once for all of them.
 constexpr int kPath = 32;                   // entries looked up at a time
-constexpr int kDeep = 8;                    // moves in flight
 
 __global__ void __launch_bounds__(kThreads) keep_kernel(const __grid_constant__ KeepArgs a)
 {
