@@ -384,8 +384,9 @@ cudaError_t launch_paged_bf16(const PagedArgs& a)
 
 cudaError_t launch_paged(const PagedArgs& a)
 {
+    cudaError_t e = cudaSuccess;
+    if (a.masks != nullptr && (a.elem == 2 ? paged_tree_bf16(a, &e) : paged_tree_f32(a, &e))) return e;
     if (a.elem != 2) return paged_rows_applies(a) ? launch_paged_rows(a) : launch_paged_simt(a);
-    if (paged_tree_applies(a)) return launch_paged_tree(a);
     return paged_tc_applies(a) ? launch_paged_tc(a) : launch_paged_bf16(a);
 }
 

@@ -21,8 +21,8 @@
 // 26 tokens over 2000 keys, 32 heads over 8, takes 13 us (22 there), one of 4 tokens 8.5.
 #include <algorithm>
 
+#include "paged_cluster.cuh"
 #include "paged_mma.cuh"
-#include "paged_plan.cuh"
 
 namespace ra {
 namespace {
@@ -32,7 +32,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kKeys = 64;                      // keys of a step
 constexpr int kKeysW = kKeys / kWarps;         // ... that a warp copies
 constexpr float kRescaleThreshold = 8.0f;
-constexpr int kMostCtas = 16;                  // of a cluster
 
 template <int D>
 struct Smem {
@@ -46,22 +45,6 @@ struct Smem {
     static constexpr int kStat = kStatW + kWarps * 16 * 8;    // [row] of the tile, over the warps
     static constexpr int kBytes = kStat + kWarps * 16 * 8;
 };
-
-__device__ __forceinline__ float4 load_remote4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 load_remote2(uint32_t addr)
-{
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
-}
 
 // kRowWarps: warps that share the tile's rows; the others share the keys of a step with them.
 template <int D, int kRowWarps>
@@ -90,46 +73,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tree_kernel(const __grid_co
     const uint32_t ring = smem_addr(smem);
 
     wait_for_earlier_work();
-    // The cluster's tile, found by each warp for itself: the tiles lie one after the other,
-    // sequence by sequence, head by head.
     TileRows t{};
     SeqSpan span{};
-    int g = -1;
-    {
-        int rest = static_cast<int>(blockIdx.x) / ctas;
-#pragma unroll 1
-        for (int base = 0; base < a.n_seqs && g < 0; base += 32) {
-            SeqSpan mine{};
-            int tiles = 0;
-            if (base + lane < a.n_seqs) {
-                mine = seq_span_of(a, base + lane);
-                tiles = (mine.n * p.G + kRows - 1) / kRows * a.H_kv;
-            }
-            int inc = tiles;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            const unsigned holds = __ballot_sync(0xffffffffu, inc > rest);
-            if (holds == 0) {
-                rest -= __shfl_sync(0xffffffffu, inc, 31);
-                continue;
-            }
-            const int k = __ffs(holds) - 1;
-            g = base + k;
-            rest -= __shfl_sync(0xffffffffu, inc - tiles, k);
-            span.first = __shfl_sync(0xffffffffu, mine.first, k);
-            span.n = __shfl_sync(0xffffffffu, mine.n, k);
-            span.kv = __shfl_sync(0xffffffffu, mine.kv, k);
-            const int per_head = __shfl_sync(0xffffffffu, tiles, k) / a.H_kv;
-            t.hk = rest / per_head;
-            t.row0 = (rest - t.hk * per_head) * kRows;
-        }
-    }
+    const int g = cluster_tile<kRows>(p, t, span);
     if (g < 0) return;                          // (all of a cluster, which has met no barrier)
-    t.first = span.first;
-    t.rows = min(kRows, span.n * p.G - t.row0);
     const int steps = (span.kv + kKeys - 1) / kKeys;
     const int s0 = static_cast<int>(static_cast<long long>(steps) * rank / ctas);
     const int s1 = static_cast<int>(static_cast<long long>(steps) * (rank + 1) / ctas);
@@ -344,38 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tree_kernel(const __grid_co
             if (c == 0) stat[r] = make_float2(M, L);
         }
     }
-    cluster_sync_all();
-    // The CTAs' parts, in order: rows rank, rank + ctas, ... are this CTA's, a warp (of 64 dims
-    // half of one) each; lane k holds the statistics of part k.
-    constexpr int kRowLanes = D / 4;            // four columns a lane
-    const int sub = lane / kRowLanes, c = lane % kRowLanes;
-    const uint32_t buf_s = smem_addr(buf), stat_s = smem_addr(stat);
-#pragma unroll 1
-    for (int r0 = rank + ctas * (warp * (32 / kRowLanes)); r0 < t.rows; r0 += ctas * kWarps * (32 / kRowLanes)) {
-        const int r = r0 + ctas * sub;
-        const bool mine = r < t.rows;
-        float2 st = make_float2(-INFINITY, 0.f);
-        if (mine && c < ctas) st = load_remote2(mapa_shared(stat_s + 8 * r, c));
-        float M = st.x;
-#pragma unroll
-        for (int w = kMostCtas / 2; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-        const float f = st.y == 0.f ? 0.f : part_weight(st.x, st.y, M), fl = st.y == 0.f ? 0.f : f * st.y;
-        float L = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < ctas; ++k) {
-            const float w = __shfl_sync(0xffffffffu, f, sub * kRowLanes + k);
-            L += __shfl_sync(0xffffffffu, fl, sub * kRowLanes + k);
-            if (!mine) continue;
-            const float4 y = load_remote4(mapa_shared(buf_s + (r * S::kLdo + 4 * c) * 4, k));
-            x.x = fmaf(w, y.x, x.x);
-            x.y = fmaf(w, y.y, x.y);
-            x.z = fmaf(w, y.z, x.z);
-            x.w = fmaf(w, y.w, x.w);
-        }
-        if (mine) write_row4<__nv_bfloat16>(p, t, r, c, x, M, L);
-    }
-    cluster_sync_all();                         // no CTA leaves while others read its parts
+    join_cluster<__nv_bfloat16, 1, D / 4>(p, t, buf, S::kLdo, stat, warp, kWarps);
 }
 
 // Rows of a tile by what a sequence and key head have on average, in units of 16.
@@ -383,46 +299,6 @@ int row_warps(const PagedArgs& a)
 {
     const long long rows = static_cast<long long>(a.T) * (a.H / a.H_kv);
     return rows <= 16ll * a.n_seqs ? 1 : rows <= 32ll * a.n_seqs ? 2 : 4;
-}
-
-// At most so many tiles of 16 w rows does a call have, whatever its lengths are.
-long long most_tiles(const PagedArgs& a, int w)
-{
-    const long long rows = static_cast<long long>(a.T) * (a.H / a.H_kv);
-    return a.H_kv * ((rows + a.n_seqs * (16ll * w - 1)) / (16 * w));
-}
-
-// Clusters of `ctas` CTAs that the current device holds at once, asked once per device (known: 0,
-// not asked yet).
-template <typename Kernel>
-cudaError_t clusters_held(std::atomic<int>* known, Kernel kernel, int bytes, int ctas, int* clusters)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    *clusters = known[dev].load(std::memory_order_acquire) - 1;
-    if (*clusters >= 0) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cudaLaunchConfig_t config{};
-    config.gridDim = dim3(ctas);
-    config.blockDim = dim3(kThreads);
-    config.dynamicSmemBytes = bytes;
-    config.attrs = &at;
-    config.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(clusters, kernel, &config);
-    if (e != cudaSuccess) {
-        cudaGetLastError();                     // (a size that the GPU does not take)
-        *clusters = 0;
-    }
-    known[dev].store(*clusters + 1, std::memory_order_release);
-    return cudaSuccess;
 }
 
 // The cluster size of a call, or 0 where the kernels for more tiles are better: the largest with
@@ -438,65 +314,47 @@ template <int D, int kRowWarps>
 int ctas_of(const PagedArgs& a)
 {
     static std::atomic<int> known[5][kMaxDevices];
-    const long long tiles = most_tiles(a, kRowWarps);
+    const long long tiles = most_tiles(a, 16 * kRowWarps);
     const long long keys = static_cast<long long>(a.max_pages) * a.page_size;
     for (int i = 0; i < (kRowWarps < 4 ? 5 : 4); ++i) {
         const int ctas = kMostCtas >> i;
         if (keys > static_cast<long long>(ctas) * kKeys * (i < 2 || kRowWarps < 4 ? 16 : 8)) return 0;
         int held = 0;
-        if (clusters_held(known[i], paged_tree_kernel<D, kRowWarps>, Smem<D>::kBytes, ctas, &held) == cudaSuccess &&
+        if (clusters_held(known[i], paged_tree_kernel<D, kRowWarps>, kThreads, Smem<D>::kBytes, ctas, &held) == cudaSuccess &&
             tiles <= held)
             return ctas;
     }
     return 0;
 }
 
+// Launches the call if it goes this way.
 template <int D, int kRowWarps>
-cudaError_t launch_d(PagedParams& p)
+bool go(const PagedArgs& a, cudaError_t* e)
 {
-    constexpr auto kernel = paged_tree_kernel<D, kRowWarps>;
-    const int ctas = ctas_of<D, kRowWarps>(p.a);
-    if (ctas == 0) return cudaErrorInvalidValue;
-    p.grid = ctas;
-    cudaLaunchAttribute at[2]{};
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = ctas;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t config{};
-    config.gridDim = dim3(static_cast<unsigned>(most_tiles(p.a, kRowWarps)) * ctas);
-    config.blockDim = dim3(kThreads);
-    config.dynamicSmemBytes = Smem<D>::kBytes;
-    config.stream = p.a.stream;
-    config.attrs = at;
-    config.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, p);
-    if (e != cudaSuccess) cudaGetLastError();       // reported here, not to the next caller who asks
-    return e;
+    const int ctas = ctas_of<D, kRowWarps>(a);
+    if (ctas == 0) return false;
+    PagedParams p;
+    fill_params(&p, a);
+    *e = launch_clusters(paged_tree_kernel<D, kRowWarps>, p, most_tiles(a, 16 * kRowWarps), ctas, kThreads,
+                         Smem<D>::kBytes);
+    return true;
+}
+template <int D>
+bool go_rows(const PagedArgs& a, cudaError_t* e)
+{
+    switch (row_warps(a)) {
+    case 1: return go<D, 1>(a, e);
+    case 2: return go<D, 2>(a, e);
+    default: return go<D, 4>(a, e);
+    }
 }
 
 }  // namespace
 
-bool paged_tree_applies(const PagedArgs& a)
+bool paged_tree_bf16(const PagedArgs& a, cudaError_t* e)
 {
-    if (a.masks == nullptr || a.elem != 2) return false;
-    switch (row_warps(a)) {
-    case 1: return (a.D == 64 ? ctas_of<64, 1>(a) : ctas_of<128, 1>(a)) > 0;
-    case 2: return (a.D == 64 ? ctas_of<64, 2>(a) : ctas_of<128, 2>(a)) > 0;
-    default: return (a.D == 64 ? ctas_of<64, 4>(a) : ctas_of<128, 4>(a)) > 0;
-    }
-}
-
-cudaError_t launch_paged_tree(const PagedArgs& a)
-{
-    PagedParams p;
-    fill_params(&p, a);
-    switch (row_warps(a)) {
-    case 1: return a.D == 64 ? launch_d<64, 1>(p) : launch_d<128, 1>(p);
-    case 2: return a.D == 64 ? launch_d<64, 2>(p) : launch_d<128, 2>(p);
-    default: return a.D == 64 ? launch_d<64, 4>(p) : launch_d<128, 4>(p);
-    }
+    if (a.D == 64) return go_rows<64>(a, e);
+    return a.D == 128 && go_rows<128>(a, e);
 }
 
 }  // namespace ra

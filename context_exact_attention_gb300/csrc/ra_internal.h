@@ -323,9 +323,10 @@ cudaError_t launch_paged_simt(const PagedArgs& a);   // fp32, few rows per key/v
 bool paged_rows_applies(const PagedArgs& a);
 cudaError_t launch_paged_rows(const PagedArgs& a);   // fp32, many rows
 cudaError_t launch_paged_bf16(const PagedArgs& a);   // bf16, few rows per key/value head
-// bf16, trees of drafted tokens in calls of few tiles: a cluster for each
-bool paged_tree_applies(const PagedArgs& a);
-cudaError_t launch_paged_tree(const PagedArgs& a);
+// Trees of drafted tokens in calls of few tiles, a cluster for each: launch the call, with *e what
+// became of it, or leave it to the others (false).
+bool paged_tree_bf16(const PagedArgs& a, cudaError_t* e);
+bool paged_tree_f32(const PagedArgs& a, cudaError_t* e);
 // bf16, many rows: CTAs, and tensor maps of q ({D, H, T}, boxes of 64 x G x tokens) and of
 // the pages ({D, H_kv, page_size, num_pages}, boxes of 64 x 1 x keys of one page x 1).
 bool paged_tc_applies(const PagedArgs& a);

@@ -451,6 +451,14 @@ TREE = {
     "fp32 rows": ([(64, 300), (90, 777)], 8, 4, 64, 16, F32, "slots", 2, 3),
     "fp32 rows 128": ([(120, 900), (70, 71)], 16, 4, 128, 24, F32, "by_page", 0, 4),
     "fp32 rows 192": ([(150, 400)], 16, 4, 192, 16, F32, "slots", 0, 5),
+    "fp32, 16 rows": ([(4, 300), (3, 77)], 8, 2, 128, 16, F32, "heads", 2, 1),
+    "fp32, 32 rows": ([(8, 500), (5, 64), (0, 9)], 8, 2, 100, 16, F32, "slots", 0, 1),
+    "fp32, narrow": ([(8, 500), (30, 64)], 4, 2, 36, 8, F32, "by_head", 0, 1),
+    "fp32, 4 dims": ([(9, 130)], 4, 1, 4, 16, F32, "slots", 0, 1),
+    "fp32, many": ([(3, 40 + 30 * i) for i in range(20)], 8, 4, 64, 16, F32, "slots", 1, 1),
+    "fp32, many rows of many": ([(40, 50 + 30 * i) for i in range(12)], 16, 4, 128, 16, F32, "slots", 0, 2),
+    "fp32, a long context": ([(20, 9000)], 4, 2, 64, 64, F32, "slots", 0, 1),
+    "fp32, many of 192": ([(3, 40 + 30 * i) for i in range(30)], 8, 4, 192, 16, F32, "slots", 0, 1),
     "fp32 rows 256": ([(100, 260)], 32, 4, 256, 16, F32, "by_slot", 0, 2),
 }
 
