@@ -6,18 +6,19 @@
 // ty + 8 i, with the keys tx + 16 j of a step, and the output of the same rows in columns
 // 4 (tx + 16 u).  Keys lie with their 16-byte chunks permuted by the key's low bits, weights with
 // bit 4 of the key flipped in odd rows.  Keys and values come 32 at a time through a ring, a step
-// or two ahead.
+// ahead.
 //
-// TODO bound
+// What bounds it: instructions, of one or two warps a scheduler, with few of each other's latencies
+// to hide: a step of 32 keys of 16 rows of 128 dims takes 2.5 us.  Measured against the kernels
+// for more tiles (four rows at a time, or 64 in paged_attn_simt_rows.cu): 8 sequences of 13
+// tokens, 8 heads over 2 of 128 dims, 500 keys, 23 us and 25; 26 tokens, 32 heads over 8, 2000
+// keys, 47 and 64; 100 tokens, 8 heads over 2, 1000 keys, 30 and 60; of 64 dims, 16 of 4 tokens,
+// 500 keys, 9 and 16; 2 of 40 tokens, 16 heads over 4, 1000 keys, 22 and 44.
 #include <algorithm>
 #include <type_traits>
 
 #include "paged_cluster.cuh"
 
-#ifndef FST
-#define FST 16
-#define FMIN 16
-#endif
 namespace ra {
 namespace {
 
@@ -29,10 +30,9 @@ constexpr int kKeysW = kKeys / kWarps;         // ... that a warp copies
 constexpr int kPer = kKeys / 16;               // ... of a thread's scores
 
 // Shared memory: queries, a ring of keys and values (then the tile's sums), weights, statistics.
-template <int kCols>
-constexpr int kStages = 2;
+constexpr int kStages = 2;                     // (a third costs the second CTA of an SM: 12 to 90 % slower)
 template <int kCols, int kR>
-constexpr int kSmem = ((kTy * kR + kStages<kCols> * 2 * kKeys) * 64 * kCols + kTy * kR * kKeys) * 4 + kTy * kR * 8;
+constexpr int kSmem = ((kTy * kR + kStages * 2 * kKeys) * 64 * kCols + kTy * kR * kKeys) * 4 + kTy * kR * 8;
 
 // kCols: column groups of 64 (D <= 64 kCols; the columns behind D are zeros).
 template <int kCols, int kR>
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThreads, kCols <= 2 ? 2 : 1)
     extern __shared__ __align__(16) float smem[];
     float* qs = smem;
     float* ring = qs + kRows * kD;
-    float* ps = ring + kStages<kCols> * 2 * kKeys * kD;
+    float* ps = ring + kStages * 2 * kKeys * kD;
     float2* stat = reinterpret_cast<float2*>(ps + kRows * kKeys);
     const PagedArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, kCols <= 2 ? 2 : 1)
     };
     auto issue = [&]() {
         if (issued < s1) {
-            float* k = ring + (issued - s0) % kStages<kCols> * (2 * kKeys * kD);
+            float* k = ring + (issued - s0) % kStages * (2 * kKeys * kD);
             copy(k, K, off, a.page_elems, kKeysW, true);
             copy(k + kKeys * kD, V, off, a.page_elems, kKeysW, false);
             ++issued;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, kCols <= 2 ? 2 : 1)
              a.q_elems, kMine, false);
     }
 #pragma unroll
-    for (int i = 0; i < kStages<kCols> - 1; ++i) issue();
+    for (int i = 0; i < kStages - 1; ++i) issue();
 
     const int before = min(span.kv - span.n, span.kv);      // keys from before the step
     uint64_t o[kR][kCols][2];
@@ -116,13 +116,13 @@ __global__ void __launch_bounds__(kThreads, kCols <= 2 ? 2 : 1)
     }
 #pragma unroll 1
     for (int n = s0; n < s1; ++n) {
-        cp_async_wait<kStages<kCols> - 2>();
+        cp_async_wait<kStages - 2>();
         __syncthreads();                        // the step is here, and the one before has been read
         issue();
-        const float* ks = ring + (n - s0) % kStages<kCols> * (2 * kKeys * kD);
+        const float* ks = ring + (n - s0) % kStages * (2 * kKeys * kD);
         const float* vs = ks + kKeys * kD;
         uint64_t acc[kR][kPer] = {};
-#pragma unroll 2
+#pragma unroll 8
         for (int c = 0; c < D4; ++c) {
             ulonglong2 q[kR], k[kPer];
 #pragma unroll
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, kCols <= 2 ? 2 : 1)
         }
         __syncthreads();                        // the weights are here
         auto add_values = [&](auto every) {
-#pragma unroll 1
+#pragma unroll 2
             for (int k4 = 0; k4 < kKeys / 4; ++k4) {
                 float w[kR][4];
 #pragma unroll
@@ -244,16 +244,21 @@ int tile_rows(const PagedArgs& a)
     return rows > 16ll * a.n_seqs && most_tiles(a, 16) >= 48 ? 32 : 16;
 }
 
+// The cluster size of a call, or 0 where the other kernels are better: where its tiles are so few
+// that the GPU would be empty (8 heads over 2 of 128 dims: 4 tokens, 2000 keys, 15.5 us and 13.5;
+// 13 tokens, 4000 keys, 34 and 25; 4 sequences of up to 13 tokens and 1500 keys, 22 and 18.6), or a
+// CTA would get too many steps.  Only the table tells beforehand how many keys there may be.
 template <int kCols, int kR>
 int ctas_of(const PagedArgs& a)
 {
+    constexpr int kLeastTiles = kCols == 1 ? 16 : 48, kMostSteps = 32;
     static std::atomic<int> known[5][kMaxDevices];
     const long long tiles = most_tiles(a, kTy * kR);
     const long long keys = static_cast<long long>(a.max_pages) * a.page_size;
-    if (most_tiles(a, 16) < FMIN) return 0;
+    if (most_tiles(a, 16) < kLeastTiles) return 0;
     for (int i = 0; i < 5; ++i) {
         const int ctas = kMostCtas >> i;
-        if (keys > static_cast<long long>(ctas) * kKeys * FST) return 0;
+        if (keys > static_cast<long long>(ctas) * kKeys * kMostSteps) return 0;
         int held = 0;
         if (clusters_held(known[i], paged_tree_f32_kernel<kCols, kR>, kThreads, kSmem<kCols, kR>, ctas, &held) ==
                 cudaSuccess &&

@@ -483,9 +483,13 @@ def tree_masks(c, words, kind, seed=0):
     return seen, torch.cat(rows + [torch.full((pad, words), -1, dtype=torch.int32)])
 
 
-def tree_attend(c, masks, **kw):
+def tree_attend(c, masks, room=0, **kw):
+    """room: keys that the page table has columns for, if more than are used.  Calls of few tiles
+    whose table is short go to kernels of their own."""
     kp, vp = c.device_pages(DEV)
-    r = cea.paged_attn_fwd(c.q.to(DEV), kp, vp, c.table.to(DEV), c.cu.to(DEV), c.kv_lens.to(DEV),
+    table = torch.full((len(c.seqs), max(c.table.shape[1], room // c.page)), -1, dtype=torch.int32)
+    table[:, :c.table.shape[1]] = c.table
+    r = cea.paged_attn_fwd(c.q.to(DEV), kp, vp, table.to(DEV), c.cu.to(DEV), c.kv_lens.to(DEV),
                            masks=masks.to(DEV), **kw)
     assert cea.check_status() == 0
     return r
@@ -493,7 +497,8 @@ def tree_attend(c, masks, **kw):
 
 @pytest.mark.parametrize("name", TREE)
 @pytest.mark.parametrize("kind", ["trees", "any", "none"])
-def test_tree_attention(name, kind):
+@pytest.mark.parametrize("room", [0, 1 << 18], ids=["short", "long"])
+def test_tree_attention(name, kind, room):
     """Slots that hold no key are NaN throughout, table entries behind a sequence's pages -1."""
     seqs, H, K, D, page, dtype, layout, pad, words = TREE[name]
     c = Cache(seqs, H, K, D, page, dtype, layout, pad, seed=len(name))
@@ -501,13 +506,13 @@ def test_tree_attention(name, kind):
     out = torch.full((c.T, H, D), 3.0, dtype=dtype, device=DEV)
     lse = torch.full((c.T, H), 5.0, device=DEV)
     ws = cea.paged_attn_workspace(D, dtype, DEV)
-    tree_attend(c, masks, out=out, lse=lse, workspace=ws)
+    tree_attend(c, masks, room, out=out, lse=lse, workspace=ws)
     assert_attends(out, lse, tree_reference(c, seen), name)
     if pad:                                        # rows behind the last sequence stay
         assert (out[-pad:] == 3).all() and (lse[-pad:] == 5).all()
     wide = torch.zeros(c.T, words + 3, dtype=torch.int32)
     wide[:, 1:1 + words] = masks                   # strided masks: the same bits
-    again, none = tree_attend(c, wide.to(DEV)[:, 1:1 + words], workspace=ws, want_lse=False)
+    again, none = tree_attend(c, wide.to(DEV)[:, 1:1 + words], room, workspace=ws, want_lse=False)
     n = c.T - pad
     assert none is None and torch.equal(again[:n], out[:n])
 
@@ -517,8 +522,9 @@ def test_a_chain_is_the_causal_rule():
                         ([(60, 300 + i) for i in range(8)], BF), ([(3, 100)] * 20, BF)):
         c = Cache(seqs, 8, 2, 128, 16, dtype, seed=8)
         masks = torch.cat([mask_words(torch.ones(n, n).tril().bool(), 2) for n, _ in seqs])
-        out, lse = tree_attend(c, masks)
-        assert_attends(out, lse, c.reference(True))
+        for room in (0, 1 << 18):
+            out, lse = tree_attend(c, masks, room)
+            assert_attends(out, lse, c.reference(True))
 
 
 def test_unseen_keys_that_are_not_finite():
@@ -536,12 +542,13 @@ def test_unseen_keys_that_are_not_finite():
             c.k[c.table[0, at // 16], at % 16] = x
             if dtype == F32:
                 c.v[c.table[0, at // 16], at % 16] = x
-        out, lse = tree_attend(c, masks)
         hit = torch.zeros(c.T, dtype=torch.bool)
         hit[:n] = seen[0][:, n - 1] | seen[0][:, n - 2]
         assert hit.any() and not hit.all()
-        assert out[hit.to(DEV)].isnan().flatten(1).any(1).all()
-        assert_attends(out[~hit.to(DEV)], lse[~hit.to(DEV)], tuple(x[~hit] for x in ref))
+        for room in (0, 1 << 18):
+            out, lse = tree_attend(c, masks, room)
+            assert out[hit.to(DEV)].isnan().flatten(1).any(1).all()
+            assert_attends(out[~hit.to(DEV)], lse[~hit.to(DEV)], tuple(x[~hit] for x in ref))
 
 
 def test_tree_python_refusals():
@@ -795,7 +802,8 @@ def test_index_checked_build(monkeypatch):
                      "fp32", "fp32 rows"):
             seqs, H, K, D, page, dtype, layout, pad, words = TREE[name]
             c = Cache(seqs, H, K, D, page, dtype, layout, pad, seed=1)
-            res += tree_attend(c, tree_masks(c, words, "trees")[1])
+            for room in (0, 1 << 18):
+                res += tree_attend(c, tree_masks(c, words, "trees")[1], room)
             kp, vp = c.device_pages(DEV)
             kept = ints([[0, 2, 3] for _ in seqs])
             res.append(cea.paged_kv_keep(kept, kp, vp, c.table.to(DEV), c.cu.to(DEV), c.kv_lens.to(DEV)))
