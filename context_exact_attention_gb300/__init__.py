@@ -1292,7 +1292,8 @@ def paged_reserve(pool: PagePool, new_lens, lens, page_table, page_size: int, st
     with the rows, lengths, positions and slots (see paged_reserve in ring_attn.h).  parents:
     int32 [rows], for drafted trees: entry i of a sequence's tokens names the one that its
     token i extends (-1: a root); positions then follow the depth, and step.masks, if there,
-    get every row's ancestors.  step.kv_lens may be lens itself.  A step that does not fit
+    get every row's ancestors (without parents all tokens before it).  step.kv_lens may be lens
+    itself.  A step that does not fit
     becomes one without rows, and pool.status says why.  Returns step."""
     cu_new, kv_lens, positions, slots, masks = step
     device = _same_device(new_lens, lens, page_table, pool.state, cu_new, kv_lens, positions, slots,
@@ -1317,12 +1318,14 @@ def paged_reserve(pool: PagePool, new_lens, lens, page_table, page_size: int, st
         at_slots = _index_array(slots, "step.slots", rows, torch.int64)
     if parents is not None:
         at_parents = _index_array(parents, "parents", rows)
-        if masks is not None:
-            words = masks.shape[-1]
-            _index_tensor(masks, "step.masks", 2, (rows, words))
-            if not masks.is_contiguous():
-                raise ValueError("step.masks must be contiguous")
-            at_masks = masks.data_ptr()
+    if masks is not None:
+        words = masks.shape[-1]
+        _index_tensor(masks, "step.masks", 2, (rows, words))
+        if not masks.is_contiguous():
+            raise ValueError("step.masks must be contiguous")
+        at_masks = masks.data_ptr()
+        if at_masks == 0:                       # no rows
+            words = 0
     _call_fast("paged_reserve", pool._c, new_lens.data_ptr(), lens.data_ptr(), table, cols,
                table_step, page_size, rows, cu_new.data_ptr(), kv_lens.data_ptr(), at_positions,
                at_slots, at_parents, at_masks, words, s)

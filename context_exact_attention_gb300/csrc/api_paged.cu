@@ -692,7 +692,7 @@ ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int
     if (st != RA_OK) return st;
     const ull n = static_cast<ull>(pool->n_seqs), t = static_cast<ull>(std::max(T, 0));
     if (!new_lens || !cu_new || !kv_lens || T < 0 || mask_words < 0 || (mask_words > 0) != (masks != nullptr) ||
-        (masks && !parents) || t * static_cast<ull>(mask_words) >= kMaxElems)
+        t * static_cast<ull>(mask_words) >= kMaxElems)
         return RA_ERR_INVALID_ARG;
     if (T > 0x7fffffff - 1024) return RA_ERR_UNSUPPORTED;
     for (const void* p : {static_cast<const void*>(new_lens), static_cast<const void*>(cu_new),

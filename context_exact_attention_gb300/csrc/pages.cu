@@ -201,19 +201,24 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
             pos -= i;
         }
         if (r.slots != nullptr && in_bounds(t, 1, r.T, a.status)) r.slots[t] = slot;
+        auto put = [&](int w, unsigned b) {
+            const long long at = static_cast<long long>(t) * r.mask_words + w;
+            if (in_bounds(at, 1, static_cast<long long>(r.T) * r.mask_words, a.status))
+                r.masks[at] = static_cast<int>(b);
+        };
         if (r.parents == nullptr) {
+            // a chain: every token follows all before it
             if (r.positions != nullptr && in_bounds(t, 1, r.T, a.status)) r.positions[t] = real ? pos + i : 0;
+            for (int w = 0; w < r.mask_words; ++w) {
+                const int bits = real ? i + 1 - 32 * w : 0;
+                put(w, bits <= 0 ? 0u : bits >= 32 ? 0xffffffffu : (1u << bits) - 1);
+            }
             continue;
         }
         // Up the chain of parents: the depth, and a bit for every ancestor.  Parents come
         // before their children (others count as none), so the words are done from the top.
         unsigned bits = 0;
         int word = r.mask_words - 1, depth = -1;
-        auto put = [&](int w, unsigned b) {
-            const long long at = static_cast<long long>(t) * r.mask_words + w;
-            if (in_bounds(at, 1, static_cast<long long>(r.T) * r.mask_words, a.status))
-                r.masks[at] = static_cast<int>(b);
-        };
         for (int node = real ? i : -1; node >= 0;) {
             ++depth;
             const int w = node >> 5;

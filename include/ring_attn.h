@@ -623,7 +623,8 @@ typedef struct {
 /*
  * qk_norm_rope_fwd -- q and k normalised by *norm, rotated (rope NULL: normalised only) and
  * written to q_out and k_out in one launch; layouts, positions, strides, in-place outputs and
- * errors as rope_fwd.  Everything between the input and the one rounding of the result is fp32.
+ * errors as rope_fwd.  Everything between the input and the one rounding of the result is fp32
+ * (the squares' sum too: a head whose squares pass 3e38 counts as infinitely long).
  *
  * qk_norm_rope_bwd -- its gradients.  q, k: the forward's inputs (strides q_stride, k_stride);
  * dq_out, dk_out: the gradients of its outputs, tokens dq_out_stride, dk_out_stride elements
@@ -820,7 +821,7 @@ typedef struct {
  *               naming the token of the same sequence that its token i extends, parents before
  *               children; anything else (-1) is a root, whose depth is 0;
  *   masks       NULL (mask_words 0) or int32 [T, mask_words]: bits of a row's ancestors and its
- *               own, as paged_attn_tree_fwd takes them; needs parents.
+ *               own, as paged_attn_tree_fwd takes them (without parents of all tokens before it).
  * Rows behind the last sequence's get position 0, slot -1 and no bits.  A step that does not fit
  * (too few free pages, more than T rows, a sequence longer than max_pages * page_size or 2^31 - 1)
  * becomes one without rows: cu_new all 0, kv_lens = lens, nothing taken, and state[2] says why.

@@ -104,6 +104,19 @@ def test_positions_without_masks():
     p.reserve([4, 3], [0, 0], 8, parents=[-1, 0, 0, 1, -1, -1, 1, 0])
 
 
+def test_chains_without_parents_and_steps_without_rows():
+    """Masks without parents are the causal rule's; a step of no rows writes lengths and starts."""
+    p = Pool(40, 3, 10, 16)
+    step = cea.paged_step(3, 110, 3, DEV)
+    p.reserve([70, 0, 33], [0, 0, 0], 110, step=step)
+    want = [mask_words(torch.ones(n, n).tril().bool(), 3) for n in (70, 33)]
+    assert torch.equal(step.masks.cpu(), torch.cat(want + [torch.zeros(7, 3, dtype=torch.int32)]))
+    none = cea.paged_step(3, 0, 2, DEV)
+    p.reserve([0, 0, 0], [70, 0, 33], 0, step=none)
+    p.reserve([1, 0, 0], [70, 0, 33], 0, step=none)
+    assert int(p.pool.status) == 2 and none.cu_new.tolist() == [0] * 4
+
+
 def test_steps_that_do_not_fit():
     p = Pool(6, 2, 4, 16)
     p.reserve([20, 10], [0, 0], 40)

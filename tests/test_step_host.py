@@ -143,7 +143,7 @@ def test_reserve_refusals(lib):
         assert call(p=pool(**kw)) == code, kw
     for kw in (dict(new=NULL), dict(lens=NULL), dict(table=NULL), dict(cu=NULL), dict(kv=NULL),
                dict(cols=0), dict(stride=9), dict(page=0), dict(T=-1), dict(words=-1), dict(words=0),
-               dict(masks=NULL), dict(parents=NULL), dict(kv=at(3)), dict(cu=at(5)), dict(pos=at(10)),
+               dict(masks=NULL), dict(kv=at(3)), dict(cu=at(5)), dict(pos=at(10)),
                dict(slots=at(11)), dict(masks=at(4)), dict(kv=off(5, 4)), dict(pos=at(9))):
         assert call(**kw) == INVALID, kw
     assert call(T=2 ** 31 - 1, slots=NULL, pos=NULL, parents=NULL, masks=NULL, words=0) == UNSUPPORTED
