@@ -15,7 +15,6 @@ import ctypes
 import os
 import struct
 import threading
-from typing import NamedTuple
 
 import torch
 
@@ -1247,14 +1246,52 @@ def page_pool(num_pages: int, n_seqs: int, device=None) -> PagePool:
     return PagePool(num_pages, n_seqs, dev)
 
 
-class PagedStep(NamedTuple):
-    """What a step knows of its rows (paged_reserve): cu_new, kv_lens as the paged calls take
-    them, positions to rotate by, slots of the keys, masks of a drafted tree (or None)."""
-    cu_new: torch.Tensor
-    kv_lens: torch.Tensor
-    positions: torch.Tensor | None
-    slots: torch.Tensor | None
-    masks: torch.Tensor | None
+def _index_array(t, name, n, dtype=torch.int32):
+    """The address of a contiguous integer tensor of n entries, checked."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape [{n}]")
+    return t.data_ptr()
+
+
+class PagedStep:
+    """What a step knows of its rows, filled by paged_reserve: cu_new [n_seqs + 1] and kv_lens
+    [n_seqs] as the paged calls take them, positions to rotate by [rows], slots of the keys
+    [rows] (int64) and masks of drafted trees [rows, words]; each of the last three may be None,
+    but not all.  Contiguous int32 tensors of one device, checked here and not to be exchanged:
+    _replace makes another PagedStep."""
+
+    __slots__ = ("cu_new", "kv_lens", "positions", "slots", "masks", "_at")
+
+    def __init__(self, cu_new, kv_lens, positions=None, slots=None, masks=None):
+        rows = next((t.shape[0] for t in (positions, slots, masks) if t is not None), None)
+        if rows is None:
+            raise ValueError("a step needs positions, slots or masks, whose size is its rows'")
+        n, words, at_masks = kv_lens.shape[0], 0, 0
+        if masks is not None:
+            words = masks.shape[-1]
+            _index_tensor(masks, "masks", 2, (rows, words))
+            if not masks.is_contiguous():
+                raise ValueError("masks must be contiguous")
+            at_masks = masks.data_ptr()
+        # device, n_seqs, rows, and what paged_reserve passes on
+        at = (cu_new.get_device(), n, rows,
+              (_index_array(cu_new, "cu_new", n + 1), _index_array(kv_lens, "kv_lens", n),
+               _index_array(positions, "positions", rows) if positions is not None else 0,
+               _index_array(slots, "slots", rows, torch.int64) if slots is not None else 0),
+              (at_masks, words if at_masks else 0))
+        if any(t is not None and t.get_device() != at[0] for t in (kv_lens, positions, slots, masks)):
+            raise ValueError("all tensors must be on one device")
+        for name, t in zip(self.__slots__, (cu_new, kv_lens, positions, slots, masks, at)):
+            object.__setattr__(self, name, t)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a PagedStep's tensors are not exchanged: use _replace")
+
+    def __iter__(self):
+        return iter((self.cu_new, self.kv_lens, self.positions, self.slots, self.masks))
+
+    def _replace(self, **tensors):
+        return PagedStep(**{**dict(zip(self.__slots__[:5], self)), **tensors})
 
 
 def paged_step(n_seqs: int, rows: int, mask_words: int = 0, device=None) -> PagedStep:
@@ -1267,13 +1304,6 @@ def paged_step(n_seqs: int, rows: int, mask_words: int = 0, device=None) -> Page
         return torch.zeros(shape, dtype=dtype, device=dev)
     return PagedStep(ints(n_seqs + 1), ints(n_seqs), ints(rows), ints(rows, dtype=torch.int64),
                      ints(rows, mask_words) if mask_words else None)
-
-
-def _index_array(t, name, n, dtype=torch.int32):
-    """The address of a contiguous integer tensor of n entries, checked."""
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape [{n}]")
-    return t.data_ptr()
 
 
 def _pool_args(pool, lens, page_table):
@@ -1295,40 +1325,18 @@ def paged_reserve(pool: PagePool, new_lens, lens, page_table, page_size: int, st
     get every row's ancestors (without parents all tokens before it).  step.kv_lens may be lens
     itself.  A step that does not fit
     becomes one without rows, and pool.status says why.  Returns step."""
-    cu_new, kv_lens, positions, slots, masks = step
-    device = _same_device(new_lens, lens, page_table, pool.state, cu_new, kv_lens, positions, slots,
-                          masks, parents)
+    device = _same_device(new_lens, lens, page_table, pool.state, parents)
     s = _stream_here(device, stream)
     if s is None:
         with _entered(device, stream):
             return paged_reserve(pool, new_lens, lens, page_table, page_size, step, parents)
-    n = pool.n_seqs
     table, cols, table_step = _pool_args(pool, lens, page_table)
-    row_wise = positions if positions is not None else slots if slots is not None else masks
-    if row_wise is None:
-        raise ValueError("step must have positions, slots or masks, whose size is its rows'")
-    rows = row_wise.shape[0]
-    _index_array(new_lens, "new_lens", n)
-    _index_array(cu_new, "step.cu_new", n + 1)
-    _index_array(kv_lens, "step.kv_lens", n)
-    at_positions = at_slots = at_parents = at_masks = words = 0
-    if positions is not None:
-        at_positions = _index_array(positions, "step.positions", rows)
-    if slots is not None:
-        at_slots = _index_array(slots, "step.slots", rows, torch.int64)
-    if parents is not None:
-        at_parents = _index_array(parents, "parents", rows)
-    if masks is not None:
-        words = masks.shape[-1]
-        _index_tensor(masks, "step.masks", 2, (rows, words))
-        if not masks.is_contiguous():
-            raise ValueError("step.masks must be contiguous")
-        at_masks = masks.data_ptr()
-        if at_masks == 0:                       # no rows
-            words = 0
-    _call_fast("paged_reserve", pool._c, new_lens.data_ptr(), lens.data_ptr(), table, cols,
-               table_step, page_size, rows, cu_new.data_ptr(), kv_lens.data_ptr(), at_positions,
-               at_slots, at_parents, at_masks, words, s)
+    step_device, n, rows, at, masks = step._at
+    if step_device != device or n != pool.n_seqs:
+        raise ValueError("step must be on the pool's device, for its sequences")
+    at_parents = _index_array(parents, "parents", rows) if parents is not None else 0
+    _call_fast("paged_reserve", pool._c, _index_array(new_lens, "new_lens", n), lens.data_ptr(),
+               table, cols, table_step, page_size, rows, *at, at_parents, *masks, s)
     return step
 
 

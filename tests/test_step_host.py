@@ -199,6 +199,14 @@ def test_python_refusals():
     assert p.free.tolist() == [3, 2, 1, 0] and int(p.count) == 4 and p.held.tolist() == [0, 0]
     step = cea.paged_step(2, 5, mask_words=3, device="cpu")
     assert step.masks.shape == (5, 3) and step.slots.dtype == torch.int64
+    cu, lens, positions, slots, masks = step
+    assert step._replace(slots=None).slots is None and step._replace(slots=None).masks is masks
+    for kw in (dict(positions=None, slots=None, masks=None), dict(cu_new=lens), dict(slots=positions),
+               dict(positions=positions[:3]), dict(masks=masks[:, :2]), dict(kv_lens=lens.long())):
+        with pytest.raises(ValueError):
+            step._replace(**kw)
+    with pytest.raises(AttributeError):
+        step.masks = masks
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
         cea.paged_reserve(p, i, i, i[None], 16, step)
