@@ -288,11 +288,17 @@ __device__ __forceinline__ Share share_of(const NormArgs& n)
 {
     const long long w = static_cast<long long>(blockIdx.x) * (kFwdThreads / 32) + (threadIdx.x >> 5);
     Share s;
-    s.t = w / n.parts;
-    const int part = static_cast<int>(w - s.t * n.parts);
-    const long long per_token = n.per_token;
-    s.j = static_cast<int>(part * per_token / n.parts);
-    s.rounds = s.t < n.rope.rows ? static_cast<int>((part + 1) * per_token / n.parts) - s.j : 0;
+    s.t = w;
+    s.j = 0;
+    s.rounds = n.per_token;
+    if (n.parts > 1) {                          // (up to 64, of fewer than 2^25 rounds)
+        const unsigned parts = n.parts, per_token = n.per_token;
+        s.t = w >> 32 ? w / n.parts : static_cast<unsigned>(w) / parts;
+        const unsigned part = static_cast<unsigned>(w - s.t * n.parts);
+        s.j = part * per_token / parts;
+        s.rounds = (part + 1) * per_token / parts - s.j;
+    }
+    if (s.t >= n.rope.rows) s.rounds = 0;
     return s;
 }
 
