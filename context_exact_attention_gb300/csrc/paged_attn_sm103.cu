@@ -41,6 +41,8 @@
 // output's own rounding.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "paged_plan.cuh"
 
 namespace ra {
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ PagedParams p)
 {
     using Lay = Layout<D>;
-    using Walk = PagedWalk<StepTiles, kKeys>;
+    using Walk = PagedWalk<std::conditional_t<kTree, WeighedTiles, StepTiles>, kKeys>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_addr(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
@@ -845,6 +847,20 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
     // to 600 keys, 4 key heads, 17 us and 31 cut; 5 prompts of 757, 19 and 28; at a third more
     // a mixed batch loses 3 %).
     p.whole = two ? 2800 : 0;
+    if (kTree) {
+        // Trees bring tiles of one and of two sub-tiles in one call.  With their outputs, partials
+        // and joins a block of one takes 1.37 us and of two 1.78 at head dim 128, but the CTAs of
+        // the former also start on their blocks together and wait for HBM longer.  Measured, 32
+        // trees of up to 64 tokens over up to 8192 keys, price of one against two: 1 (the other
+        // calls') 108 us, the CTAs ending between 74 and 112; 0.81 102; 0.75 101; 0.69 97; 0.63 98.
+        constexpr int kTwo = 16, kOne = D == 64 ? 8 : 11;
+        p.key_cost = kTwo;
+        p.key_cost_single = kOne;
+        p.tile_cost *= kTwo / 2;        // (units of half a key so far)
+        p.min_chunk *= kTwo / 2;
+        p.join_cost *= kTwo / 2;
+        p.whole *= kTwo / 2;
+    }
     const PagedWorkspace w = paged_workspace_of(p.grid, 2 * kSub, D);
     uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
     p.counters = reinterpret_cast<unsigned int*>(ws);

@@ -40,6 +40,7 @@ struct PagedParams {
     int tile_cost;          // a tile's fixed cost (its queries and output)
     int key_shift;          // log2 of a key's cost
     int key_shift_single;   // StepTiles: the same in a tile with one sub-tile of rows
+    int key_cost, key_cost_single;      // WeighedTiles: a key's cost itself
     int tile_tokens;        // new tokens of a tile (StepTiles)
     int page_shift;         // log2 of the page size, or -1
     int box_rows;           // keys of one tensor-map box (tensor-core kernel)
@@ -121,6 +122,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b)
 template <int kRows>
 struct FlatTiles {
     static constexpr bool kLongest = true;
+    __device__ __forceinline__ static long long keys_of(long long cost, int shift) { return cost >> shift; }
     int n_tiles;
     long long cost;         // of one tile
     __device__ __forceinline__ static int rows(const PagedParams&) { return kRows; }
@@ -138,8 +140,20 @@ struct FlatTiles {
 // sees (up to) the keys before the new tokens and the first (j + 1) per of those, so a
 // sequence's costs form an arithmetic series, summed in closed form and searched by halving.
 // Its last tile may have one sub-tile of rows only, whose keys cost less.
-struct StepTiles {
+//
+// kWeighed: keys cost what key_cost and key_cost_single say, not powers of two.
+template <bool kWeighed>
+struct StepTilesOf {
     static constexpr bool kLongest = false;
+    // the cost of keys of weight w, and the keys that a cost pays for
+    __device__ __forceinline__ static long long cost_of(long long keys, int w)
+    {
+        return kWeighed ? keys * w : keys << w;
+    }
+    __device__ __forceinline__ static long long keys_of(long long cost, int w)
+    {
+        return kWeighed ? quotient(cost, w) : cost >> w;
+    }
     int n_tiles, per, fixed, wide, last_shift;
     long long seen, last_keys;      // keys of tile j < n_tiles - 1: seen + j step; of the last
     int step;
@@ -149,20 +163,22 @@ struct StepTiles {
         per = p.tile_tokens;
         n_tiles = (s.n + per - 1) / per;
         fixed = p.tile_cost;
-        wide = p.key_shift;
+        wide = kWeighed ? p.key_cost : p.key_shift;
         const long long before = max(s.kv - s.n, 0);
         step = p.a.causal ? per : 0;
         seen = p.a.causal ? before + per : s.kv;
         last_keys = p.a.causal ? before + s.n : s.kv;
-        last_shift = 2 * (s.n - (n_tiles - 1) * per) <= per ? p.key_shift_single : wide;
+        last_shift = 2 * (s.n - (n_tiles - 1) * per) > per ? wide
+                     : kWeighed                            ? p.key_cost_single
+                                                           : p.key_shift_single;
     }
     __device__ __forceinline__ long long prefix(int j) const
     {
         if (n_tiles == 0) return 0;
         const long long full = j < n_tiles ? j : n_tiles - 1;
         const long long keys = full * seen + step * (full * (full - 1) / 2);
-        const long long c = static_cast<long long>(j) * fixed + (keys << wide);
-        return j < n_tiles ? c : c + (last_keys << last_shift);
+        const long long c = static_cast<long long>(j) * fixed + cost_of(keys, wide);
+        return j < n_tiles ? c : c + cost_of(last_keys, last_shift);
     }
     __device__ __forceinline__ int at(long long x) const
     {
@@ -180,6 +196,9 @@ struct StepTiles {
         return j + 1 < n_tiles ? wide : last_shift;
     }
 };
+
+using StepTiles = StepTilesOf<false>;
+using WeighedTiles = StepTilesOf<true>;
 
 // One CTA's share of one tile.
 struct Segment {
@@ -208,14 +227,14 @@ struct PagedWalk {
         head_cost = tiles.prefix(tiles.n_tiles);
         seq_cost = head_cost * p.a.H_kv;
     }
-    // Keys before the cut at offset x of a tile that has `keys` keys of cost 2^shift: whole
+    // Keys before the cut at offset x of a tile that has `keys` keys of weight `shift`: whole
     // steps of the kernel, and no piece at either end shorter than `snap` keys (a piece costs a
     // partial result and its share of the joining).
     __device__ __forceinline__ static int cut(long long x, int keys, int fixed, int shift, int snap)
     {
         const long long k = x - fixed;
         if (k <= 0) return 0;
-        const long long n = (k >> shift) & -static_cast<long long>(kUnit);
+        const long long n = Tiles::keys_of(k, shift) & -static_cast<long long>(kUnit);
         static_assert((kUnit & (kUnit - 1)) == 0, "cuts at a power of two");
         if (n < snap) return 0;
         return n > keys - snap ? keys : static_cast<int>(n);
@@ -257,7 +276,7 @@ struct PagedWalk {
             const int snap = Tiles::kLongest && b - a <= p.whole
                                  ? t.keys / 2 + 1               // not cut
                                  : static_cast<int>(min(static_cast<long long>(p.snap),
-                                                        chunk >> (shift + 2)));
+                                                        Tiles::keys_of(chunk, shift) >> 2));
             // The CTAs that touch the tile, without the first and the last of them where their
             // piece has no keys; the first keeps a tile without keys.  Others can have none
             // too (a part inside the fixed cost, and with FlatTiles the parts behind the last
