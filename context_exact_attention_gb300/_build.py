@@ -24,7 +24,7 @@ SOURCES = ["api.cu", "attn_bf16_sm103.cu", "attn_bwd_sm103.cu", "attn_f32.cu", "
            "ulysses.cu", "host_pipeline.cu", "bwd_noalloc.cu", "varlen_schedule.cu", "api_paged.cu",
            "rope.cu", "paged_attn_simt.cu", "paged_attn_simt_rows.cu", "paged_attn_bf16.cu",
            "paged_attn_sm103.cu", "paged_attn_tree.cu", "paged_attn_tree_f32.cu",
-           "pages.cu", "qk_norm.cu"]
+           "pages.cu", "qk_norm.cu", "qk_norm_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

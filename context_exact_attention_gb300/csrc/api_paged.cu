@@ -578,7 +578,7 @@ ra_status paged_kv_append_ex(const ra_paged_desc* d, const ra_rope* rope, const 
     a.stream = reinterpret_cast<cudaStream_t>(stream);
     st = ra::current_status_word(&a.status);
     if (st != RA_OK) return st;
-    return from_cuda(norm ? ra::launch_norm(args, false) : ra::launch_rope(a));
+    return from_cuda(norm ? ra::launch_norm(args) : ra::launch_rope(a));
 }
 
 unsigned long long paged_attn_workspace_bytes(int D, ra_dtype dtype)
@@ -623,7 +623,7 @@ ra_status qk_norm_rope_fwd(const ra_rope_desc* desc, const ra_rope* rope, const 
                           static_cast<ull>(n.rope.k_out_elems) * n.rope.elem};
     st = norm_args(norm, n.rope.D, outs, bytes, 2, &n);
     if (st == RA_OK) st = ra::current_status_word(&n.rope.status);
-    return st != RA_OK ? st : from_cuda(ra::launch_norm(n, false));
+    return st != RA_OK ? st : from_cuda(ra::launch_norm(n));
 }
 
 ra_status qk_norm_rope_bwd(const ra_rope_desc* desc, const ra_rope* rope, const ra_head_norm* norm,
@@ -679,7 +679,7 @@ ra_status qk_norm_rope_bwd(const ra_rope_desc* desc, const ra_rope* rope, const 
     n.ticket = static_cast<unsigned int*>(workspace);
     n.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
     st = ra::current_status_word(&a.status);
-    return st != RA_OK ? st : from_cuda(ra::launch_norm(n, true));
+    return st != RA_OK ? st : from_cuda(ra::launch_norm_bwd(n));
 }
 
 ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int* lens, int* page_table,

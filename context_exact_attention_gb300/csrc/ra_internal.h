@@ -242,7 +242,8 @@ struct NormArgs {
 constexpr int kNormCtas = 640;     // of the backward
 constexpr int kNormGroup = 16;     // of its blocks, whose sums are added at once
 static_assert(4 * (1 + (kNormCtas + kNormGroup - 1) / kNormGroup) <= 256, "counters before the partial sums");
-cudaError_t launch_norm(const NormArgs& a, bool backward);
+cudaError_t launch_norm(const NormArgs& a);
+cudaError_t launch_norm_bwd(const NormArgs& a);
 
 // The pool of pages (paged_reserve, paged_release).
 struct PoolArgs {

@@ -188,6 +188,19 @@ NORM = {
     "fp32 odd half": (1, 31, 3, 1, 128, 126, "half", "contiguous", F32, F32, 0.0),
     "fp32 256": (1, 20, 2, 2, 256, 256, "interleaved", "packed", F32, BF, 1.0),
     "fp32 256, part": (1, 20, 2, 2, 256, 128, "half", "zigzag", F32, F32, 0.0),
+    "96 dims": (2, 60, 5, 2, 96, 96, "half", "contiguous", BF, BF, 0.0),
+    "96 dims, odd half": (1, 60, 5, 2, 96, 24, "half", "given", BF, F32, 0.0),
+    "64 dims, odd half": (1, 70, 9, 2, 64, 62, "half", "contiguous", BF, BF, 0.0),
+    "72 dims, odd half": (1, 30, 3, 2, 72, 70, "half", "contiguous", BF, BF, 0.0),
+    "interleaved 64": (1, 50, 6, 2, 64, 64, "interleaved", "contiguous", BF, BF, 0.0),
+    "interleaved 80": (1, 50, 6, 2, 80, 78, "interleaved", "given", BF, F32, 0.0),
+    "interleaved 256": (1, 20, 2, 1, 256, 256, "interleaved", "contiguous", BF, BF, 1.0),
+    "interleaved 72": (1, 33, 3, 1, 72, 72, "interleaved", "contiguous", BF, BF, 0.0),
+    "fp32 interleaved 96": (1, 33, 3, 1, 96, 94, "interleaved", "contiguous", F32, F32, 0.0),
+    "24 dims": (1, 90, 3, 2, 24, 24, "half", "contiguous", BF, BF, 0.0),
+    "fp32 80 dims": (1, 40, 4, 2, 80, 40, "half", "contiguous", F32, F32, 0.0),
+    "fp32 96 dims": (1, 40, 4, 2, 96, 96, "half", "given", F32, F32, 1.0),
+    "fp32 256 odd half": (1, 25, 2, 1, 256, 254, "half", "contiguous", F32, F32, 0.0),
     "fp32 4 dims": (1, 600, 2, 1, 4, 2, "half", "contiguous", F32, F32, 0.0),
     "fp32 100 dims": (1, 90, 4, 2, 100, 50, "half", "contiguous", F32, None, 0.0),
     "more tokens than blocks": (1, 6001, 4, 2, 64, 64, "half", "contiguous", BF, BF, 0.0),
@@ -806,7 +819,8 @@ def test_index_checked_build(monkeypatch):
     """Every entry point in the build that checks its indexes: no check fails, and the same bits."""
     def everything():
         res = []
-        for name in ("odd tokens", "packed", "interleaved part", "odd half", "fp32 256, part", "no rotation"):
+        for name in ("odd tokens", "packed", "interleaved part", "odd half", "fp32 256, part", "no rotation",
+                     "96 dims", "72 dims, odd half", "fp32 256 odd half"):
             c = NormCase(name)
             res += cea.qk_norm_rope_fwd(*c.dev("q", "k", "wq", "wk"), **c.kw)
             c.kw["dq"], c.kw["dk"] = torch.zeros_like(c.q, device=DEV), torch.zeros_like(c.k, device=DEV)
