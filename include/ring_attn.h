@@ -797,7 +797,9 @@ ra_status paged_attn_tree_fwd(const ra_paged_desc* desc, const int* masks, int m
  *               calls), and how the last paged_reserve ended: 0, or 1 too few free pages, 2 more
  *               than T new rows, 3 a sequence longer than its row of the table.
  * Filled by the caller once (every page on the stack, the rest zero) and afterwards changed by
- * the calls below, which must not overlap on the GPU.  At most 8192 sequences.
+ * the calls below, which must not overlap on the GPU.  At most 8192 sequences.  The pool counts no
+ * references: a page belongs to the one sequence that holds it, and pages that several sequences
+ * read (a common beginning) are kept out of the pool as long as they do.
  */
 typedef struct {
     int num_pages, n_seqs;

@@ -640,6 +640,78 @@ def test_keep_leaves_bad_pages_alone():
     assert torch.equal(kp, want)
 
 
+# -------------------------------------------------------------------- large and apart --
+
+def test_slots_beyond_32_bits():
+    p = Pool(6000, 2, 2100, 1 << 20)
+    p.reserve([0, 0], [2 ** 31 - 9, 2 ** 31 - 1], 4)          # lengths only: pages for both
+    assert int(p.pool.count) == 6000 - 4096
+    p.reserve([4, 0], [2 ** 31 - 9, 2 ** 31 - 1], 4)
+    p.reserve([9, 0], [2 ** 31 - 9, 0], 12)
+    assert int(p.pool.status) == 3
+
+
+def test_caches_beyond_32_bits():
+    """Pages whose elements pass 2^32: appended to, attended to and kept."""
+    g = torch.Generator().manual_seed(3)
+    page, K, D, H = 16, 8, 128, 16
+    pages = (1 << 32) // (page * K * D) + 8
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 18 GB of device memory")
+    c = Cache([(20, 45)], H, K, D, page, BF, seed=6)
+    kp, vp = (torch.empty(pages, page, K, D, dtype=BF, device=DEV) for _ in "kv")
+    table = torch.tensor([[pages - 3, 1, pages - 1]], dtype=torch.int32, device=DEV)
+    for j in range(3):
+        kp[table[0, j]], vp[table[0, j]] = c.k[c.table[0, j]].to(DEV), c.v[c.table[0, j]].to(DEV)
+    x = torch.randn(20, K, D, generator=g).to(BF).to(DEV)
+    cu, lens = c.cu.to(DEV), c.kv_lens.to(DEV)
+    for j in range(20):                             # the reference's keys: what the append is to store
+        at = 25 + j
+        c.k[c.table[0, at // page], at % page] = x[j].cpu()
+        c.v[c.table[0, at // page], at % page] = x[j].cpu()
+    cea.paged_kv_append(x, x, kp, vp, table, cu, lens, positions=torch.zeros(20, dtype=torch.int32, device=DEV))
+    seen, masks = tree_masks(c, 1, "trees", 2)
+    for room in (3, 4000):                          # (few tiles, and the kernel for many)
+        wide = torch.full((1, room), -1, dtype=torch.int32, device=DEV)
+        wide[:, :3] = table
+        out, lse = cea.paged_attn_fwd(c.q.to(DEV), kp, vp, wide, cu, lens, masks=masks.to(DEV))
+        assert_attends(out, lse, tree_reference(c, seen))
+    cea.paged_kv_keep(ints([[3, 9, 19]]), kp, vp, table, cu, lens)
+    assert cea.check_status() == 0
+    for i, node in enumerate((3, 9, 19)):
+        at = 25 + i
+        assert torch.equal(kp[table[0, at // page], at % page], x[node])
+        assert torch.equal(vp[table[0, at // page], at % page], x[node])
+
+
+def test_on_streams_of_their_own():
+    """Every call on a stream that is not the current one, beside work on the current one."""
+    s = torch.cuda.Stream()
+    c = Cache([(9, 200), (4, 77)], 8, 2, 128, 16, BF, seed=4)
+    seen, masks = tree_masks(c, 1, "trees", 3)
+    kp, vp = c.device_pages(DEV)
+    q, table, cu, lens, m = (t.to(DEV) for t in (c.q, c.table, c.cu, c.kv_lens, masks))
+    pool, step = cea.page_pool(30, 2, DEV), cea.paged_step(2, 13, 1, DEV)
+    own, new = torch.full((2, 13), -1, dtype=torch.int32, device=DEV), ints([9, 4])
+    zero, k2, v2 = ints([0, 0]), kp.clone(), vp.clone()
+    kept, w = ints([[0, 2, -1], [1, 3, -1]]), torch.ones(128, dtype=BF, device=DEV)
+    x = q[:, :2].contiguous()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = cea.paged_attn_fwd(q, kp, vp, table, cu, lens, masks=m, stream=s)
+    cea.paged_reserve(pool, new, zero, own, 16, step, stream=s)
+    cea.paged_release(pool, zero, own, 16, stream=s)
+    cea.paged_kv_append(x, x, k2, v2, table, cu, lens, k_weight=w, stream=s)
+    left = cea.paged_kv_keep(kept, k2, v2, table, cu, lens, stream=s)
+    busy = torch.randn(2000, 2000, device=DEV) @ torch.randn(2000, 2000, device=DEV)
+    s.synchronize()
+    assert busy.isfinite().all() and cea.check_status(s) == 0
+    assert_attends(out, lse, tree_reference(c, seen))
+    assert step.cu_new.tolist() == [0, 9, 13] and int(pool.count) == 30 and left.tolist() == [193, 75]
+    y, tol = norm64(x.cpu(), torch.ones(128, dtype=torch.float64), torch.zeros(13, 0, dtype=torch.float64), "half")
+    at = 200 - 9 + 1                                # node 2 went to place 1 of the first sequence's step
+    assert_within(k2[table[0, at // 16], at % 16], y[2], tol[2])
+
+
 # ---------------------------------------------------------------------- together --
 
 def drafting_step(pool, lens, new, parents, kept, qkv, table, k, v, wq, wk, rope, page, step, ws, out):
