@@ -872,34 +872,24 @@ def _float_code(dtype, name):
 
 def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out, k_out, stream,
                norm=None):
-    """norm: None, or (q_weight, k_weight, eps, weight_offset), and rope may then be None."""
+    """The checks and the call of the function that rotates q into q_out and k into k_out.  norm:
+    (q_weight, k_weight, eps, weight_offset) of qk_norm_rope_fwd, and rope may then be None.
+    With name None no call is made: (packed ra_rope_desc, B, L, D, q_out, k_out)."""
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    device = _same_device(ref, k, rope.phases if rope is not None else None, positions, cu_seqlens,
-                          q_out, k_out, *(norm[:2] if norm is not None else ()))
+    if norm is None and name is not None:
+        device = _same_device(ref, k, rope.phases, positions, cu_seqlens, q_out, k_out)
+    else:
+        device = _same_device(ref, k, rope.phases if rope is not None else None, positions,
+                              cu_seqlens, q_out, k_out, *(norm[:2] if norm is not None else ()))
     s = _stream_here(device, stream)
     if s is None:
         with _entered(device, stream):
             return _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out,
                               k_out, None, norm)
-    d, B, L, D, q_out, k_out = _rope_args(q, k, ref, device, positions, offset, layout, P,
-                                          cu_seqlens, q_out, k_out)
-    if B > 0 and L > 0:
-        r = rope._c if rope is not None else None
-        if norm is None:
-            _call_fast(name, d, r, _addr(q), _addr(k), _addr(q_out), _addr(k_out), s)
-        else:
-            _call_fast(name, d, r, _head_norm(D, *norm), _addr(q), _addr(k), _addr(q_out),
-                       _addr(k_out), s)
-    return q_out, k_out
-
-
-def _rope_args(q, k, ref, device, positions, offset, layout, P, cu_seqlens, q_out, k_out):
-    """The checks of a call that rotates q into q_out and k into k_out (ref: one that is given):
-    (packed ra_rope_desc, B, L, D, q_out, k_out), the outputs allocated if they were None."""
     dtype = ref.dtype
     code = _float_code(dtype, "q and k")
     packed = layout == "packed"
@@ -948,7 +938,15 @@ def _rope_args(q, k, ref, device, positions, offset, layout, P, cu_seqlens, q_ou
         raise ValueError("an output without its input")
     d = _ROPE_DESC.pack(B, L, H, H_kv, D, P, LAYOUTS[layout], _addr(cu_seqlens), n_seqs,
                         _addr(positions), offset, code, qs, ks, qos, kos)
-    return d, B, L, D, q_out, k_out
+    if name is None:
+        return d, B, L, D, q_out, k_out
+    if B > 0 and L > 0:
+        if norm is None:
+            _call_fast(name, d, rope._c, _addr(q), _addr(k), _addr(q_out), _addr(k_out), s)
+        else:
+            _call_fast(name, d, rope._c if rope is not None else None, _head_norm(D, *norm),
+                       _addr(q), _addr(k), _addr(q_out), _addr(k_out), s)
+    return q_out, k_out
 
 
 def rope_fwd(q, k, rope: RopeTable, positions=None, offset: int = 0, layout: str = "contiguous",
@@ -1036,8 +1034,8 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, rope: RopeTable |
             return qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, rope, eps,
                                     weight_offset, positions, offset, layout, P, cu_seqlens, dq,
                                     dk, dq_weight, dk_weight, workspace)
-    d, B, L, D, dq, dk = _rope_args(q, k, ref, device, positions, offset, layout, P, cu_seqlens,
-                                    dq, dk)
+    d, B, L, D, dq, dk = _rope_call(None, q, k, rope, positions, offset, layout, P, cu_seqlens,
+                                    dq, dk, None)
     steps, weights = [], []
     for x, dy, w in ((q, dq_out, dq_weight), (k, dk_out, dk_weight)):
         if x is None:
@@ -1070,13 +1068,12 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, rope: RopeTable |
 def _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, causal, layers=False):
     """Packed ra_paged_desc; of the first layer, if the pages may be [layers, ...]."""
     shape, stride = k_pages.shape, k_pages.stride()
-    if layers and len(shape) == 5 and shape == v_pages.shape and stride == v_pages.stride():
-        shape, stride = shape[1:], stride[1:]
-    elif len(shape) != 4 or shape != v_pages.shape or stride != v_pages.stride():
-        shape = ()
-    if len(shape) != 4 or k_pages.dtype is not v_pages.dtype:
+    if len(shape) != (5 if layers else 4) or shape != v_pages.shape \
+            or k_pages.dtype != v_pages.dtype or stride != v_pages.stride():
         raise ValueError("k_pages and v_pages must be alike: [num_pages, page_size, H_kv, D] "
                          "of one dtype with the same strides")
+    if layers:
+        shape, stride = shape[1:], stride[1:]
     if stride[3] != 1 and shape[3] > 1:
         raise ValueError("the head vectors of the pages must be contiguous")
     code = _float_code(k_pages.dtype, "the pages")
@@ -1107,7 +1104,10 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
     be None for ones) normalise q and k first, as qk_norm_rope_fwd does; normalise=True does so
     without any weights."""
     device = _same_device(k, v, k_pages, v_pages, page_table, cu_new, kv_lens, q, q_out,
-                          rope.phases if rope is not None else None, positions, q_weight, k_weight)
+                          rope.phases if rope is not None else None)
+    more = positions is not None or q_weight is not None or k_weight is not None or normalise
+    if more:
+        _same_device(k, positions, q_weight, k_weight)
     s = _stream_here(device, stream)
     if s is None:
         with _entered(device, stream):
@@ -1135,24 +1135,22 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, cu_new, kv_lens,
     elif q_out is not None:
         raise ValueError("q_out must be shaped and typed like q")
     d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, T, H, 0)
-    norm = None
-    if q_weight is not None or k_weight is not None or normalise:
-        if normalise is False:
-            raise ValueError("weights without a norm")
-        norm = _head_norm(shape[2], q_weight, k_weight, eps, weight_offset)
-    if positions is not None:
-        _index_tensor(positions, "positions", 1, (T,))
-        if not positions.is_contiguous():
-            raise ValueError("positions must be contiguous")
     if T > 0:
+        r = rope._c if rope is not None else None
         args = (_addr(q), qs, k.data_ptr(), _token_stride(k, shape, "k"), v.data_ptr(),
                 _token_stride(v, shape, "v"), _addr(q_out), qos, k_pages.data_ptr(),
                 v_pages.data_ptr(), s)
-        r = rope._c if rope is not None else None
-        if norm is None and positions is None:
+        if not more:
             _call_fast("paged_kv_append", d, r, *args)
-        else:
-            _call_fast("paged_kv_append_ex", d, r, norm, _addr(positions), *args)
+            return q_out
+        norm = None
+        if q_weight is not None or k_weight is not None or normalise:
+            if normalise is False:
+                raise ValueError("weights without a norm")
+            norm = _head_norm(shape[2], q_weight, k_weight, eps, weight_offset)
+        if positions is not None:
+            _index_array(positions, "positions", T)
+        _call_fast("paged_kv_append_ex", d, r, norm, _addr(positions), *args)
     return q_out
 
 
@@ -1177,8 +1175,7 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
     sequence whose bits its mask has, whatever causal says.  Returns (out [T, H, D], lse fp32
     [T, H]); rows behind the last sequence are left as they are (zero in an out allocated
     here)."""
-    device = _same_device(q, k_pages, v_pages, page_table, cu_new, kv_lens, out, lse, workspace,
-                          masks)
+    device = _same_device(q, k_pages, v_pages, page_table, cu_new, kv_lens, out, lse, workspace)
     s = _stream_here(device, stream)
     if s is None:
         with _entered(device, stream):
@@ -1199,6 +1196,7 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
     elif want_lse:
         lse = torch.zeros((T, H), dtype=torch.float32, device=device)
     if masks is not None:
+        _same_device(q, masks)
         words = masks.shape[-1] if masks.dim() == 2 else 0
         _index_tensor(masks, "masks", 2, (T, words))
     if T > 0:
@@ -1365,12 +1363,14 @@ def paged_kv_keep(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens=None
     if s is None:
         with _entered(device, stream):
             return paged_kv_keep(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens)
-    d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, 0, 1, 0, True)
     layers, step = 1, 0
     if k_pages.dim() == 5:
         layers, step = k_pages.shape[0], k_pages.stride(0)
         if layers < 1:
             raise ValueError("k_pages and v_pages must have a layer")
+        d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, 0, 1, 0, True)
+    else:
+        d = _paged_desc(k_pages, v_pages, page_table, cu_new, kv_lens, 0, 1, 0)
     n = kv_lens.shape[0]
     _index_tensor(kept, "kept", 2)
     width = kept.shape[1]
