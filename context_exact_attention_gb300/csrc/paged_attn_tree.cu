@@ -76,7 +76,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tree_kernel(const __grid_co
     TileRows t{};
     SeqSpan span{};
     const int g = cluster_tile<kRows>(p, t, span);
-    if (g < 0) return;                          // (all of a cluster, which has met no barrier)
+    if (g < 0) {                                // (meeting the barriers of join_cluster all the same, so
+        cluster_sync_all();                     // that CTAs wait for none that has left, whatever the
+        cluster_sync_all();                     // lengths held while each of them read them)
+        return;
+    }
     const int steps = (span.kv + kKeys - 1) / kKeys;
     const int s0 = static_cast<int>(static_cast<long long>(steps) * rank / ctas);
     const int s1 = static_cast<int>(static_cast<long long>(steps) * (rank + 1) / ctas);
