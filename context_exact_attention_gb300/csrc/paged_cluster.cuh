@@ -84,8 +84,21 @@ __device__ __forceinline__ void join_cluster(const PagedParams& p, const TileRow
     for (int r0 = rank + ctas * warp * kAbreast; r0 < t.rows; r0 += ctas * n_warps * kAbreast) {
         const int r = r0 + ctas * sub;
         const bool mine = r < t.rows;
+        // (all reads of a batch first: a read of another CTA's shared memory takes some 200 ns)
+        constexpr int kBatch = 8;
         float2 st = make_float2(-INFINITY, 0.f);
         if (mine && c < ctas) st = load_remote2(mapa_shared(stat_s + 8 * r, c));
+        float4 y[kBatch][kVec4];
+        auto read = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (!mine || k0 + k >= ctas) continue;
+#pragma unroll
+                for (int u = 0; u < kVec4; ++u)
+                    y[k][u] = load_remote4(mapa_shared(buf_s + (r * ldo + 4 * (c + kRowLanes * u)) * 4, k0 + k));
+            }
+        };
+        read(0);
         float M = st.x;
 #pragma unroll
         for (int w = kRowLanes / 2; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
@@ -94,18 +107,21 @@ __device__ __forceinline__ void join_cluster(const PagedParams& p, const TileRow
         float4 x[kVec4];
 #pragma unroll
         for (int u = 0; u < kVec4; ++u) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < ctas; ++k) {
-            const float w = __shfl_sync(0xffffffffu, f, sub * kRowLanes + k);
-            L += __shfl_sync(0xffffffffu, fl, sub * kRowLanes + k);
-            if (!mine) continue;
+#pragma unroll 1
+        for (int k0 = 0; k0 < ctas; k0 += kBatch) {
+            if (k0 > 0) read(k0);
 #pragma unroll
-            for (int u = 0; u < kVec4; ++u) {
-                const float4 y = load_remote4(mapa_shared(buf_s + (r * ldo + 4 * (c + kRowLanes * u)) * 4, k));
-                x[u].x = fmaf(w, y.x, x[u].x);
-                x[u].y = fmaf(w, y.y, x[u].y);
-                x[u].z = fmaf(w, y.z, x[u].z);
-                x[u].w = fmaf(w, y.w, x[u].w);
+            for (int k = 0; k < kBatch; ++k) {
+                const float w = __shfl_sync(0xffffffffu, f, sub * kRowLanes + ((k0 + k) & (kMostCtas - 1)));
+                L += __shfl_sync(0xffffffffu, fl, sub * kRowLanes + ((k0 + k) & (kMostCtas - 1)));
+                if (!mine || k0 + k >= ctas) continue;
+#pragma unroll
+                for (int u = 0; u < kVec4; ++u) {
+                    x[u].x = fmaf(w, y[k][u].x, x[u].x);
+                    x[u].y = fmaf(w, y[k][u].y, x[u].y);
+                    x[u].z = fmaf(w, y[k][u].z, x[u].z);
+                    x[u].w = fmaf(w, y[k][u].w, x[u].w);
+                }
             }
         }
 #pragma unroll

@@ -778,7 +778,7 @@ ra_status paged_attn_fwd(const ra_paged_desc* desc, const void* q, long long q_s
  * masks: DEVICE int32 [T, mask_words], rows mask_stride entries apart (0: mask_words); rows that
  * no sequence holds are not read.  paged_reserve writes them from the tokens' parents.
  * Everything else as paged_attn_fwd, the workspace too.  Calls of few rows and heads whose page
- * table is short (16384 keys a sequence at most, 512 with many sequences) run on kernels of their
+ * table is short (for 1024 keys a sequence, for 16384 if tiles are few) run on kernels of their
  * own, which differ in the last bits and in bf16 keep a weight as two parts for up to 16 rows per
  * sequence and key head on average and as one beyond, whatever the pages.  A value that is not
  * finite, of a new token of a call with several new tokens per sequence, may in bf16 reach rows of
