@@ -874,22 +874,26 @@ def _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out
                norm=None):
     """The checks and the call of the function that rotates q into q_out and k into k_out.  norm:
     (q_weight, k_weight, eps, weight_offset) of qk_norm_rope_fwd, and rope may then be None.
-    With name None no call is made: (packed ra_rope_desc, B, L, D, q_out, k_out)."""
+    With name None no call is made and the caller has checked the devices and entered the stream:
+    (packed ra_rope_desc, B, L, D, q_out, k_out)."""
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    if norm is None and name is not None:
-        device = _same_device(ref, k, rope.phases, positions, cu_seqlens, q_out, k_out)
+    if name is None:
+        device = ref.get_device()
     else:
-        device = _same_device(ref, k, rope.phases if rope is not None else None, positions,
-                              cu_seqlens, q_out, k_out, *(norm[:2] if norm is not None else ()))
-    s = _stream_here(device, stream)
-    if s is None:
-        with _entered(device, stream):
-            return _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens, q_out,
-                              k_out, None, norm)
+        if norm is None:
+            device = _same_device(ref, k, rope.phases, positions, cu_seqlens, q_out, k_out)
+        else:
+            device = _same_device(ref, k, rope.phases if rope is not None else None, positions,
+                                  cu_seqlens, q_out, k_out, norm[0], norm[1])
+        s = _stream_here(device, stream)
+        if s is None:
+            with _entered(device, stream):
+                return _rope_call(name, q, k, rope, positions, offset, layout, P, cu_seqlens,
+                                  q_out, k_out, None, norm)
     dtype = ref.dtype
     code = _float_code(dtype, "q and k")
     packed = layout == "packed"
