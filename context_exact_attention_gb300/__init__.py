@@ -838,6 +838,17 @@ def _index_tensor(t, name, dim, sizes=None):
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
+def _row_stride(t, name):
+    """Elements between the rows of a 2-D index tensor, each with entries of its own."""
+    rows, width = t.shape
+    if rows < 2:
+        return width
+    step = t.stride(0)
+    if step < width:            # broadcast (0, which the library would read as contiguous)
+        raise ValueError(f"{name}: rows must not overlap")
+    return step
+
+
 def _token_stride(t, shape, name):
     """Elements between tokens of [..., H, D] rows whose heads lie side by side (a view of a
     fused projection output is one such); shape is t's."""
@@ -1213,8 +1224,8 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
         if masks is None:
             _call_fast("paged_attn_fwd", d, *args)
         else:
-            _call_fast("paged_attn_tree_fwd", d, masks.data_ptr(), words,
-                       masks.stride(0) if T > 1 else words, *args)
+            _call_fast("paged_attn_tree_fwd", d, masks.data_ptr(), words, _row_stride(masks, "masks"),
+                       *args)
     return out, lse
 
 
@@ -1384,8 +1395,8 @@ def paged_kv_keep(kept, k_pages, v_pages, page_table, cu_new, kv_lens, lens=None
         lens = torch.empty(n, dtype=torch.int32, device=device)
     else:
         _index_array(lens, "lens", n)
-    _call_fast("paged_kv_keep", d, kept.data_ptr(), width, kept.stride(0) if n > 1 else width,
-               layers, step if layers > 1 else 0, k_pages.data_ptr(), v_pages.data_ptr(),
+    _call_fast("paged_kv_keep", d, kept.data_ptr(), width, _row_stride(kept, "kept"), layers,
+               step if layers > 1 else 0, k_pages.data_ptr(), v_pages.data_ptr(),
                lens.data_ptr(), s)
     return lens
 

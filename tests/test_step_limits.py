@@ -1,0 +1,62 @@
+"""What a step of drafted tokens refuses or reports at the edges of what its calls describe, host
+side (no GPU): the library's calls are recorded instead of made."""
+import pytest
+import torch
+
+import context_exact_attention_gb300 as cea
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The calls of the library, (name, arguments), made by the binding on CPU tensors."""
+    made = []
+    monkeypatch.setattr(cea, "_same_device", lambda *tensors: 0)
+    monkeypatch.setattr(cea, "_stream_here", lambda device, stream: 0)
+    monkeypatch.setattr(cea, "_call_fast", lambda name, *args: made.append((name, args)))
+    return made
+
+
+def ints(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def attend(masks, T, n_seqs=3):
+    pages = torch.zeros(8, 16, 1, 64, dtype=torch.bfloat16)
+    q = torch.zeros(T, 2, 64, dtype=torch.bfloat16)
+    cea.paged_attn_fwd(q, pages, pages, ints(n_seqs, 2), ints(n_seqs + 1), ints(n_seqs), masks=masks,
+                       out=torch.empty_like(q), lse=torch.empty(T, 2), workspace=ints(1))
+
+
+def test_masks_of_a_broadcast(calls):
+    """One row for all new tokens, as expand makes it, has no memory for a row each."""
+    for masks in (ints(1, 1).expand(9, 1), ints(1, 4).expand(9, 4), ints(4).expand(9, 4),
+                  ints(12).as_strided((9, 4), (1, 1))):
+        with pytest.raises(ValueError):
+            attend(masks, 9)
+    assert not calls
+    for masks, step in ((ints(9, 4), 4), (ints(9, 7)[:, 2:6], 7), (ints(9, 3)[:, :1], 3), (ints(18, 2)[::2], 4)):
+        attend(masks, 9)
+        assert calls.pop()[1][1:4] == (masks.data_ptr(), masks.shape[1], step)
+    attend(ints(5).expand(1, 5), 1)                 # one row is one row, whatever its stride
+    assert calls.pop()[1][2:4] == (5, 5)
+
+
+def keep(kept):
+    n = kept.shape[0]
+    pages = torch.zeros(8, 16, 1, 64, dtype=torch.bfloat16)
+    cea.paged_kv_keep(kept, pages, pages.clone(), ints(n, 2), ints(n + 1), ints(n),
+                      lens=ints(n))
+
+
+def test_kept_paths_of_a_broadcast(calls):
+    """One path for all sequences, as expand makes it, has no memory for a path each."""
+    for kept in (ints(1, 4).expand(3, 4), ints(4).expand(3, 4), ints(1, 1).expand(3, 1),
+                 ints(8).as_strided((3, 4), (2, 1))):
+        with pytest.raises(ValueError):
+            keep(kept)
+    assert not calls
+    for kept, step in ((ints(3, 4), 4), (ints(3, 9)[:, 1:5], 9), (ints(6, 4)[::2], 8), (ints(3, 5)[:, :1], 5)):
+        keep(kept)
+        assert calls.pop()[1][1:4] == (kept.data_ptr(), kept.shape[1], step)
+    keep(ints(4).expand(1, 4))
+    assert calls.pop()[1][2:4] == (4, 4)
