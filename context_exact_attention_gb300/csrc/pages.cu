@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
     const bool last = last_block(a.state + 1);
     if (gridDim.x == 1) __syncthreads();
 
+    // (64-bit counters: rows and pages may be so many that a step beyond the last passes 2^31)
     const int step = gridDim.x * kThreads, first = blockIdx.x * kThreads + threadIdx.x;
     // the page of entry p of those that this step takes
     auto page_from = [&](int p) {
@@ -174,12 +175,16 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
     };
     for (int g = first; g <= n; g += step)
         if (in_bounds(g, 1, n + 1, a.status)) r.cu_new[g] = g < n ? cu[g] : static_cast<int>(all_rows);
-    for (int p = first; p < all_pages; p += step) {
+    for (long long i = first; i < all_pages; i += step) {
+        const int p = static_cast<int>(i);
         const int g = seq_of(fresh, n, p);
         const long long at = g * a.table_stride + held[g] + (p - fresh[g]);
         if (in_bounds(at, 1, a.table_elems, a.status)) a.page_table[at] = page_from(p);
     }
-    for (int t = first; t < r.T; t += step) {
+    // (no rows to fill in where a program wants the starts, lengths and pages only)
+    const bool fills = r.positions != nullptr || r.slots != nullptr || r.masks != nullptr;
+    for (long long row = first; fills && row < r.T; row += step) {
+        const int t = static_cast<int>(row);
         int pos = 0, i = 0, c = 0;
         long long slot = -1;
         const bool real = t < all_rows;
@@ -301,7 +306,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
     const long long top = available + all - 1;
     const int step = gridDim.x * kThreads;
     const int total = static_cast<int>(min(all, 0x7fffffffll));
-    for (int p = blockIdx.x * kThreads + threadIdx.x; p < total; p += step) {
+    for (long long i = blockIdx.x * kThreads + threadIdx.x; i < total; i += step) {
+        const int p = static_cast<int>(i);
         const int g = seq_of(gone, n, p);
         const long long from = g * a.table_stride + left[g] + (p - gone[g]);
         if (!in_bounds(from, 1, a.table_elems, a.status)) continue;
@@ -347,9 +353,9 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const __grid_constant__ 
     const int n = max(hi - lo, 0);
     const long long first = static_cast<long long>(kv) - n;
     int kept_before = -1, total = 0;        // warp 0's: the last valid entry, how many
-    for (int i0 = 0; i0 < a.width; i0 += kPath) {
+    for (long long i0 = 0; i0 < a.width; i0 += kPath) {
         if (threadIdx.x < 32) {
-            const int i = i0 + lane;
+            const long long i = i0 + lane;
             int node = -1;
             if (i < a.width) node = checked_ldg(a.kept, g * a.kept_stride + i, a.kept_elems, a.status);
             // RA_KEEP_ALL in front: every new token stays where it is
