@@ -1230,30 +1230,52 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
 
 
 KEEP_ALL = -2
+# the library's limits (see paged_reserve in ring_attn.h)
+_POOL_SEQS, _POOL_PAGES = 8192, 2 ** 31 - 1025
 
 
-class PagePool:
+class _Fixed:
+    """An object whose attributes are set once: the library's calls use the addresses of the tensors
+    that it was made with."""
+
+    __slots__ = ()
+
+    def _set(self, **values):
+        for name, value in values.items():
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"the attributes of a {type(self).__name__} are not exchanged "
+                             "(its tensors are filled: copy_)")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+
+class PagePool(_Fixed):
     """Handle of a pool of pages (ra_page_pool), made by page_pool: free, the stack of free pages
     of which the first count are free, held, the pages of every sequence, and status, how the
     last paged_reserve ended (0, or 1 too few pages, 2 too many rows, 3 a sequence too long);
-    int32 tensors on the device.  Calls that share a pool must not overlap on the GPU."""
+    int32 tensors on the device, to be filled (copy_) and not to be exchanged.  Calls that share
+    a pool must not overlap on the GPU."""
+
+    __slots__ = ("num_pages", "n_seqs", "free", "held", "state", "count", "status", "_desc", "_c")
 
     def __init__(self, num_pages: int, n_seqs: int, device):
-        self.num_pages, self.n_seqs = num_pages, n_seqs
-        self.free = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
-        self.held = torch.zeros(n_seqs, dtype=torch.int32, device=device)
-        self.state = torch.zeros(3, dtype=torch.int32, device=device)
-        self.count, self.status = self.state[:1], self.state[2:]
-        self.count.fill_(num_pages)
-        self._desc = PagePoolDesc(num_pages, n_seqs, self.free.data_ptr(), self.held.data_ptr(),
-                                  self.state.data_ptr())
-        self._c = ctypes.byref(self._desc)
+        free = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        held = torch.zeros(n_seqs, dtype=torch.int32, device=device)
+        state = torch.zeros(3, dtype=torch.int32, device=device)
+        state[:1].fill_(num_pages)
+        desc = PagePoolDesc(num_pages, n_seqs, free.data_ptr(), held.data_ptr(), state.data_ptr())
+        self._set(num_pages=num_pages, n_seqs=n_seqs, free=free, held=held, state=state,
+                  count=state[:1], status=state[2:], _desc=desc, _c=ctypes.byref(desc))
 
 
 def page_pool(num_pages: int, n_seqs: int, device=None) -> PagePool:
-    """A PagePool of num_pages pages, all free (page 0 taken first), for n_seqs sequences."""
-    if num_pages < 1 or n_seqs < 1:
-        raise ValueError("num_pages and n_seqs must be positive")
+    """A PagePool of num_pages pages, all free (page 0 taken first), for n_seqs sequences, 8192 at
+    most."""
+    if not 1 <= num_pages <= _POOL_PAGES or not 1 <= n_seqs <= _POOL_SEQS:
+        raise ValueError(f"a pool has 1 to {_POOL_PAGES} pages and 1 to {_POOL_SEQS} sequences")
     dev = torch.device(device) if device is not None else torch.device(
         "cuda", torch.cuda.current_device())
     return PagePool(num_pages, n_seqs, dev)
@@ -1266,7 +1288,7 @@ def _index_array(t, name, n, dtype=torch.int32):
     return t.data_ptr()
 
 
-class PagedStep:
+class PagedStep(_Fixed):
     """What a step knows of its rows, filled by paged_reserve: cu_new [n_seqs + 1] and kv_lens
     [n_seqs] as the paged calls take them, positions to rotate by [rows], slots of the keys
     [rows] (int64) and masks of drafted trees [rows, words]; each of the last three may be None,
@@ -1294,11 +1316,7 @@ class PagedStep:
               (at_masks, words if at_masks else 0))
         if any(t is not None and t.get_device() != at[0] for t in (kv_lens, positions, slots, masks)):
             raise ValueError("all tensors must be on one device")
-        for name, t in zip(self.__slots__, (cu_new, kv_lens, positions, slots, masks, at)):
-            object.__setattr__(self, name, t)
-
-    def __setattr__(self, name, value):
-        raise AttributeError("a PagedStep's tensors are not exchanged: use _replace")
+        self._set(cu_new=cu_new, kv_lens=kv_lens, positions=positions, slots=slots, masks=masks, _at=at)
 
     def __iter__(self):
         return iter((self.cu_new, self.kv_lens, self.positions, self.slots, self.masks))

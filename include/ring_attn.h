@@ -835,8 +835,8 @@ typedef struct {
  * sequence (lens[g] = 0: all it holds) and sets their table entries to -1.  It undoes a
  * paged_reserve: released down to the lengths before it, the stack is what it was.
  * Whatever the arrays hold, no access leaves them.  Errors: RA_ERR_INVALID_ARG (NULL pointers,
- * sizes, arrays that share memory), RA_ERR_UNSUPPORTED (more than 8192 sequences, T above
- * 2^31 - 1025), RA_ERR_MISALIGNED, RA_ERR_CUDA.
+ * sizes, arrays that share memory), RA_ERR_UNSUPPORTED (more than 8192 sequences, T or num_pages
+ * above 2^31 - 1025), RA_ERR_MISALIGNED, RA_ERR_CUDA.
  */
 ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int* lens, int* page_table,
                         int max_pages, long long table_stride, int page_size, int T, int* cu_new,

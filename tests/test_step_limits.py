@@ -60,3 +60,31 @@ def test_kept_paths_of_a_broadcast(calls):
         assert calls.pop()[1][1:4] == (kept.data_ptr(), kept.shape[1], step)
     keep(ints(4).expand(1, 4))
     assert calls.pop()[1][2:4] == (4, 4)
+
+
+def test_a_pool_keeps_its_tensors():
+    """The calls use the addresses that a pool was made with: its tensors are filled, not exchanged."""
+    pool = cea.page_pool(6, 2, device="cpu")
+    for name in ("free", "held", "state", "count", "status", "num_pages", "n_seqs"):
+        with pytest.raises(AttributeError):
+            setattr(pool, name, getattr(pool, name))
+        with pytest.raises(AttributeError):
+            delattr(pool, name)
+    with pytest.raises(AttributeError):
+        pool.other = 1
+    pool.held.copy_(torch.tensor([2, 1]))
+    assert pool.held.tolist() == [2, 1]
+    assert (pool._desc.free_pages, pool._desc.held, pool._desc.state) == (
+        pool.free.data_ptr(), pool.held.data_ptr(), pool.state.data_ptr())
+    step = cea.paged_step(2, 5, device="cpu")
+    with pytest.raises(AttributeError):
+        del step.cu_new
+
+
+def test_pools_that_no_call_takes():
+    """More sequences or pages than the calls know are refused where the pool is made."""
+    cea.page_pool(1, 8192, device="cpu")
+    with pytest.raises(ValueError):
+        cea.page_pool(1, 8193, device="cpu")
+    with pytest.raises(ValueError):
+        cea.page_pool(2 ** 31 - 1024, 1, device="cpu")
