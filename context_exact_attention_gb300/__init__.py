@@ -57,7 +57,7 @@ EXPORTED_SYMBOLS = (
     "ra_rope_phases", "ra_rope_phases_of", "rope_fwd", "rope_bwd", "paged_kv_append",
     "paged_attn_fwd", "paged_attn_workspace_bytes", "qk_norm_workspace_bytes", "qk_norm_rope_fwd",
     "qk_norm_rope_bwd", "paged_kv_append_ex", "paged_attn_tree_fwd", "paged_reserve",
-    "paged_release", "paged_kv_keep",
+    "paged_reserve_ex", "paged_release", "paged_kv_keep",
 )
 
 
@@ -208,6 +208,7 @@ def _open(path, build_if_missing, debug_bounds):
         "paged_kv_append_ex": [vp, vp, vp, vp, vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, vp],
         "paged_attn_tree_fwd": [vp, vp, i, ll, vp, ll, vp, vp, vp, vp, vp, ctypes.c_ulonglong, vp],
         "paged_reserve": [vp, vp, vp, vp, i, ll, i, i, vp, vp, vp, vp, vp, vp, i, vp],
+        "paged_reserve_ex": [vp, vp, vp, vp, i, ll, i, i, vp, vp, vp, vp, vp, vp, i, vp, vp],
         "paged_release": [vp, vp, vp, i, ll, i, vp],
         "paged_kv_keep": [vp, vp, i, ll, i, ll, vp, vp, vp, vp],
     }
@@ -1187,7 +1188,8 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
     with causal=False.  workspace: paged_attn_workspace(D, dtype), kept by the caller (None
     allocates and zeroes one for this call).  masks: int32 [T, words], drafted trees
     (paged_reserve's): row i then sees the keys from before the step and the new tokens of its
-    sequence whose bits its mask has, whatever causal says.  Returns (out [T, H, D], lse fp32
+    sequence whose bits its mask has, whatever causal says; no row sees new tokens behind the first
+    32 * words of a sequence (pool.unmasked counts them).  Returns (out [T, H, D], lse fp32
     [T, H]); rows behind the last sequence are left as they are (zero in an out allocated
     here)."""
     device = _same_device(q, k_pages, v_pages, page_table, cu_new, kv_lens, out, lse, workspace)
@@ -1254,12 +1256,15 @@ class _Fixed:
 
 class PagePool(_Fixed):
     """Handle of a pool of pages (ra_page_pool), made by page_pool: free, the stack of free pages
-    of which the first count are free, held, the pages of every sequence, and status, how the
-    last paged_reserve ended (0, or 1 too few pages, 2 too many rows, 3 a sequence too long);
-    int32 tensors on the device, to be filled (copy_) and not to be exchanged.  Calls that share
-    a pool must not overlap on the GPU."""
+    of which the first count are free, held, the pages of every sequence, status, how the last
+    paged_reserve ended (0, or 1 too few pages, 2 too many rows, 3 a sequence too long), and
+    unmasked, how many of its tokens the step's masks had no bit for (0 unless a sequence brought
+    more than 32 * mask_words: no row sees the tokens behind those, and paged_attn_fwd with these
+    masks is not the trees' attention); int32 tensors on the device, to be filled (copy_) and not
+    to be exchanged.  Calls that share a pool must not overlap on the GPU."""
 
-    __slots__ = ("num_pages", "n_seqs", "free", "held", "state", "count", "status", "_desc", "_c")
+    __slots__ = ("num_pages", "n_seqs", "free", "held", "state", "count", "status", "unmasked",
+                 "_desc", "_c")
 
     def __init__(self, num_pages: int, n_seqs: int, device):
         free = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
@@ -1268,7 +1273,8 @@ class PagePool(_Fixed):
         state[:1].fill_(num_pages)
         desc = PagePoolDesc(num_pages, n_seqs, free.data_ptr(), held.data_ptr(), state.data_ptr())
         self._set(num_pages=num_pages, n_seqs=n_seqs, free=free, held=held, state=state,
-                  count=state[:1], status=state[2:], _desc=desc, _c=ctypes.byref(desc))
+                  count=state[:1], status=state[2:], unmasked=torch.zeros_like(state[:1]),
+                  _desc=desc, _c=ctypes.byref(desc))
 
 
 def page_pool(num_pages: int, n_seqs: int, device=None) -> PagePool:
@@ -1327,7 +1333,8 @@ class PagedStep(_Fixed):
 
 def paged_step(n_seqs: int, rows: int, mask_words: int = 0, device=None) -> PagedStep:
     """Buffers for steps of up to `rows` new tokens, with masks of 32 * mask_words of them per
-    sequence, to be filled by paged_reserve step after step (and replayed in a graph)."""
+    sequence (enough for the longest that a step may bring: a prompt beside trees, too), to be
+    filled by paged_reserve step after step (and replayed in a graph)."""
     dev = torch.device(device) if device is not None else torch.device(
         "cuda", torch.cuda.current_device())
 
@@ -1354,8 +1361,8 @@ def paged_reserve(pool: PagePool, new_lens, lens, page_table, page_size: int, st
     int32 [rows], for drafted trees: entry i of a sequence's tokens names the one that its
     token i extends (-1: a root); positions then follow the depth, and step.masks, if there,
     get every row's ancestors (without parents all tokens before it).  step.kv_lens may be lens
-    itself.  A step that does not fit
-    becomes one without rows, and pool.status says why.  Returns step."""
+    itself.  A step that does not fit becomes one without rows, and pool.status says why; tokens
+    that step.masks have no bit for are counted in pool.unmasked.  Returns step."""
     device = _same_device(new_lens, lens, page_table, pool.state, parents)
     s = _stream_here(device, stream)
     if s is None:
@@ -1366,8 +1373,9 @@ def paged_reserve(pool: PagePool, new_lens, lens, page_table, page_size: int, st
     if step_device != device or n != pool.n_seqs:
         raise ValueError("step must be on the pool's device, for its sequences")
     at_parents = _index_array(parents, "parents", rows) if parents is not None else 0
-    _call_fast("paged_reserve", pool._c, _index_array(new_lens, "new_lens", n), lens.data_ptr(),
-               table, cols, table_step, page_size, rows, *at, at_parents, *masks, s)
+    _call_fast("paged_reserve_ex", pool._c, _index_array(new_lens, "new_lens", n), lens.data_ptr(),
+               table, cols, table_step, page_size, rows, *at, at_parents, *masks,
+               pool.unmasked.data_ptr(), s)
     return step
 
 

@@ -687,6 +687,15 @@ ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int
                         int* kv_lens, int* positions, long long* slots, const int* parents, int* masks,
                         int mask_words, ra_stream_t stream)
 {
+    return paged_reserve_ex(pool, new_lens, lens, page_table, max_pages, table_stride, page_size, T, cu_new,
+                            kv_lens, positions, slots, parents, masks, mask_words, nullptr, stream);
+}
+
+ra_status paged_reserve_ex(const ra_page_pool* pool, const int* new_lens, const int* lens, int* page_table,
+                           int max_pages, long long table_stride, int page_size, int T, int* cu_new,
+                           int* kv_lens, int* positions, long long* slots, const int* parents, int* masks,
+                           int mask_words, int* unmasked, ra_stream_t stream)
+{
     ra::ReserveArgs r{};
     ra_status st = pool_args(pool, lens, page_table, max_pages, table_stride, page_size, &r);
     if (st != RA_OK) return st;
@@ -697,17 +706,18 @@ ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int
     if (T > 0x7fffffff - 1024) return RA_ERR_UNSUPPORTED;
     for (const void* p : {static_cast<const void*>(new_lens), static_cast<const void*>(cu_new),
                           static_cast<const void*>(kv_lens), static_cast<const void*>(positions),
-                          static_cast<const void*>(parents), static_cast<const void*>(masks)})
+                          static_cast<const void*>(parents), static_cast<const void*>(masks),
+                          static_cast<const void*>(unmasked)})
         if (!aligned(p, 4)) return RA_ERR_MISALIGNED;
     if (!aligned(slots, 8)) return RA_ERR_MISALIGNED;
     // what is written, and what is only read; kv_lens may be lens
-    const Span outs[9] = {{cu_new, 4 * n + 4}, {kv_lens, 4 * n}, {positions, positions ? 4 * t : 0},
+    const Span outs[10] = {{cu_new, 4 * n + 4}, {kv_lens, 4 * n}, {positions, positions ? 4 * t : 0},
                           {slots, slots ? 8 * t : 0}, {masks, masks ? 4 * t * mask_words : 0},
                           {page_table, 4ull * r.pool.table_elems}, {pool->held, 4 * n}, {pool->state, 12},
-                          {pool->free_pages, 4ull * pool->num_pages}};
+                          {pool->free_pages, 4ull * pool->num_pages}, {unmasked, unmasked ? 4ull : 0}};
     const Span ins[3] = {{new_lens, 4 * n}, {parents, parents ? 4 * t : 0}, {lens, 4 * n}};
-    for (int i = 0; i < 9; ++i) {
-        for (int j = i + 1; j < 9; ++j)
+    for (int i = 0; i < 10; ++i) {
+        for (int j = i + 1; j < 10; ++j)
             if (overlap(outs[i].base, outs[i].bytes, outs[j].base, outs[j].bytes)) return RA_ERR_INVALID_ARG;
         for (int j = 0; j < 3; ++j)
             if (!(i == 1 && j == 2 && kv_lens == lens) &&
@@ -722,6 +732,7 @@ ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int
     r.slots = slots;
     r.parents = parents;
     r.masks = masks;
+    r.unmasked = unmasked;
     r.T = T;
     r.mask_words = mask_words;
     r.stream = reinterpret_cast<cudaStream_t>(stream);

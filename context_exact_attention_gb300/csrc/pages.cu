@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
     int* fresh = sums + n;                  // pages that the sequences before it take
     int* len = fresh + n;
     int* held = len + n;
-    __shared__ int too_long;
-    if (threadIdx.x == 0) too_long = 0;
+    __shared__ int too_long, unmasked;
+    if (threadIdx.x == 0) too_long = unmasked = 0;
     wait_for_earlier_work();
     const int available = free_count(a);
     __syncthreads();
@@ -244,17 +244,21 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
         if (r.positions != nullptr && in_bounds(t, 1, r.T, a.status)) r.positions[t] = real ? pos + depth : 0;
     }
     if (!last) return;
-    // what others read before
+    // what others read before, and the tokens that masks have no bit for
+    const long long bits = r.mask_words > 0 ? 32ll * r.mask_words : 0x7fffffffll;
     for (int g = threadIdx.x; g < n; g += kThreads) {
         const int end = g + 1 < n ? cu[g + 1] : static_cast<int>(all_rows);
         const int taken = g + 1 < n ? fresh[g + 1] : static_cast<int>(all_pages);
         if (!in_bounds(g, 1, n, a.status)) continue;
         r.kv_lens[g] = len[g] + (end - cu[g]);
+        if (end - cu[g] > bits) atomicAdd(&unmasked, static_cast<int>(end - cu[g] - bits));
         a.held[g] = held[g] + (taken - fresh[g]);
     }
+    __syncthreads();
     if (threadIdx.x == 0) {
         a.state[0] = available - static_cast<int>(all_pages);
         a.state[2] = status;
+        if (r.unmasked != nullptr) *r.unmasked = unmasked;
     }
 }
 

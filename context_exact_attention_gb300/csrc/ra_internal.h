@@ -266,6 +266,7 @@ struct ReserveArgs {
     long long* slots;
     const int* parents;
     int* masks;
+    int* unmasked;                 // or null: new tokens that masks have no bit for
     int T, mask_words;
     cudaStream_t stream;
 };

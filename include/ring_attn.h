@@ -772,8 +772,9 @@ ra_status paged_attn_fwd(const ra_paged_desc* desc, const void* q, long long q_s
  * paged_attn_tree_fwd -- paged_attn_fwd for trees of drafted tokens (or any other mask among a
  * step's new tokens): row i of sequence g sees the kv_lens[g] - n keys before the step, and new
  * token j of its sequence where bit j % 32 of word j / 32 of its mask is set, itself included
- * only if its own bit is.  New tokens beyond 32 * mask_words are seen by no row; causal is not
- * looked at.
+ * only if its own bit is.  New tokens beyond 32 * mask_words are seen by no row, themselves
+ * included: mask_words has to do for the sequence with the most new tokens, a prompt beside the
+ * trees among them (paged_reserve_ex tells).  causal is not looked at.
  *
  * masks: DEVICE int32 [T, mask_words], rows mask_stride entries apart (0: mask_words); rows that
  * no sequence holds are not read.  paged_reserve writes them from the tokens' parents.
@@ -830,6 +831,13 @@ typedef struct {
  * Rows behind the last sequence's get position 0, slot -1 and no bits.  A step that does not fit
  * (too few free pages, more than T rows, a sequence longer than max_pages * page_size or 2^31 - 1)
  * becomes one without rows: cu_new all 0, kv_lens = lens, nothing taken, and state[2] says why.
+ * A sequence may bring more tokens than its masks have bits, 32 * mask_words.  It fits all the same,
+ * but no row sees the tokens behind them (paged_attn_tree_fwd): its attention is then not the
+ * tree's.  paged_reserve_ex counts them.
+ *
+ * paged_reserve_ex -- the same, and *unmasked (DEVICE int32, or NULL) is the number of the step's
+ * tokens that masks have no bit for, over all sequences; 0 if all have one, without masks, and for
+ * a step that does not fit.
  *
  * paged_release -- gives back the pages behind the first ceil(lens[g] / page_size) of every
  * sequence (lens[g] = 0: all it holds) and sets their table entries to -1.  It undoes a
@@ -842,6 +850,10 @@ ra_status paged_reserve(const ra_page_pool* pool, const int* new_lens, const int
                         int max_pages, long long table_stride, int page_size, int T, int* cu_new,
                         int* kv_lens, int* positions, long long* slots, const int* parents, int* masks,
                         int mask_words, ra_stream_t stream);
+ra_status paged_reserve_ex(const ra_page_pool* pool, const int* new_lens, const int* lens, int* page_table,
+                           int max_pages, long long table_stride, int page_size, int T, int* cu_new,
+                           int* kv_lens, int* positions, long long* slots, const int* parents, int* masks,
+                           int mask_words, int* unmasked, ra_stream_t stream);
 ra_status paged_release(const ra_page_pool* pool, const int* lens, int* page_table, int max_pages,
                         long long table_stride, int page_size, ra_stream_t stream);
 
@@ -850,7 +862,8 @@ ra_status paged_release(const ra_page_pool* pool, const int* lens, int* page_tab
  * (desc: cu_new, kv_lens, the cache) the accepted ones, kept[g][0 .. m), ascending indices, move
  * to the front of the step's slots, in all layers at once, and lens[g] = kv_lens[g] - n + m.  A
  * row of kept ends at the first entry that is not above the one before it and below n (-1, say).
- * RA_KEEP_ALL in its first entry keeps every new token where it is (a prompt beside the trees).
+ * RA_KEEP_ALL in its first entry keeps every new token where it is (a prompt beside the trees,
+ * which masks that are wide enough for it let attend to all of itself).
  * Their keys have the right positions already if they turned by depth (paged_kv_append_ex).
  *
  * kept: DEVICE int32 [n_seqs, width], rows kept_stride apart (0: width).  The cache is desc's,

@@ -5,6 +5,8 @@ import pytest
 import torch
 
 import context_exact_attention_gb300 as cea
+from paged_helpers import Cache, assert_attends
+from step_helpers import ancestors, random_parents, tree_reference
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -50,3 +52,67 @@ def test_as_many_rows_and_pages_as_there_may_be():
     # (the three pages that were left lie below them)
     assert torch.equal(pool.free[3:MOST - 5].flip(0), up[5:-3]) and (pool.free[:3] == -1).all()
     assert torch.equal(table[0, :5], up[:5]) and bool((table[0, 5:] == -1).all())
+
+
+# new tokens, lengths before: a prompt beside trees, a token, and a sequence that brings none
+MIXED = [100, 13, 0, 33, 1], [40, 0, 7, 60, 500]
+
+
+def reserved(words, new=MIXED[0], lens=MIXED[1], chain=True, T=None):
+    """A step of prompts (chains) and trees with masks of 32 * words tokens: (step, pool, page table,
+    what new tokens see)."""
+    g = torch.Generator().manual_seed(words)
+    n = len(new)
+    pool, step = cea.page_pool(200, n, DEV), cea.paged_step(n, sum(new) + 3 if T is None else T, words, DEV)
+    table = torch.full((n, 60), -1, dtype=torch.int32, device=DEV)
+    before = cea.paged_step(n, sum(lens), device=DEV)
+    cea.paged_reserve(pool, ints(lens), ints([0] * n), table, 16, before)
+    trees = [list(range(-1, a - 1)) if a > 64 and chain else random_parents(a, g) for a in new]
+    parents = [p for t in trees for p in t]
+    pool.unmasked.fill_(77)
+    cea.paged_reserve(pool, ints(new), ints(lens), table, 16, step,
+                      parents=ints((parents + [-1] * step.positions.shape[0])[:step.positions.shape[0]]))
+    assert cea.check_status() == 0
+    return step, pool, table, [ancestors(t)[0] for t in trees]
+
+
+def test_tokens_that_masks_have_no_bit_for():
+    """Counted wherever a sequence brings more than 32 * words, and only there."""
+    for words, want in ((1, 68 + 1), (2, 36), (3, 4), (4, 0), (0, 0)):
+        step, pool, _, _ = reserved(words)
+        assert int(pool.status) == 0 and pool.unmasked.tolist() == [want], words
+    step, pool, _, _ = reserved(1, T=100)                   # does not fit: no rows
+    assert int(pool.status) == 2 and pool.unmasked.tolist() == [0]
+    # without parents, and many sequences in one call of several blocks
+    pool, step = cea.page_pool(9000, 3000, DEV), cea.paged_step(3000, 90000, 1, DEV)
+    table, zero = torch.full((3000, 3), -1, dtype=torch.int32, device=DEV), ints([0] * 3000)
+    new = torch.arange(3000, device=DEV).remainder(40).int()
+    cea.paged_reserve(pool, new, zero, table, 16, step)
+    assert int(pool.status) == 0 and pool.unmasked.tolist() == [75 * sum(i - 32 for i in range(33, 40))]
+
+
+@pytest.mark.parametrize("dtype,H,K,D", [(torch.bfloat16, 8, 2, 128), (torch.bfloat16, 4, 2, 64),
+                                         (torch.float32, 8, 2, 64)])
+def test_a_prompt_beside_trees(dtype, H, K, D):
+    """Masks wide enough for the prompt: its rows follow the causal rule, the trees' their ancestors."""
+    step, pool, table, seen = reserved(4)
+    assert pool.unmasked.tolist() == [0]
+    seqs = [(a, a + b) for a, b in zip(*MIXED)]
+    c = Cache(seqs, H, K, D, 16, dtype, "slots", pad=3, seed=D)
+    c.table, c.num_pages = table.cpu(), 200
+    used = pool.held.tolist()
+    g = torch.Generator().manual_seed(1)
+    c.k, c.v = (torch.full((200, 16, K, D), float("nan"), dtype=dtype) for _ in "kv")
+    for i, (_, kv) in enumerate(seqs):
+        for j in range(used[i]):
+            n = max(0, min(16, kv - 16 * j))
+            for x in (c.k, c.v):
+                x[c.table[i, j], :n] = torch.randn(n, K, D, generator=g).to(dtype)
+    assert step.cu_new.cpu().tolist() == c.cu.tolist() and step.kv_lens.cpu().tolist() == c.kv_lens.tolist()
+    kp, vp = c.device_pages(DEV)
+    out, lse = cea.paged_attn_fwd(c.q.to(DEV), kp, vp, table, step.cu_new, step.kv_lens, masks=step.masks)
+    assert cea.check_status() == 0
+    assert_attends(out, lse, tree_reference(c, seen))
+    causal = c.reference(True)
+    rows = slice(0, 100)
+    assert_attends(out[rows], lse[rows], tuple(x[rows] for x in causal))

@@ -10,7 +10,7 @@ import context_exact_attention_gb300 as cea
 def calls(monkeypatch):
     """The calls of the library, (name, arguments), made by the binding on CPU tensors."""
     made = []
-    monkeypatch.setattr(cea, "_same_device", lambda *tensors: 0)
+    monkeypatch.setattr(cea, "_same_device", lambda first, *others: first.get_device())
     monkeypatch.setattr(cea, "_stream_here", lambda device, stream: 0)
     monkeypatch.setattr(cea, "_call_fast", lambda name, *args: made.append((name, args)))
     return made
@@ -88,3 +88,25 @@ def test_pools_that_no_call_takes():
         cea.page_pool(1, 8193, device="cpu")
     with pytest.raises(ValueError):
         cea.page_pool(2 ** 31 - 1024, 1, device="cpu")
+
+
+def test_reserve_counts_what_masks_leave_out(calls):
+    """The pool has a place for the number of tokens that masks have no bit for, and the call gets it."""
+    pool, step = cea.page_pool(6, 2, device="cpu"), cea.paged_step(2, 50, mask_words=1, device="cpu")
+    assert pool.unmasked.tolist() == [0]
+    cea.paged_reserve(pool, ints(2), ints(2), ints(2, 3), 16, step)
+    assert calls[0][1][-3:-1] == (1, pool.unmasked.data_ptr())
+
+
+def test_unmasked_refusals():
+    from test_step_host import INVALID, MISALIGNED, NULL, S, at, off, pool
+    lib = cea.load_library()
+
+    def call(unmasked, masks=at(11), words=2):
+        return lib.paged_reserve_ex(pool(), at(3), at(5), at(4), 10, 10, 16, 40, at(6), at(7), at(8), at(9),
+                                    at(10), masks, words, unmasked, S)
+
+    for i in range(12):                     # (2: state, 11: masks, ...; no array holds the number too)
+        assert call(at(i)) == INVALID, i
+    assert call(off(12, 2)) == MISALIGNED
+    assert call(at(12), masks=NULL) == INVALID
