@@ -122,7 +122,9 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) norm_bwd_kernel(const
             }
             const float sum = lanes_sum<kLanes>(both(ss), lanes), product = lanes_sum<kLanes>(both(dot), lanes);
             const float rs = rsqrtf(fmaf(sum, over_D, n.eps));
-            const float c = -(product * rs * over_D);               // - mean(g o u)
+            // - mean(g o u); u = 0 in a head whose squares' sum is infinite, though the sum of
+            // products may be, too
+            const float c = rs == 0.f ? 0.f : -(product * rs * over_D);
             const uint64_t rr = f2pack(rs, rs), cc = f2pack(c, c);
             if (live && j * abreast + sub < heads) {
 #pragma unroll

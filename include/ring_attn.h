@@ -632,7 +632,7 @@ typedef struct {
  * may be written over q, k or dq_out, dk_out (the same rows); dq_weight, dk_weight: fp32 [D],
  * the sums over all rows and heads, or NULL.  With R^T the rotation back, g = w R^T dy,
  * u = x / sqrt(mean(x^2) + eps):  dx = (g - u mean(g u)) / sqrt(mean(x^2) + eps),
- * dw = sum R^T dy u.  Packed rows that no sequence holds are left as they are and add nothing.
+ * dw = sum R^T dy u (a head that counts as infinitely long has u = 0, dx = 0).  Packed rows that no sequence holds are left as they are and add nothing.
  * No atomics on results: repeated calls give the same bits.  workspace: at least
  * qk_norm_workspace_bytes() bytes, 256-byte aligned, ZEROED before its first use; every call
  * leaves it ready for the next, and calls that share one must not overlap on the GPU.

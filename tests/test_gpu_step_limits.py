@@ -116,3 +116,25 @@ def test_a_prompt_beside_trees(dtype, H, K, D):
     causal = c.reference(True)
     rows = slice(0, 100)
     assert_attends(out[rows], lse[rows], tuple(x[rows] for x in causal))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot", [(128, 0), (128, 126), (72, 72), (64, 64)])
+def test_heads_that_count_as_infinitely_long(dtype, D, rot):
+    """A head whose squares pass fp32's range gives zeros, and zero gradients (u = 0, g over infinity),
+    however large the sum of g x is; the heads beside it and the weights' gradients as without it."""
+    g = torch.Generator().manual_seed(D)
+    x, dy = (torch.randn(1, 6, 3, D, generator=g).to(dtype).to(DEV) for _ in "xy")
+    w = torch.randn(D, generator=g).to(dtype).to(DEV)
+    rope = cea.rope_table(rot, device=DEV) if rot else None
+    x[0, 0, 1], dy[0, 0, 1] = 2.0 ** 124, 8.0
+    x[0, 4, 2], dy[0, 4, 2] = -2.0 ** 126, 2.0 ** 20
+    long = torch.zeros(1, 6, 3, dtype=torch.bool)
+    long[0, 0, 1] = long[0, 4, 2] = True
+    y, _ = cea.qk_norm_rope_fwd(x, None, w.abs(), None, rope)
+    dx, _, dw, _ = cea.qk_norm_rope_bwd(x, None, w.abs(), None, dy, None, rope)
+    assert cea.check_status() == 0
+    assert (y[long] == 0).all() and (dx[long] == 0).all()
+    x[long.to(DEV)], dy[long.to(DEV)] = 1.0, 0.0            # heads that add nothing
+    want, _, want_w, _ = cea.qk_norm_rope_bwd(x, None, w.abs(), None, dy, None, rope)
+    assert torch.equal(dx[~long], want[~long]) and torch.equal(dw, want_w)
