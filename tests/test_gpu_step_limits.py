@@ -138,3 +138,30 @@ def test_heads_that_count_as_infinitely_long(dtype, D, rot):
     x[long.to(DEV)], dy[long.to(DEV)] = 1.0, 0.0            # heads that add nothing
     want, _, want_w, _ = cea.qk_norm_rope_bwd(x, None, w.abs(), None, dy, None, rope)
     assert torch.equal(dx[~long], want[~long]) and torch.equal(dw, want_w)
+
+
+@pytest.mark.parametrize("dtype,D,layout", [(torch.bfloat16, 128, "slots"), (torch.bfloat16, 80, "by_head"),
+                                            (torch.float32, 64, "by_slot")])
+@pytest.mark.parametrize("normed", [True, False], ids=["norm", "plain"])
+def test_append_writes_its_slots_and_no_others(dtype, D, layout, normed):
+    """By bits, keys and values alike, in pages that hold something everywhere."""
+    c = Cache([(1, 1), (0, 5), (7, 40), (33, 33), (3, 2)], 4, 2, D, 16, dtype, layout, pad=3, seed=D)
+    g = torch.Generator().manual_seed(D)
+    c.k, c.v = (torch.randn(c.k.shape, generator=g).to(dtype) for _ in "kv")
+    k, v = (torch.randn(c.T, 2, D, generator=g).to(dtype) for _ in "kv")
+    kp, vp = c.device_pages(DEV)
+    more = dict(k_weight=torch.ones(D, dtype=dtype, device=DEV)) if normed else {}
+    cea.paged_kv_append(k.to(DEV), v.to(DEV), kp, vp, c.table.to(DEV), c.cu.to(DEV), c.kv_lens.to(DEV), **more)
+    assert cea.check_status() == 0
+    kp, vp, want_v, mine = kp.cpu(), vp.cpu(), c.v.clone(), torch.zeros(c.k.shape[:2], dtype=torch.bool)
+    for s, (n, kv) in enumerate(c.seqs):
+        for j in range(max(0, n - kv), n):
+            at = kv - n + j
+            page, slot, row = int(c.table[s, at // 16]), at % 16, int(c.cu[s]) + j
+            want_v[page, slot], mine[page, slot] = v[row], True
+            if not normed:
+                c.k[page, slot] = k[row]
+    bits = lambda x: x.contiguous().view(torch.int16 if dtype == torch.bfloat16 else torch.int32)
+    assert torch.equal(bits(vp), bits(want_v))
+    assert torch.equal(bits(kp[~mine]), bits(c.k[~mine]))
+    assert normed or torch.equal(bits(kp), bits(c.k))
