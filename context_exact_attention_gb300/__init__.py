@@ -739,15 +739,34 @@ def ring_attn_bwd_ex(q, k, v, out, lse, dout, P: int = 1, causal: bool = False,
     return dq, dk, dv
 
 
-class RopeTable:
+class _Fixed:
+    """An object whose attributes are set once: the library's calls use the addresses and values
+    that it was made with."""
+
+    __slots__ = ()
+
+    def _set(self, **values):
+        for name, value in values.items():
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"the attributes of a {type(self).__name__} are not exchanged "
+                             "(its tensors are filled: copy_)")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+
+class RopeTable(_Fixed):
     """Handle of a rotation (ra_rope): frequencies as 64-bit fixed-point fractions of a turn
     on the device, the number of rotated dims, the pair style and the amplitude.  Made once
-    per model by rope_table."""
+    per model by rope_table; its attributes are not exchanged."""
+
+    __slots__ = ("phases", "rot_dim", "style", "amplitude", "_c")
 
     def __init__(self, phases, rot_dim: int, style: str, amplitude: float):
-        self.phases, self.rot_dim, self.style = phases, rot_dim, style
-        self.amplitude = amplitude
-        self._c = ctypes.byref(Rope(phases.data_ptr(), rot_dim, ROPE_STYLES[style], amplitude))
+        self._set(phases=phases, rot_dim=rot_dim, style=style, amplitude=amplitude,
+                  _c=ctypes.byref(Rope(phases.data_ptr(), rot_dim, ROPE_STYLES[style], amplitude)))
 
 
 def rope_table(rot_dim: int, base: float = 10000.0, style: str = "half", scaling: str = "none",
@@ -1234,24 +1253,6 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, cu_new, kv_lens, causal: boo
 KEEP_ALL = -2
 # the library's limits (see paged_reserve in ring_attn.h)
 _POOL_SEQS, _POOL_PAGES = 8192, 2 ** 31 - 1025
-
-
-class _Fixed:
-    """An object whose attributes are set once: the library's calls use the addresses of the tensors
-    that it was made with."""
-
-    __slots__ = ()
-
-    def _set(self, **values):
-        for name, value in values.items():
-            object.__setattr__(self, name, value)
-
-    def __setattr__(self, name, value):
-        raise AttributeError(f"the attributes of a {type(self).__name__} are not exchanged "
-                             "(its tensors are filled: copy_)")
-
-    def __delattr__(self, name):
-        self.__setattr__(name, None)
 
 
 class PagePool(_Fixed):

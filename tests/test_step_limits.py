@@ -110,3 +110,12 @@ def test_unmasked_refusals():
         assert call(at(i)) == INVALID, i
     assert call(off(12, 2)) == MISALIGNED
     assert call(at(12), masks=NULL) == INVALID
+
+
+def test_a_rotation_keeps_what_it_was_made_with():
+    """As a pool does: a new amplitude or new frequencies would not reach the calls."""
+    table = cea.rope_table(8, device="cpu")
+    for name in ("phases", "rot_dim", "style", "amplitude"):
+        with pytest.raises(AttributeError):
+            setattr(table, name, getattr(table, name))
+    assert cea.RopeTable(table.phases, 8, "half", 2.0).amplitude == 2.0
