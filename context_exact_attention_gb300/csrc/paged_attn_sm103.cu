@@ -853,6 +853,10 @@ cudaError_t launch_d(PagedParams& p, const CUtensorMap& tq, const CUtensorMap& t
         // the former also start on their blocks together and wait for HBM longer.  Measured, 32
         // trees of up to 64 tokens over up to 8192 keys, price of one against two: 1 (the other
         // calls') 108 us, the CTAs ending between 74 and 112; 0.81 102; 0.75 101; 0.69 97; 0.63 98.
+        // Other batches at 128 dims, price 1, 0.69 and 0.5: 16 trees of up to 16384 keys 106, 91 and
+        // 91 us; 64 of up to 40 tokens and 4096 keys, 16 heads over 4, 70, 62 and 66; 48 of up to 30
+        // over 3000, 65 each.  At 64 dims a half is right: the first batch 86, 71 and 71 us, the
+        // second 79, 65 and 64, the third 58, 51 and 46, the last 49 each.
         constexpr int kTwo = 16, kOne = D == 64 ? 8 : 11;
         p.key_cost = kTwo;
         p.key_cost_single = kOne;

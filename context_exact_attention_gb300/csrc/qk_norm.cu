@@ -21,8 +21,10 @@
 // Measured: 32768 tokens of 32 and 8 heads of 128 in bf16 100 us, 6.7 TB/s, the copy rate; 8192
 // tokens of the same heads appended to pages 37 us, 5.4 TB/s (launch 2, and the positions: rows
 // starts and lengths, then the page, before a token's first store); one decoding step of 64
-// tokens 2.9 us.  16384 tokens of 12 and 4 heads of 96, 64, 80 dims 4.0, 4.7, 3.5 TB/s (their
-// angles serve few heads, and 6 or 5 of 8 lanes work), with odd halves 1.5 to 2.7.
+// tokens 2.9 us.  16384 tokens of 12 and 4 heads of 128, 96, 80, 64 dims 5.4, 4.0, 3.4, 4.7 TB/s
+// (their angles serve few heads, and 6 or 5 of 8 lanes work at 96 and 80), of 112 and 192, known at
+// run time only, 3.6 and 3.8; with halves that are no whole vectors 1.7 to 2.9, at run time 1.3 to
+// 1.9.  In fp32 the 32768 tokens 199 us, 6.7 TB/s, the appended ones 64, 6.3 TB/s.
 #include "qk_norm.cuh"
 
 namespace ra {
