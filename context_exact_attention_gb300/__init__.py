@@ -743,7 +743,7 @@ class _Fixed:
     """An object whose attributes are set once: the library's calls use the addresses and values
     that it was made with."""
 
-    __slots__ = ()
+    __slots__ = ("__weakref__",)
 
     def _set(self, **values):
         for name, value in values.items():
@@ -755,6 +755,9 @@ class _Fixed:
 
     def __delattr__(self, name):
         self.__setattr__(name, None)
+
+    def __copy__(self):                 # (of the same tensors)
+        return self
 
 
 class RopeTable(_Fixed):

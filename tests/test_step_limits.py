@@ -1,5 +1,8 @@
 """What a step of drafted tokens refuses or reports at the edges of what its calls describe, host
 side (no GPU): the library's calls are recorded instead of made."""
+import copy
+import weakref
+
 import pytest
 import torch
 
@@ -119,3 +122,4 @@ def test_a_rotation_keeps_what_it_was_made_with():
         with pytest.raises(AttributeError):
             setattr(table, name, getattr(table, name))
     assert cea.RopeTable(table.phases, 8, "half", 2.0).amplitude == 2.0
+    assert copy.copy(table).phases is table.phases and weakref.ref(table)() is table
